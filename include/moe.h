@@ -535,6 +535,51 @@ int moe_layer_bwd_ring(const moe_desc *d, int32_t mb_tokens, int32_t ring_slots,
                        void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * moe_layer_fwd_few — the layer forward for a few tokens (a decode step), in
+ * two launches: no schedule, no table, no padded rows.  With r = (t, j) a
+ * local slot of token t and e its expert,
+ *     a[r]   = silu(X[t] W13[e][:I]^T) * (X[t] W13[e][I:]^T)
+ *                                       (fp32 accumulate, rounded once to bf16)
+ *     out[t] = bf16( sum_{j asc, local} w[t][j] (a[r] W2[e]^T) + S[t] )
+ * all in fp32 after a (moe_layer_fwd rounds each expert's row to bf16 before
+ * the combine; this call does not, so the two differ by that rounding).
+ * Only the weights of experts that a slot names are read.
+ *   routes int32 [P][Np][K]   w float [P][Np][K]   X bf16 [P][Np][H]
+ *   W13 bf16 [L][2I][H]       W2 bf16 [L][H][I]
+ *   Is, S13, S2  the shared expert ([BPT] section 2.C; S[t] = S2 (silu(gate) *
+ *                up) of every token, its activation rounded to bf16 as above):
+ *                S13 bf16 [2 Is][H] (gate rows, up rows), S2 bf16 [H][Is], Is a
+ *                multiple of 128; Is = 0 and NULLs: no shared expert, S = 0
+ *   out  bf16 [P][Np][H]      zeros for a token with no local slot (plus S)
+ *   ws >= moe_few_workspace_bytes(d, Is), 16-byte aligned; after the call its
+ *        first int32 is the number of route ids outside [0, E)
+ *        (MOE_WS_INVALID_IDS of the other calls)
+ * Needs P*Np*K <= 1024 (else MOE_EUNSUPPORTED: moe_layer_fwd takes those),
+ * H % 256 == 0 and I % 128 == 0, d->num_batches == 1; every pointer 16-byte
+ * aligned.  pad_rows and sched_threads play no part.  A slot may name the same
+ * expert as another slot of its token; both count.  X and w of slots that are
+ * not local are not read into any sum, and a token's output does not depend on
+ * what the other tokens hold.  Repeated calls give bitwise the same outputs.
+ *
+ * moe_layer_fwd_few_mx — the same with MXFP8 routed weights (codes and scale
+ * bytes as moe_quantize_mx writes them: W13q [L][2I][H], W13s [L][2I][H/32],
+ * W2q [L][H][I], W2s [L][H][I/32]; scales 4-byte aligned).  X and a stay bf16:
+ * the weights' read bounds the call and the codes are exact in bf16, so
+ * nothing is gained by quantizing the activations as moe_layer_fwd_mx does.
+ * The shared expert stays bf16 ([MoK] section 5).
+ *
+ * moe_few_workspace_bytes returns -1 for a d or Is that the calls refuse.
+ */
+int64_t moe_few_workspace_bytes(const moe_desc *d, int32_t Is);
+int moe_layer_fwd_few(const moe_desc *d, int32_t Is, const int32_t *routes, const float *w, const uint16_t *X,
+                      const uint16_t *W13, const uint16_t *W2, const uint16_t *S13, const uint16_t *S2, uint16_t *out,
+                      void *ws, size_t ws_bytes, void *stream);
+int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, const float *w, const uint16_t *X,
+                         const uint8_t *W13q, const uint8_t *W13s, const uint8_t *W2q, const uint8_t *W2s,
+                         const uint16_t *S13, const uint16_t *S2, uint16_t *out, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/*
  * Launch trace (optional, host side).  moe_trace_enable(n) records, for the
  * next n kernel launches made by this library on any stream, a start and stop
  * event on the launch's own stream; moe_trace_read copies the finished

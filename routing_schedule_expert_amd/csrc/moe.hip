@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.hpp"
+#include "few.hpp"
 #include "gemm.hpp"
 #include "layer.hpp"
 #include "mxbwd.hpp"
@@ -201,6 +202,18 @@ __global__ __launch_bounds__(kFwdThreads) void k_bwd_gateup(BwdArgs a) {
 __global__ __launch_bounds__(kFwdThreads) void k_wgrad(WgradArgs a, WindowCombine c) {
     __shared__ __attribute__((aligned(16))) char lds[kGemmLds];
     wgrad_phase(a, c, lds);
+}
+
+template <bool MX>
+__global__ __launch_bounds__(kFewThreads, 4) void k_few_gateup(FewArgs a) {
+    extern __shared__ __attribute__((aligned(16))) int32_t few_smem[];
+    few_gateup_body<MX>(a, few_smem);
+}
+
+template <bool MX>
+__global__ __launch_bounds__(kFewThreads, 4) void k_few_down(FewArgs a) {
+    extern __shared__ __attribute__((aligned(16))) int32_t few_smem[];
+    few_down_body<MX>(a, few_smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1531,6 +1544,124 @@ int moe_layer_bwd_ring(const moe_desc *d, int32_t mb_tokens, int32_t ring_slots,
         }
     }
     return MOE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The layer forward for a few tokens.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Rows of the activations (and of the down launch's sums): the routes, then
+// the shared expert's tokens.
+int few_rows(const moe_desc *d, int32_t Is) { return d->P * d->Np * (d->K + (Is > 0 ? 1 : 0)); }
+
+int few_check(const moe_desc *d, int32_t Is) {
+    const int rc = check_desc(d, true);
+    if (rc != MOE_OK) return rc;
+    if (d->num_batches != 1 || Is < 0) return MOE_EINVAL;
+    if ((int64_t)d->P * d->Np * d->K > kFewMaxRoutes) return MOE_EUNSUPPORTED;
+    if (Is % 128 || 768ll * Is >= (1ll << 30)) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+int64_t few_plan_bytes(const moe_desc *d) { return align256(4ll * few_plan_words(d->L, d->P * d->Np * d->K)); }
+int64_t few_ws_bytes(const moe_desc *d, int32_t Is) {
+    return few_plan_bytes(d) + align256(2ll * few_rows(d, Is) * std::max(d->I, Is));
+}
+
+template <bool MX>
+int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s) {
+    a.T = d->P * d->Np;
+    a.K = d->K;
+    a.R = a.T * a.K;
+    a.E = d->E;
+    a.L = d->L;
+    a.base = d->expert_base;
+    a.H = d->H;
+    a.I = d->I;
+    a.Is = Is;
+    a.ld = std::max(d->I, Is);
+    a.plan = static_cast<int32_t *>(ws);
+    a.act = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + few_plan_bytes(d));
+    const int rows = few_rows(d, Is);
+    // parts of the reduction dimension in the down launch: 8 while the sums of
+    // all rows and parts stay within 64 KiB of LDS (two workgroups per CU)
+    a.S = std::max(1, std::min(kFewWaves, 1024 / rows));
+    const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R), lds_down = 4 * (size_t)few_down_words(a.L, a.R, rows, a.S);
+    if (lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
+    const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + Is / kFewRows;
+    {
+        TraceScope tr("few_gateup", s);
+        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, 2ll * device_cus())), dim3(kFewThreads),
+                           lds_gu, s, a);
+    }
+    if (launch_status() != MOE_OK) return MOE_EHIP;
+    TraceScope tr("few_down", s);
+    hipLaunchKernelGGL(k_few_down<MX>, dim3(a.H / kFewRows), dim3(kFewThreads), lds_down, s, a);
+    return launch_status();
+}
+
+// The arguments that both forms share; n_aligned pointers (16 bytes) besides.
+int few_args_check(const moe_desc *d, int32_t Is, const uint16_t *S13, const uint16_t *S2, const void *const *p, int n,
+                   const void *ws, size_t ws_bytes) {
+    const int rc = few_check(d, Is);
+    if (rc != MOE_OK) return rc;
+    for (int i = 0; i < n; ++i)
+        if (!p[i] || !aligned16(p[i])) return MOE_EINVAL;
+    if (Is > 0 ? (!S13 || !S2 || !aligned16(S13) || !aligned16(S2)) : (S13 || S2)) return MOE_EINVAL;
+    if (!ws || !aligned16(ws)) return MOE_EINVAL;
+    return (int64_t)ws_bytes < few_ws_bytes(d, Is) ? MOE_ENOSPC : MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_few_workspace_bytes(const moe_desc *d, int32_t Is) {
+    return few_check(d, Is) == MOE_OK ? few_ws_bytes(d, Is) : -1;
+}
+
+int moe_layer_fwd_few(const moe_desc *d, int32_t Is, const int32_t *routes, const float *w, const uint16_t *X,
+                      const uint16_t *W13, const uint16_t *W2, const uint16_t *S13, const uint16_t *S2, uint16_t *out,
+                      void *ws, size_t ws_bytes, void *stream) {
+    const void *p[] = {routes, w, X, W13, W2, out};
+    const int rc = few_args_check(d, Is, S13, S2, p, 6, ws, ws_bytes);
+    if (rc != MOE_OK) return rc;
+    FewArgs a{};
+    a.routes = routes;
+    a.w = w;
+    a.X = X;
+    a.W13 = W13;
+    a.W2 = W2;
+    a.S13 = S13;
+    a.S2 = S2;
+    a.out = out;
+    return few_launch<false>(d, Is, a, ws, static_cast<hipStream_t>(stream));
+}
+
+int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, const float *w, const uint16_t *X,
+                         const uint8_t *W13q, const uint8_t *W13s, const uint8_t *W2q, const uint8_t *W2s,
+                         const uint16_t *S13, const uint16_t *S2, uint16_t *out, void *ws, size_t ws_bytes,
+                         void *stream) {
+    const void *p[] = {routes, w, X, W13q, W2q, out};
+    int rc = few_args_check(d, Is, S13, S2, p, 6, ws, ws_bytes);
+    if (rc != MOE_OK) return rc;
+    if (!W13s || !W2s || !aligned4(W13s) || !aligned4(W2s)) return MOE_EINVAL;
+    FewArgs a{};
+    a.routes = routes;
+    a.w = w;
+    a.X = X;
+    a.W13 = W13q;
+    a.W2 = W2q;
+    a.W13s = W13s;
+    a.W2s = W2s;
+    a.S13 = S13;
+    a.S2 = S2;
+    a.out = out;
+    return few_launch<true>(d, Is, a, ws, static_cast<hipStream_t>(stream));
 }
 
 int moe_trace_enable(int max_records) {

@@ -36,6 +36,7 @@ EXPORTED = (
     "moe_layer_fwd_mx", "moe_layer_bwd_mx",
     "moe_ring_capacity_rows", "moe_ring_workspace_bytes", "moe_layer_fwd_ring", "moe_layer_bwd_ring",
     "moe_layer_fwd_shared", "moe_layer_fwd_noalloc",
+    "moe_few_workspace_bytes", "moe_layer_fwd_few", "moe_layer_fwd_few_mx",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -92,6 +93,9 @@ def load() -> ctypes.CDLL:
         "moe_ring_workspace_bytes": (i64, [D, i32, i32, ctypes.c_int]),
         "moe_layer_fwd_ring": (ctypes.c_int, [D, i32, i32] + [P] * 14 + [sz, P]),
         "moe_layer_bwd_ring": (ctypes.c_int, [D, i32, i32, i32] + [P] * 15 + [sz, P]),
+        "moe_few_workspace_bytes": (i64, [D, i32]),
+        "moe_layer_fwd_few": (ctypes.c_int, [D, i32] + [P] * 9 + [sz, P]),
+        "moe_layer_fwd_few_mx": (ctypes.c_int, [D, i32] + [P] * 11 + [sz, P]),
         "moe_trace_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_trace_read": (ctypes.c_int, [P, P, ctypes.c_int]),
     }
@@ -122,6 +126,19 @@ def _dev(t):
     if not t.is_contiguous():
         raise ValueError("device buffers must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _buf(name: str, t, dtype, n: int, ref=None):
+    """_dev with the size the call will touch: at least n elements of dtype on
+    ref's device (None stays NULL)."""
+    if t is None:
+        return None
+    p = _dev(t)
+    if t.dtype != dtype or t.numel() < n:
+        raise ValueError(f"{name}: needs {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+    if ref is not None and t.device != ref.device:
+        raise ValueError(f"{name}: on {t.device}, the other buffers on {ref.device}")
+    return p
 
 
 def _stream(stream, ref: torch.Tensor):
@@ -528,3 +545,65 @@ def layer_fwd_shared(d, routes, w, X, W13, W2, W13s, W2s, bufs: FwdBuffers, sh: 
     """Forward with a shared expert; bufs.Xd is not used (fused dispatch)."""
     return moe_layer_fwd_shared(d, sh.Is, routes, w, X, W13, W2, W13s, W2s, bufs.counts, bufs.seg_off, bufs.phi,
                                 bufs.route_row, bufs.HU, bufs.A, bufs.Y, sh.HUs, sh.As, sh.Ys, bufs.out, sh.ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# The layer forward for a few tokens.
+# ---------------------------------------------------------------------------
+
+def few_workspace_bytes(d: moe_desc, Is: int = 0) -> int:
+    n = load().moe_few_workspace_bytes(ctypes.byref(d), Is)
+    if n < 0:
+        raise MoeError(MOE_EINVAL, "moe_few_workspace_bytes")
+    return int(n)
+
+
+def _few_args(d, Is, routes, w, X, S13, S2, out, ws):
+    n, H, i32, f32, bf = d.P * d.Np, d.H, torch.int32, torch.float32, torch.bfloat16
+    return ([_buf("routes", routes, i32, n * d.K, X), _buf("w", w, f32, n * d.K, X), _buf("X", X, bf, n * H)],
+            [_buf("S13", S13, bf, 2 * Is * H, X), _buf("S2", S2, bf, Is * H, X), _buf("out", out, bf, n * H, X),
+             _buf("ws", ws, torch.uint8, 0, X), 0 if ws is None else ws.numel()])
+
+
+def moe_layer_fwd_few(d, Is, routes, w, X, W13, W2, S13, S2, out, ws, stream=None):
+    head, tail = _few_args(d, Is, routes, w, X, S13, S2, out, ws)
+    n, bf = d.L * d.I * d.H, torch.bfloat16
+    with torch.cuda.device(X.device):
+        rc = load().moe_layer_fwd_few(ctypes.byref(d), Is, *head, _buf("W13", W13, bf, 2 * n, X), _buf("W2", W2, bf, n, X),
+                                      *tail, _stream(stream, X))
+    return _check(rc, "moe_layer_fwd_few")
+
+
+def moe_layer_fwd_few_mx(d, Is, routes, w, X, W13q, W13s, W2q, W2s, S13, S2, out, ws, stream=None):
+    head, tail = _few_args(d, Is, routes, w, X, S13, S2, out, ws)
+    n, u8 = d.L * d.I * d.H, torch.uint8
+    with torch.cuda.device(X.device):
+        rc = load().moe_layer_fwd_few_mx(ctypes.byref(d), Is, *head, _buf("W13q", W13q, u8, 2 * n, X),
+                                         _buf("W13s", W13s, u8, 2 * n // 32, X), _buf("W2q", W2q, u8, n, X),
+                                         _buf("W2s", W2s, u8, n // 32, X), *tail, _stream(stream, X))
+    return _check(rc, "moe_layer_fwd_few_mx")
+
+
+@dataclass
+class FewBuffers:
+    Is: int
+    out: torch.Tensor
+    ws: torch.Tensor
+
+
+def alloc_few(d: moe_desc, device, Is: int = 0) -> FewBuffers:
+    """Output and workspace of the few-token forwards (Is: the shared expert's
+    intermediate size, 0 without one)."""
+    return FewBuffers(
+        Is=Is,
+        out=torch.empty((d.P, d.Np, d.H), dtype=torch.bfloat16, device=device),
+        ws=torch.empty(few_workspace_bytes(d, Is), dtype=torch.uint8, device=device),
+    )
+
+
+def layer_fwd_few(d, routes, w, X, W13, W2, bufs: FewBuffers, S13=None, S2=None, stream=None):
+    return moe_layer_fwd_few(d, bufs.Is, routes, w, X, W13, W2, S13, S2, bufs.out, bufs.ws, stream)
+
+
+def layer_fwd_few_mx(d, routes, w, X, W13q, W13s, W2q, W2s, bufs: FewBuffers, S13=None, S2=None, stream=None):
+    return moe_layer_fwd_few_mx(d, bufs.Is, routes, w, X, W13q, W13s, W2q, W2s, S13, S2, bufs.out, bufs.ws, stream)
