@@ -98,6 +98,7 @@ enum {
     MOE_OP_LAYER_BWD = 5,
     MOE_OP_LAYER_FWD_SHARED = 6,
     MOE_OP_LAYER_BWD_MX = 7,
+    MOE_OP_LAYER_BWD_CKPT = 8,
 };
 int64_t moe_workspace_bytes(const moe_desc *d, int op);
 
@@ -578,6 +579,113 @@ int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, c
                          const uint8_t *W13q, const uint8_t *W13s, const uint8_t *W2q, const uint8_t *W2s,
                          const uint16_t *S13, const uint16_t *S2, uint16_t *out, void *ws, size_t ws_bytes,
                          void *stream);
+
+/*
+ * moe_block_norm_fwd — what stands between one block's output and the next
+ * block's input, in one pass: post-norm, gate, residual scale, add, pre-norm.
+ * For every row (token), in fp32:
+ *     p  = y / rms(y) * g_post         (g_post NULL: p = y)
+ *     s  = sigmoid(z)                  (by n->gate: 1, one per row, one per element)
+ *     r' = alpha * r + beta * s * p
+ *     xn = r' / rms(r') * g_pre        (g_pre NULL: not computed)
+ *     rms(v) = sqrt(mean(v^2) + eps)
+ * r' enters the pre-norm before it is rounded; every output is rounded once.
+ *   n      host descriptor: rows (>= 0), H (a multiple of 8, at most 32768),
+ *          gate, res_fp32 (1: r, r_out and their gradients are float, 0: bf16),
+ *          alpha, beta, eps (>= 0)
+ *   y      bf16 [rows][H]   the block's output (moe_layer_fwd's out); NULL: only
+ *                           the pre-norm of r (xn = r / rms(r) * g_pre), then
+ *                           z, g_post and r_out are NULL too
+ *   r      [rows][H]        the residual stream
+ *   z      MOE_GATE_TOKEN: float [rows]; MOE_GATE_ELEM: bf16 [rows][H];
+ *          MOE_GATE_NONE: NULL
+ *   g_post, g_pre  float [H], nullable
+ *   r_out  [rows][H] out    may be r itself
+ *   xn     bf16 [rows][H] out, NULL exactly where g_pre is; may be y itself
+ *   stats  float [rows][2] out: 1 / rms(y), 1 / rms(r') (0 where that norm is
+ *          absent), what the backward needs besides the inputs
+ * Other overlaps of inputs and outputs are not allowed.  Pointers 16-byte
+ * aligned.  A row's outputs depend on that row alone; rows = 0 does nothing
+ * (its buffers may be NULL).
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED for H % 8 or H > 32768.
+ *
+ * moe_block_norm_bwd — its gradient, in one pass and a small column sum.
+ *   y, r, z, g_post, g_pre, stats   as the forward had them
+ *   dr_out [rows][H]        gradient of r' (with y NULL: what else arrives for
+ *                           r), nullable when dxn is given
+ *   dxn    bf16 [rows][H]   gradient of xn, NULL exactly where g_pre is
+ *   dy     bf16 [rows][H] out, NULL exactly where y is; may be y or dxn itself
+ *   dr     [rows][H] out    may be r or dr_out itself
+ *   dz     as z, out, NULL exactly where z is; may be z itself
+ *   dg_post, dg_pre  float [H] out, NULL exactly where g_post / g_pre are; zeros
+ *                           for rows = 0
+ *   ws >= moe_block_norm_workspace_bytes(n) (unused without g_post and g_pre:
+ *         may be NULL then), 16-byte aligned
+ * The column sums have a fixed order, so repeated calls give bitwise the same.
+ */
+enum {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_TOKEN = 1,
+    MOE_GATE_ELEM = 2,
+};
+typedef struct moe_norm_desc {
+    int64_t rows;
+    int32_t H, gate, res_fp32;
+    float alpha, beta, eps;
+} moe_norm_desc;
+int64_t moe_block_norm_workspace_bytes(const moe_norm_desc *n);
+int moe_block_norm_fwd(const moe_norm_desc *n, const uint16_t *y, const void *r, const void *z, const float *g_post,
+                       const float *g_pre, void *r_out, uint16_t *xn, float *stats, void *stream);
+int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r, const void *z, const float *g_post,
+                       const float *g_pre, const float *stats, const void *dr_out, const uint16_t *dxn, uint16_t *dy,
+                       void *dr, void *dz, float *dg_post, float *dg_pre, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Activation checkpoints in 8 bits.  Format: 128 consecutive elements of a row
+ * share one float scale; with amax the largest magnitude of the block,
+ *     scale = amax / 127,   code = rint(x * (127 / amax))   (int8, ties to even)
+ * each operation one IEEE fp32 operation; the value read back is code * scale.
+ * A block with amax < 2^-100 gets scale 0 and codes 0; a block that holds an
+ * infinity or a NaN gets scale NaN and codes 0 (all of it reads back as NaN).
+ *
+ * moe_ckpt_pack — bf16 rows to codes and scales.
+ *   src    bf16 [rows][cols], cols a multiple of 128 (a layer's HU: cols = 2I)
+ *   nrows  device int32, nullable: only rows [0, min(rows, *nrows)) are packed,
+ *          the rest of q and scales is left as it is (a layer's seg_off + L)
+ *   q      int8 [rows][cols] out    scales float [rows][cols / 128] out
+ *
+ * moe_ckpt_swiglu_bwd — the SwiGLU backward of packed rows, for a caller with
+ * its own down dgrad (moe_layer_bwd_ckpt has it in the GEMM's epilogue): with
+ * h, u the values of a row's first and last I codes, d = dA[row], wr = wrow[row]
+ * (1 if wrow is NULL) and s = sigmoid(h), in fp32,
+ *     A = h s u,  dHU = [wr d u s (1 + h (1 - s)), wr d h s],  dw = sum d A
+ *   q, scales   [rows][2I] and [rows][2I / 128] from moe_ckpt_pack
+ *   dA     bf16 [rows][I]   gradient of the activation before the router weight
+ *   wrow   float [rows], nullable     nrows as above
+ *   dHU    bf16 [rows][2I] out        A bf16 [rows][I] out, nullable
+ *   dw     float [rows] out, nullable (from A before its rounding)
+ * Errors of both: MOE_EINVAL (sizes, NULL or misaligned pointers: 16 bytes, the
+ * float and int32 arrays 4 bytes).  rows = 0 does nothing.
+ *
+ * moe_layer_bwd_ckpt — moe_layer_bwd on a checkpoint: q and scales (moe_ckpt_pack
+ * of the forward's HU with cols = 2I and nrows = seg_off + L; q [cap][2I]) take
+ * the place of HU and A, and X (the forward's input) that of Xd: its rows are
+ * pulled again, h and u are decoded in the down dgrad's epilogue, which also
+ * computes a again for the weight gradients.  Per dispatched row 2I (1 + 1/32)
+ * bytes are kept for the backward instead of 6I + 2H.  Other arguments as
+ * moe_layer_bwd; ws >= moe_workspace_bytes(d, MOE_OP_LAYER_BWD_CKPT).  The
+ * gradients are moe_layer_bwd's at the h and u that the codes stand for.
+ * d->num_batches == 1; dOut, X, phi, q, W13, W2, dX, dW13, dW2, ws 16-byte
+ * aligned, the others 4-byte.  Every reduction has a fixed order.
+ */
+int moe_ckpt_pack(const uint16_t *src, int64_t rows, int32_t cols, const int32_t *nrows, int8_t *q, float *scales,
+                  void *stream);
+int moe_ckpt_swiglu_bwd(const int8_t *q, const float *scales, const uint16_t *dA, const float *wrow, int64_t rows,
+                        int32_t I, const int32_t *nrows, uint16_t *dHU, uint16_t *A, float *dw, void *stream);
+int moe_layer_bwd_ckpt(const moe_desc *d, const uint16_t *dOut, const float *w, const uint16_t *X, const moe_src *phi,
+                       const int32_t *route_row, const int32_t *seg_off, const int8_t *q, const float *scales,
+                       const uint16_t *W13, const uint16_t *W2, uint16_t *dX, float *dW13, float *dW2, float *dw, void *ws,
+                       size_t ws_bytes, void *stream);
 
 /*
  * Launch trace (optional, host side).  moe_trace_enable(n) records, for the

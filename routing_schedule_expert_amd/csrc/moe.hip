@@ -6,14 +6,17 @@
 
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
+#include "ckpt.hpp"
 #include "common.hpp"
 #include "few.hpp"
 #include "gemm.hpp"
 #include "layer.hpp"
 #include "mxbwd.hpp"
+#include "norm.hpp"
 #include "rowops.hpp"
 #include "schedule.hpp"
 
@@ -216,6 +219,41 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_few_down(FewArgs a) {
     few_down_body<MX>(a, few_smem);
 }
 
+template <bool F32, int CH>
+__global__ __launch_bounds__(CH <= 1 ? 256 : CH == 2 ? 512 : 1024) void k_norm_fwd(NormArgs a) {
+    __shared__ float lds[2 * 16];
+    norm_fwd_body<F32, CH>(a, lds);
+}
+
+template <bool F32, int CH>
+__global__ __launch_bounds__(CH <= 1 ? 256 : CH == 2 ? 512 : 1024) void k_norm_bwd(NormBwdArgs a) {
+    __shared__ float lds[2 * 2 * 16];
+    norm_bwd_body<F32, CH>(a, lds);
+}
+
+__global__ __launch_bounds__(1024) void k_norm_dg(const float *part, int groups, int H, float *dg_post, float *dg_pre) {
+    __shared__ float lds[1024];
+    norm_dg_body(part, groups, H, dg_post, dg_pre, lds);
+}
+
+__global__ __launch_bounds__(kCkptThreads) void k_ckpt_pack(const uint16_t *src, int64_t rows, int cols,
+                                                            const int32_t *nrows, int8_t *q, float *scales) {
+    ckpt_pack_body(src, rows, cols, nrows, q, scales);
+}
+
+template <int LANES>
+__global__ __launch_bounds__(kCkptThreads) void k_ckpt_swiglu_bwd(const int8_t *q, const float *scales,
+                                                                  const uint16_t *dA, const float *wrow, int64_t rows,
+                                                                  int I, const int32_t *nrows, uint16_t *dHU,
+                                                                  uint16_t *A, float *dw) {
+    ckpt_swiglu_bwd_body<LANES>(q, scales, dA, wrow, rows, I, nrows, dHU, A, dw);
+}
+
+__global__ __launch_bounds__(kFwdThreads) void k_bwd_down_ckpt(CkptBwdArgs a) {
+    __shared__ __attribute__((aligned(16))) char lds[kGemmLds];
+    bwd_down_ckpt_phase(a, lds);
+}
+
 // ---------------------------------------------------------------------------
 // Launch trace.
 // ---------------------------------------------------------------------------
@@ -389,6 +427,12 @@ MxBwdBufs carve_mx_bwd(char *ws, const moe_desc *d) {
     MxBwdBufs m;
     for (int i = 0; i < kMxBufs; ++i) m.b[i] = reinterpret_cast<uint8_t *>(ws + off[i]);
     return m;
+}
+
+// The checkpointed backward's workspace: the bf16 backward's, then the pulled
+// rows of X and the activations computed again (bf16 [cap][H] and [cap][I]).
+int64_t ckpt_bwd_ws_bytes(const moe_desc *d) {
+    return bwd_ws_bytes(d) + align256(cap_rows(d) * d->H * 2) + align256(cap_rows(d) * d->I * 2);
 }
 
 int64_t mx_bwd_ws_bytes(const moe_desc *d) {
@@ -642,7 +686,7 @@ int64_t moe_capacity_rows(const moe_desc *d) {
 int64_t moe_workspace_bytes(const moe_desc *d, int op) {
     const bool ffn = op == MOE_OP_EXPERT_FFN || op == MOE_OP_LAYER_FWD || op == MOE_OP_LAYER_BWD ||
                      op == MOE_OP_DISPATCH || op == MOE_OP_COMBINE || op == MOE_OP_LAYER_FWD_SHARED ||
-                     op == MOE_OP_LAYER_BWD_MX;
+                     op == MOE_OP_LAYER_BWD_MX || op == MOE_OP_LAYER_BWD_CKPT;
     if (check_desc(d, ffn) != MOE_OK) return -1;
     switch (op) {
         case MOE_OP_SCHEDULE: return sched_ws_bytes(d);
@@ -656,6 +700,7 @@ int64_t moe_workspace_bytes(const moe_desc *d, int op) {
         }
         case MOE_OP_LAYER_BWD: return bwd_ws_bytes(d);
         case MOE_OP_LAYER_BWD_MX: return mx_bwd_ws_bytes(d);
+        case MOE_OP_LAYER_BWD_CKPT: return ckpt_bwd_ws_bytes(d);
         case MOE_OP_LAYER_FWD_SHARED: {
             moe_desc one = *d;
             one.num_batches = 1;
@@ -888,13 +933,21 @@ int bwd_gather(const moe_desc *d, int64_t tstride, const uint16_t *dOut, const f
     return launch_status();
 }
 
+struct CkptSource {
+    const int8_t *q;
+    const float *scales;
+    uint16_t *A;
+};
+
 // The data gradients of one table's rows (B1, B2, dw, B3).  d describes the
 // tokens the table covers (a window of tstride tokens per partition when
 // tstride > d->Np: dOut, w, route_row and dw then point at the window's first
-// token).
+// token).  ck: h and u come from a checkpoint's codes instead of HU, and a is
+// computed again into ck->A instead of read from A.
 int bwd_dgrad(const moe_desc *d, int64_t tstride, const uint16_t *dOut, const float *w, const moe_src *phi,
               const int32_t *route_row, const int32_t *seg_off, const uint16_t *HU, const uint16_t *A,
-              const uint16_t *W13, const uint16_t *W2, float *dw, const BwdBufs &bb, hipStream_t s) {
+              const uint16_t *W13, const uint16_t *W2, float *dw, const BwdBufs &bb, hipStream_t s,
+              const CkptSource *ck = nullptr) {
     const int64_t cap = cap_rows(d);
     const bool window = tstride > d->Np;
     BwdArgs a;
@@ -917,8 +970,12 @@ int bwd_dgrad(const moe_desc *d, int64_t tstride, const uint16_t *dOut, const fl
     const int grid = gemm_grid();
     // B2: down-projection dgrad with the SwiGLU backward and dw partials
     {
-        TraceScope tr("bwd_down", s);
-        hipLaunchKernelGGL(k_bwd_down, dim3(grid), dim3(kFwdThreads), 0, s, a);
+        TraceScope tr(ck ? "bwd_down_ckpt" : "bwd_down", s);
+        if (ck)
+            hipLaunchKernelGGL(k_bwd_down_ckpt, dim3(grid), dim3(kFwdThreads), 0, s,
+                               CkptBwdArgs{a, ck->q, ck->scales, ck->A});
+        else
+            hipLaunchKernelGGL(k_bwd_down, dim3(grid), dim3(kFwdThreads), 0, s, a);
     }
     if (launch_status() != MOE_OK) return MOE_EHIP;
     const int64_t nslots = (int64_t)d->P * d->Np * d->K;
@@ -1662,6 +1719,182 @@ int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, c
     a.S2 = S2;
     a.out = out;
     return few_launch<true>(d, Is, a, ws, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Norms before and after a block.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+constexpr int kNormGroups = 512;  // workgroups of the backward at most: each leaves one row of partial sums
+
+int norm_check(const moe_norm_desc *n) {
+    if (!n || n->rows < 0 || n->H < 1 || n->gate < MOE_GATE_NONE || n->gate > MOE_GATE_ELEM || !(n->eps >= 0.0f) ||
+        (n->res_fp32 != 0 && n->res_fp32 != 1))
+        return MOE_EINVAL;
+    if (n->H % 8 || n->H > 8 * kNormMaxChunks * kNormMaxThreads || n->rows > (1ll << 40)) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+int64_t norm_groups(const moe_norm_desc *n) { return std::min<int64_t>(n->rows, kNormGroups); }
+int64_t norm_ws_bytes(const moe_norm_desc *n) { return align256(norm_groups(n) * 2 * n->H * 4); }
+
+// Chunks of 8 elements per thread, and the threads of a row's workgroup.
+int norm_chunks(const moe_norm_desc *n) { return n->H <= 2048 ? 1 : n->H <= 8192 ? 2 : 4; }
+int norm_threads(const moe_norm_desc *n) {
+    const int per = 8 * 64 * norm_chunks(n);
+    return 64 * ((n->H + per - 1) / per);
+}
+
+auto *norm_fwd_kernel(const moe_norm_desc *n) {
+    const int ch = norm_chunks(n);
+    if (n->res_fp32) return ch == 1 ? k_norm_fwd<true, 1> : ch == 2 ? k_norm_fwd<true, 2> : k_norm_fwd<true, 4>;
+    return ch == 1 ? k_norm_fwd<false, 1> : ch == 2 ? k_norm_fwd<false, 2> : k_norm_fwd<false, 4>;
+}
+auto *norm_bwd_kernel(const moe_norm_desc *n) {
+    const int ch = norm_chunks(n);
+    if (n->res_fp32) return ch == 1 ? k_norm_bwd<true, 1> : ch == 2 ? k_norm_bwd<true, 2> : k_norm_bwd<true, 4>;
+    return ch == 1 ? k_norm_bwd<false, 1> : ch == 2 ? k_norm_bwd<false, 2> : k_norm_bwd<false, 4>;
+}
+
+NormArgs norm_args(const moe_norm_desc *n, const uint16_t *y, const void *r, const void *z, const float *g_post,
+                   const float *g_pre, float *stats) {
+    return NormArgs{y, r, z, g_post, g_pre, nullptr, nullptr, stats, n->rows, n->H, n->gate, n->alpha, n->beta, n->eps};
+}
+
+// NULL or 16-byte aligned, each of them.
+bool all_aligned(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (!aligned16(p)) return false;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_block_norm_workspace_bytes(const moe_norm_desc *n) { return norm_check(n) == MOE_OK ? norm_ws_bytes(n) : -1; }
+
+int moe_block_norm_fwd(const moe_norm_desc *n, const uint16_t *y, const void *r, const void *z, const float *g_post,
+                       const float *g_pre, void *r_out, uint16_t *xn, float *stats, void *stream) {
+    const int rc = norm_check(n);
+    if (rc != MOE_OK) return rc;
+    if (n->rows == 0) return MOE_OK;
+    if (!r || !stats || !y != !r_out || !g_pre != !xn || !z != (n->gate == MOE_GATE_NONE)) return MOE_EINVAL;
+    if (!y && (z || g_post || !g_pre)) return MOE_EINVAL;
+    if (!all_aligned({y, r, z, g_post, g_pre, r_out, xn, stats})) return MOE_EINVAL;
+    NormArgs a = norm_args(n, y, r, z, g_post, g_pre, stats);
+    a.r_out = r_out;
+    a.xn = xn;
+    const int threads = norm_threads(n);
+    const int grid = (int)std::min<int64_t>(n->rows, std::max<int64_t>(1, 1024 / threads) * device_cus());
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TraceScope tr("block_norm_fwd", s);
+    auto *fn = norm_fwd_kernel(n);
+    hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), 0, s, a);
+    return launch_status();
+}
+
+int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r, const void *z, const float *g_post,
+                       const float *g_pre, const float *stats, const void *dr_out, const uint16_t *dxn, uint16_t *dy,
+                       void *dr, void *dz, float *dg_post, float *dg_pre, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = norm_check(n);
+    if (rc != MOE_OK) return rc;
+    const bool some = n->rows > 0, sums = g_post || g_pre;
+    if (!g_post != !dg_post || !g_pre != !dg_pre || !all_aligned({g_post, g_pre, dg_post, dg_pre})) return MOE_EINVAL;
+    if (some) {
+        if (!r || !stats || !dr || !y != !dy || !z != !dz || !z != (n->gate == MOE_GATE_NONE) || !g_pre != !dxn ||
+            (!dr_out && !dxn))
+            return MOE_EINVAL;
+        if (!y && (z || g_post || !g_pre)) return MOE_EINVAL;
+        if (!all_aligned({y, r, z, stats, dr_out, dxn, dy, dr, dz, ws})) return MOE_EINVAL;
+    }
+    if (sums && some) {
+        if (!ws) return MOE_EINVAL;
+        if ((int64_t)ws_bytes < norm_ws_bytes(n)) return MOE_ENOSPC;
+    }
+    NormBwdArgs b{norm_args(n, y, r, z, g_post, g_pre, const_cast<float *>(stats)), dr_out, dxn, dy, dr, dz,
+                  static_cast<float *>(ws)};
+    const int threads = norm_threads(n), grid = (int)norm_groups(n);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (some) {
+        TraceScope tr("block_norm_bwd", s);
+        auto *fn = norm_bwd_kernel(n);
+        hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), 0, s, b);
+        if (launch_status() != MOE_OK) return MOE_EHIP;
+    }
+    if (!sums) return MOE_OK;
+    TraceScope tr("block_norm_dg", s);
+    hipLaunchKernelGGL(k_norm_dg, dim3((n->H + 63) / 64, 2), dim3(1024), 0, s, b.part, grid, n->H, dg_post, dg_pre);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Activation checkpoints in 8 bits.
+// ---------------------------------------------------------------------------
+
+int moe_ckpt_pack(const uint16_t *src, int64_t rows, int32_t cols, const int32_t *nrows, int8_t *q, float *scales,
+                  void *stream) {
+    if (rows < 0 || cols < 1 || cols % kCkptBlock || rows > (1ll << 40)) return MOE_EINVAL;
+    if (rows == 0) return MOE_OK;
+    if (!src || !q || !scales || !aligned16(src) || !aligned16(q) || !aligned4(scales) || !aligned4(nrows))
+        return MOE_EINVAL;
+    const int64_t n = rows * (cols / 16);
+    const int grid = (int)std::min<int64_t>((n + kCkptThreads - 1) / kCkptThreads, 8ll * device_cus());
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TraceScope tr("ckpt_pack", s);
+    hipLaunchKernelGGL(k_ckpt_pack, dim3(grid), dim3(kCkptThreads), 0, s, src, rows, cols, nrows, q, scales);
+    return launch_status();
+}
+
+int moe_ckpt_swiglu_bwd(const int8_t *q, const float *scales, const uint16_t *dA, const float *wrow, int64_t rows,
+                        int32_t I, const int32_t *nrows, uint16_t *dHU, uint16_t *A, float *dw, void *stream) {
+    if (rows < 0 || I < 1 || I % kCkptBlock || I > (1 << 30) || rows > (1ll << 40)) return MOE_EINVAL;
+    if (rows == 0) return MOE_OK;
+    if (!q || !scales || !dA || !dHU || !aligned16(q) || !aligned4(scales) || !aligned16(dA) || !aligned4(wrow) ||
+        !aligned4(nrows) || !aligned16(dHU) || !aligned16(A) || !aligned4(dw))
+        return MOE_EINVAL;
+    const int lanes = I >= 1024 ? 64 : I >= 512 ? 32 : I >= 256 ? 16 : 8;
+    const int64_t wgs = (rows * lanes + kCkptThreads - 1) / kCkptThreads;
+    const int grid = (int)std::min<int64_t>(wgs, 8ll * device_cus());
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TraceScope tr("ckpt_swiglu_bwd", s);
+    auto *fn = lanes == 64   ? k_ckpt_swiglu_bwd<64>
+               : lanes == 32 ? k_ckpt_swiglu_bwd<32>
+               : lanes == 16 ? k_ckpt_swiglu_bwd<16>
+                             : k_ckpt_swiglu_bwd<8>;
+    hipLaunchKernelGGL(fn, dim3(grid), dim3(kCkptThreads), 0, s, q, scales, dA, wrow, rows, I, nrows, dHU, A, dw);
+    return launch_status();
+}
+
+int moe_layer_bwd_ckpt(const moe_desc *d, const uint16_t *dOut, const float *w, const uint16_t *X, const moe_src *phi,
+                       const int32_t *route_row, const int32_t *seg_off, const int8_t *q, const float *scales,
+                       const uint16_t *W13, const uint16_t *W2, uint16_t *dX, float *dW13, float *dW2, float *dw, void *ws,
+                       size_t ws_bytes, void *stream) {
+    int rc = check_desc(d, true);
+    if (rc != MOE_OK) return rc;
+    if (d->num_batches != 1) return MOE_EINVAL;
+    const void *a16[] = {dOut, X, phi, q, W13, W2, dX, dW13, dW2, ws};
+    for (const void *p : a16)
+        if (!p || !aligned16(p)) return MOE_EINVAL;
+    const void *a4[] = {w, route_row, seg_off, scales, dw};
+    for (const void *p : a4)
+        if (!p || !aligned4(p)) return MOE_EINVAL;
+    if ((int64_t)ws_bytes < ckpt_bwd_ws_bytes(d)) return MOE_ENOSPC;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *p = static_cast<char *>(ws);
+    const BwdBufs bb = carve_bwd(p, d);
+    uint16_t *Xd = reinterpret_cast<uint16_t *>(p + bwd_ws_bytes(d));
+    const CkptSource ck{q, scales, reinterpret_cast<uint16_t *>(p + bwd_ws_bytes(d) + align256(cap_rows(d) * d->H * 2))};
+    rc = launch_gather(d, X, phi, seg_off, Xd, s, "bwd_gather_x");
+    if (rc != MOE_OK) return rc;
+    rc = bwd_dgrad(d, 0, dOut, w, phi, route_row, seg_off, nullptr, nullptr, W13, W2, dw, bb, s, &ck);
+    if (rc != MOE_OK) return rc;
+    const WgradArgs wa = wgrad_args(d, bb.dOw, ck.A, bb.dHU, Xd, seg_off, dW13, dW2, false);
+    return launch_wgrad(wa, reverse_dispatch(d, 0, bb.dXd, route_row, dX), s);
 }
 
 int moe_trace_enable(int max_records) {

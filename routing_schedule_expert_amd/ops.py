@@ -21,12 +21,14 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED, MOE_EHIP = 0, -1, -2, -3, -4
 (MOE_OP_SCHEDULE, MOE_OP_DISPATCH, MOE_OP_EXPERT_FFN, MOE_OP_COMBINE, MOE_OP_LAYER_FWD, MOE_OP_LAYER_BWD,
- MOE_OP_LAYER_FWD_SHARED, MOE_OP_LAYER_BWD_MX) = range(8)
+ MOE_OP_LAYER_FWD_SHARED, MOE_OP_LAYER_BWD_MX, MOE_OP_LAYER_BWD_CKPT) = range(9)
 MOE_PERSISTENT = 1
 MOE_WS_INVALID_IDS, MOE_WS_BARRIER_STATUS = 0, 1
 (MOE_WS_MX_DHU, MOE_WS_MX_DO_Q, MOE_WS_MX_DO_S, MOE_WS_MX_DHU_Q, MOE_WS_MX_DHU_S, MOE_WS_MX_DOWT_Q, MOE_WS_MX_DOWT_S,
  MOE_WS_MX_AT_Q, MOE_WS_MX_AT_S, MOE_WS_MX_XDT_Q, MOE_WS_MX_XDT_S, MOE_WS_MX_DHUT_Q, MOE_WS_MX_DHUT_S) = range(2, 15)
 MOE_WS_SINGLE_ROUTE = 15
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_ELEM = range(3)
+CKPT_BLOCK = 128
 
 EXPORTED = (
     "moe_strerror", "moe_capacity_rows", "moe_workspace_bytes", "moe_workspace_field", "moe_schedule",
@@ -37,6 +39,8 @@ EXPORTED = (
     "moe_ring_capacity_rows", "moe_ring_workspace_bytes", "moe_layer_fwd_ring", "moe_layer_bwd_ring",
     "moe_layer_fwd_shared", "moe_layer_fwd_noalloc",
     "moe_few_workspace_bytes", "moe_layer_fwd_few", "moe_layer_fwd_few_mx",
+    "moe_block_norm_workspace_bytes", "moe_block_norm_fwd", "moe_block_norm_bwd",
+    "moe_ckpt_pack", "moe_ckpt_swiglu_bwd", "moe_layer_bwd_ckpt",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -50,6 +54,11 @@ class MoeError(RuntimeError):
 class moe_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("P", "Np", "K", "E", "L", "expert_base", "pad_rows", "sched_threads", "H", "I", "num_batches")]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("H", "gate", "res_fp32")] +
+                [(n, ctypes.c_float) for n in ("alpha", "beta", "eps")])
 
 
 def make_desc(P, Np, K, E, L=None, expert_base=0, pad_rows=256, sched_threads=1024, H=0, I=0, num_batches=1):
@@ -70,7 +79,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with routing_schedule_expert_amd/build.py "
                           "(or __graft_entry__.build()); there is no fallback path")
     lib = ctypes.CDLL(LIB_PATH)
-    P, D = ctypes.c_void_p, ctypes.POINTER(moe_desc)
+    P, D, N = ctypes.c_void_p, ctypes.POINTER(moe_desc), ctypes.POINTER(moe_norm_desc)
     i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -96,6 +105,12 @@ def load() -> ctypes.CDLL:
         "moe_few_workspace_bytes": (i64, [D, i32]),
         "moe_layer_fwd_few": (ctypes.c_int, [D, i32] + [P] * 9 + [sz, P]),
         "moe_layer_fwd_few_mx": (ctypes.c_int, [D, i32] + [P] * 11 + [sz, P]),
+        "moe_block_norm_workspace_bytes": (i64, [N]),
+        "moe_block_norm_fwd": (ctypes.c_int, [N] + [P] * 9),
+        "moe_block_norm_bwd": (ctypes.c_int, [N] + [P] * 14 + [sz, P]),
+        "moe_ckpt_pack": (ctypes.c_int, [P, i64, i32, P, P, P, P]),
+        "moe_ckpt_swiglu_bwd": (ctypes.c_int, [P, P, P, P, i64, i32, P, P, P, P, P]),
+        "moe_layer_bwd_ckpt": (ctypes.c_int, [D] + [P] * 15 + [sz, P]),
         "moe_trace_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_trace_read": (ctypes.c_int, [P, P, ctypes.c_int]),
     }
@@ -607,3 +622,129 @@ def layer_fwd_few(d, routes, w, X, W13, W2, bufs: FewBuffers, S13=None, S2=None,
 
 def layer_fwd_few_mx(d, routes, w, X, W13q, W13s, W2q, W2s, bufs: FewBuffers, S13=None, S2=None, stream=None):
     return moe_layer_fwd_few_mx(d, bufs.Is, routes, w, X, W13q, W13s, W2q, W2s, S13, S2, bufs.out, bufs.ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block.
+# ---------------------------------------------------------------------------
+
+def make_norm_desc(rows, H, gate=MOE_GATE_NONE, res_fp32=False, alpha=1.0, beta=1.0, eps=1e-6):
+    return moe_norm_desc(rows, H, gate, int(res_fp32), alpha, beta, eps)
+
+
+def block_norm_workspace_bytes(n: moe_norm_desc) -> int:
+    b = load().moe_block_norm_workspace_bytes(ctypes.byref(n))
+    if b < 0:
+        raise MoeError(MOE_EINVAL, "moe_block_norm_workspace_bytes")
+    return int(b)
+
+
+def _norm_inputs(n, y, r, z, g_post, g_pre):
+    e, bf, f32 = n.rows * n.H, torch.bfloat16, torch.float32
+    elem = n.gate == MOE_GATE_ELEM
+    return [_buf("y", y, bf, e, r), _buf("r", r, f32 if n.res_fp32 else bf, e),
+            _buf("z", z, bf if elem else f32, e if elem else n.rows, r), _buf("g_post", g_post, f32, n.H, r),
+            _buf("g_pre", g_pre, f32, n.H, r)]
+
+
+def moe_block_norm_fwd(n, y, r, z, g_post, g_pre, r_out, xn, stats, stream=None):
+    e = n.rows * n.H
+    args = _norm_inputs(n, y, r, z, g_post, g_pre)
+    args += [_buf("r_out", r_out, r.dtype, e, r), _buf("xn", xn, torch.bfloat16, e, r),
+             _buf("stats", stats, torch.float32, 2 * n.rows, r)]
+    with torch.cuda.device(r.device):
+        rc = load().moe_block_norm_fwd(ctypes.byref(n), *args, _stream(stream, r))
+    return _check(rc, "moe_block_norm_fwd")
+
+
+def moe_block_norm_bwd(n, y, r, z, g_post, g_pre, stats, dr_out, dxn, dy, dr, dz, dg_post, dg_pre, ws, stream=None):
+    e, bf, f32 = n.rows * n.H, torch.bfloat16, torch.float32
+    elem = n.gate == MOE_GATE_ELEM
+    args = _norm_inputs(n, y, r, z, g_post, g_pre)
+    args += [_buf("stats", stats, f32, 2 * n.rows, r), _buf("dr_out", dr_out, r.dtype, e, r), _buf("dxn", dxn, bf, e, r),
+             _buf("dy", dy, bf, e, r), _buf("dr", dr, r.dtype, e, r),
+             _buf("dz", dz, bf if elem else f32, e if elem else n.rows, r), _buf("dg_post", dg_post, f32, n.H, r),
+             _buf("dg_pre", dg_pre, f32, n.H, r), _buf("ws", ws, torch.uint8, 0, r)]
+    with torch.cuda.device(r.device):
+        rc = load().moe_block_norm_bwd(ctypes.byref(n), *args, 0 if ws is None else ws.numel(), _stream(stream, r))
+    return _check(rc, "moe_block_norm_bwd")
+
+
+@dataclass
+class NormGrads:
+    dy: torch.Tensor | None
+    dr: torch.Tensor
+    dz: torch.Tensor | None
+    dg_post: torch.Tensor | None
+    dg_pre: torch.Tensor | None
+    ws: torch.Tensor
+
+
+def alloc_norm_bwd(n: moe_norm_desc, device, post: bool = True, pre: bool = True, y: bool = True) -> NormGrads:
+    """Gradients and workspace of moe_block_norm_bwd for a block with or
+    without a post-norm, a pre-norm and (y=False: a pre-norm alone) an output."""
+    bf, f32 = torch.bfloat16, torch.float32
+    shape = (n.rows, n.H)
+    dz = {MOE_GATE_NONE: None, MOE_GATE_TOKEN: ((n.rows,), f32), MOE_GATE_ELEM: (shape, bf)}[n.gate]
+    return NormGrads(
+        dy=torch.empty(shape, dtype=bf, device=device) if y else None,
+        dr=torch.empty(shape, dtype=f32 if n.res_fp32 else bf, device=device),
+        dz=torch.empty(dz[0], dtype=dz[1], device=device) if dz else None,
+        dg_post=torch.empty(n.H, dtype=f32, device=device) if post else None,
+        dg_pre=torch.empty(n.H, dtype=f32, device=device) if pre else None,
+        ws=torch.empty(max(block_norm_workspace_bytes(n), 256), dtype=torch.uint8, device=device),
+    )
+
+
+def block_norm_bwd(n, y, r, z, g_post, g_pre, stats, dr_out, dxn, b: NormGrads, stream=None):
+    return moe_block_norm_bwd(n, y, r, z, g_post, g_pre, stats, dr_out, dxn, b.dy, b.dr, b.dz, b.dg_post, b.dg_pre, b.ws,
+                              stream)
+
+
+# ---------------------------------------------------------------------------
+# Activation checkpoints in 8 bits.
+# ---------------------------------------------------------------------------
+
+def moe_ckpt_pack(src, q, scales, nrows=None, stream=None):
+    """Pack a bf16 tensor [rows][cols] into int8 codes (same shape) and float
+    scales [rows][cols/128]; nrows: a device int32 (one element, e.g.
+    seg_off[L:]) that limits the rows packed."""
+    rows, cols = src.shape
+    args = [_buf("src", src, torch.bfloat16, 0), rows, cols, _buf("nrows", nrows, torch.int32, 1, src),
+            _buf("q", q, torch.int8, rows * cols, src), _buf("scales", scales, torch.float32, rows * (cols // CKPT_BLOCK), src)]
+    with torch.cuda.device(src.device):
+        rc = load().moe_ckpt_pack(*args, _stream(stream, src))
+    return _check(rc, "moe_ckpt_pack")
+
+
+def ckpt_pack(src, nrows=None, stream=None):
+    """Allocate and fill (codes, scales) of a bf16 tensor [rows][cols]."""
+    q = torch.empty(src.shape, dtype=torch.int8, device=src.device)
+    s = torch.empty((src.shape[0], src.shape[1] // CKPT_BLOCK), dtype=torch.float32, device=src.device)
+    moe_ckpt_pack(src, q, s, nrows, stream)
+    return q, s
+
+
+def moe_ckpt_swiglu_bwd(q, scales, dA, wrow, dHU, A, dw, nrows=None, stream=None):
+    rows, I = dA.shape
+    bf, f32 = torch.bfloat16, torch.float32
+    args = [_buf("q", q, torch.int8, 2 * rows * I, dA), _buf("scales", scales, f32, 2 * rows * I // CKPT_BLOCK, dA),
+            _buf("dA", dA, bf, 0), _buf("wrow", wrow, f32, rows, dA), rows, I, _buf("nrows", nrows, torch.int32, 1, dA),
+            _buf("dHU", dHU, bf, 2 * rows * I, dA), _buf("A", A, bf, rows * I, dA), _buf("dw", dw, f32, rows, dA)]
+    with torch.cuda.device(dA.device):
+        rc = load().moe_ckpt_swiglu_bwd(*args, _stream(stream, dA))
+    return _check(rc, "moe_ckpt_swiglu_bwd")
+
+
+def moe_layer_bwd_ckpt(d, dOut, w, X, phi, route_row, seg_off, q, scales, W13, W2, dX, dW13, dW2, dw, ws, stream=None):
+    cap, n, H, I = capacity_rows(d), d.P * d.Np, d.H, d.I
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    args = [_buf("dOut", dOut, bf, n * H, X), _buf("w", w, f32, n * d.K, X), _buf("X", X, bf, n * H),
+            _buf("phi", phi, i32, 2 * cap, X), _buf("route_row", route_row, i32, n * d.K, X),
+            _buf("seg_off", seg_off, i32, d.L + 1, X), _buf("q", q, torch.int8, cap * 2 * I, X),
+            _buf("scales", scales, f32, cap * 2 * I // CKPT_BLOCK, X), _buf("W13", W13, bf, d.L * 2 * I * H, X),
+            _buf("W2", W2, bf, d.L * H * I, X), _buf("dX", dX, bf, n * H, X), _buf("dW13", dW13, f32, d.L * 2 * I * H, X),
+            _buf("dW2", dW2, f32, d.L * H * I, X), _buf("dw", dw, f32, n * d.K, X), _buf("ws", ws, torch.uint8, 0, X)]
+    with torch.cuda.device(X.device):
+        rc = load().moe_layer_bwd_ckpt(ctypes.byref(d), *args, ws.numel(), _stream(stream, X))
+    return _check(rc, "moe_layer_bwd_ckpt")

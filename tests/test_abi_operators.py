@@ -64,3 +64,102 @@ def test_few_refusals():
     a = [P[0], P[1], P[2], P[3], _fake(0x10002), P[5], P[6], None, None, P[7], P[8]]
     assert mx(ref, 0, *a, ws, None) == ops.MOE_EINVAL  # scale bytes are 4-byte aligned
     assert mx(ref, 2048, *P[:11], ws - 1, None) == ops.MOE_ENOSPC
+
+
+def norm_desc(**kw):
+    v = dict(rows=16, H=7168, gate=ops.MOE_GATE_NONE) | kw
+    return ops.make_norm_desc(v.pop("rows"), v.pop("H"), **v)
+
+
+def test_norm_sizes():
+    lib = ops.load()
+    assert ops.block_norm_workspace_bytes(norm_desc()) == 16 * 2 * 7168 * 4
+    assert ops.block_norm_workspace_bytes(norm_desc(rows=1 << 20)) == 512 * 2 * 7168 * 4
+    assert ops.block_norm_workspace_bytes(norm_desc(rows=0)) == 0
+    for bad in (norm_desc(rows=-1), norm_desc(H=0), norm_desc(H=7164), norm_desc(H=32776), norm_desc(gate=3), norm_desc(gate=-1),
+                norm_desc(eps=-1e-6), norm_desc(eps=float("nan"))):
+        assert lib.moe_block_norm_workspace_bytes(ctypes.byref(bad)) == -1
+    odd = norm_desc()
+    odd.res_fp32 = 2
+    assert lib.moe_block_norm_workspace_bytes(ctypes.byref(odd)) == -1
+
+
+def test_norm_fwd_refusals():
+    lib = ops.load()
+
+    def fwd(n, y=P[0], r=P[1], z=None, g_post=P[2], g_pre=P[3], r_out=P[4], xn=P[5], stats=P[6]):
+        return lib.moe_block_norm_fwd(ctypes.byref(n), y, r, z, g_post, g_pre, r_out, xn, stats, None)
+
+    assert lib.moe_block_norm_fwd(ctypes.byref(norm_desc(rows=0)), *([None] * 8), None) == ops.MOE_OK  # nothing to do
+    n = norm_desc()
+    assert lib.moe_block_norm_fwd(None, *P[:8], None) == ops.MOE_EINVAL
+    for kw in (dict(r=None), dict(stats=None), dict(y=None), dict(r_out=None), dict(xn=None), dict(g_pre=None), dict(z=P[7]),
+               dict(y=None, r_out=None), dict(y=None, r_out=None, g_post=None, g_pre=None, xn=None)):
+        assert fwd(n, **kw) == ops.MOE_EINVAL, kw
+    for k in ("y", "r", "g_post", "g_pre", "r_out", "xn", "stats"):
+        assert fwd(n, **{k: BAD}) == ops.MOE_EINVAL, k
+    for gate in (ops.MOE_GATE_TOKEN, ops.MOE_GATE_ELEM):
+        g = norm_desc(gate=gate)
+        assert fwd(g) == fwd(g, z=BAD) == ops.MOE_EINVAL
+        assert fwd(g, z=P[7], y=None, r_out=None, g_post=None) == ops.MOE_EINVAL
+    assert fwd(norm_desc(H=12)) == ops.MOE_EUNSUPPORTED
+    assert fwd(norm_desc(H=40000)) == ops.MOE_EUNSUPPORTED
+
+
+def test_norm_bwd_refusals():
+    lib = ops.load()
+    names = ("y", "r", "z", "g_post", "g_pre", "stats", "dr_out", "dxn", "dy", "dr", "dz", "dg_post", "dg_pre", "ws")
+    full = dict(zip(names, P))
+
+    def bwd(n, ws_bytes=1 << 30, **kw):
+        a = full | kw
+        return lib.moe_block_norm_bwd(ctypes.byref(n), *(a[k] for k in names), ws_bytes, None)
+
+    n = norm_desc(gate=ops.MOE_GATE_ELEM)
+    need = ops.block_norm_workspace_bytes(n)
+    assert bwd(n, need - 1) == ops.MOE_ENOSPC
+    for k in names:  # each alone is missed by its partner (dr_out alone may go)
+        if k != "dr_out":
+            assert bwd(n, **{k: None}) == ops.MOE_EINVAL, k
+        assert bwd(n, **{k: BAD}) == ops.MOE_EINVAL, k
+    assert bwd(n, dr_out=None, dxn=None, g_pre=None, dg_pre=None) == ops.MOE_EINVAL  # no gradient arrives
+    assert bwd(norm_desc()) == ops.MOE_EINVAL  # a gate's input without a gate
+    assert bwd(norm_desc(H=12, gate=ops.MOE_GATE_ELEM)) == ops.MOE_EUNSUPPORTED
+
+
+def test_ckpt_refusals():
+    lib = ops.load()
+    pack, bwd = lib.moe_ckpt_pack, lib.moe_ckpt_swiglu_bwd
+    assert pack(None, 0, 128, None, None, None, None) == ops.MOE_OK
+    for rows, cols in ((-1, 128), (4, 0), (4, 100), (4, -128)):
+        assert pack(P[0], rows, cols, None, P[1], P[2], None) == ops.MOE_EINVAL
+    for a in ((None, P[1], P[2]), (P[0], None, P[2]), (P[0], P[1], None), (BAD, P[1], P[2]), (P[0], BAD, P[2]), (P[0], P[1], _fake(0x10002))):
+        assert pack(a[0], 4, 128, None, a[1], a[2], None) == ops.MOE_EINVAL
+    assert pack(P[0], 4, 128, _fake(0x10002), P[1], P[2], None) == ops.MOE_EINVAL
+    assert bwd(None, None, None, None, 0, 128, None, None, None, None, None) == ops.MOE_OK
+    for rows, I in ((-1, 128), (4, 0), (4, 64)):
+        assert bwd(*P[:4], rows, I, None, *P[4:7], None) == ops.MOE_EINVAL
+    for i in range(8):
+        a = [P[0], P[1], P[2], P[3], P[4], P[5], P[6], P[7]]  # q, scales, dA, wrow, nrows, dHU, A, dw
+        if i in (0, 1, 2, 5):
+            a[i] = None
+            assert bwd(*a[:4], 4, 128, *a[4:], None) == ops.MOE_EINVAL, i
+        a[i] = _fake(0x10002)
+        assert bwd(*a[:4], 4, 128, *a[4:], None) == ops.MOE_EINVAL, i
+
+
+def test_layer_bwd_ckpt_refusals():
+    lib = ops.load()
+    d = ops.make_desc(8, 7168, 8, 384, 48, H=7168, I=2048)
+    cap = ops.capacity_rows(d)
+    ws = ops.workspace_bytes(d, ops.MOE_OP_LAYER_BWD_CKPT)
+    assert ws >= ops.workspace_bytes(d, ops.MOE_OP_LAYER_BWD) + cap * (7168 + 2048) * 2
+    args = P[:15]
+    assert lib.moe_layer_bwd_ckpt(ctypes.byref(d), *args, ws - 1, None) == ops.MOE_ENOSPC
+    for i in range(15):
+        assert lib.moe_layer_bwd_ckpt(ctypes.byref(d), *args[:i], None, *args[i + 1:], ws, None) == ops.MOE_EINVAL, i
+        assert lib.moe_layer_bwd_ckpt(ctypes.byref(d), *args[:i], _fake(0x10002), *args[i + 1:], ws, None) == ops.MOE_EINVAL, i
+    two = ops.make_desc(8, 7168, 8, 384, 48, H=7168, I=2048, num_batches=2)
+    assert lib.moe_layer_bwd_ckpt(ctypes.byref(two), *args, ws, None) == ops.MOE_EINVAL
+    odd = ops.make_desc(8, 7168, 8, 384, 48, H=7000, I=2048)
+    assert lib.moe_layer_bwd_ckpt(ctypes.byref(odd), *args, ws, None) == ops.MOE_EUNSUPPORTED
