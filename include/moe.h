@@ -643,7 +643,7 @@ int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
 /*
  * Activation checkpoints in 8 bits.  Format: 128 consecutive elements of a row
  * share one float scale; with amax the largest magnitude of the block,
- *     scale = amax / 127,   code = rint(x * (127 / amax))   (int8, ties to even)
+ *     scale = amax / 127,   code = rint(x * (127 * (1 / amax)))   (int8, ties to even)
  * each operation one IEEE fp32 operation; the value read back is code * scale.
  * A block with amax < 2^-100 gets scale 0 and codes 0; a block that holds an
  * infinity or a NaN gets scale NaN and codes 0 (all of it reads back as NaN).

@@ -1,7 +1,7 @@
 // Activation checkpoints in 8 bits, and the backward that reads them.
 //
 // Format: 128 consecutive elements of a row share one fp32 scale
-//   s = fl(amax / 127),  code = rint(fl(x fl(127 / amax))) in [-127, 127],
+//   s = fl(amax / 127),  code = rint(fl(x fl(127 fl(1 / amax)))) in [-127, 127],
 // every operation one IEEE fp32 operation, so the codes are the same wherever
 // they are computed.  A block whose largest magnitude is below 2^-100 gets
 // scale 0; one that holds an infinity or a NaN gets scale NaN (and codes 0),
@@ -52,7 +52,7 @@ __device__ __forceinline__ void ckpt_pack_body(const uint16_t *src, int64_t rows
         for (int o = 4; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
         const float amax = __uint_as_float(m);
         const bool finite = m < 0x7f800000u, tiny = amax < kCkptTiny;
-        const float inv = finite && !tiny ? 127.0f / amax : 0.0f;
+        const float inv = finite && !tiny ? 127.0f * (1.0f / amax) : 0.0f;
         u32x4 c;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

@@ -18,7 +18,7 @@ def pack_np(x: np.ndarray):
     v = np.ascontiguousarray(x, np.float32).reshape(x.shape[0], -1, B)
     amax = np.abs(v).max(-1, keepdims=True)
     with np.errstate(all="ignore"):
-        q = np.rint(v * (np.float32(127) / amax))
+        q = np.rint(v * (np.float32(127) * (np.float32(1) / amax)))
         s = amax / np.float32(127)
     tiny, bad = amax < np.float32(2.0 ** -100), ~np.isfinite(amax)
     q = np.where(tiny | bad, 0, q).astype(np.int8)
