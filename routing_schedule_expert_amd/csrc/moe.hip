@@ -213,10 +213,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_few_gateup(FewArgs a) {
     few_gateup_body<MX>(a, few_smem);
 }
 
-template <bool MX>
+template <bool MX, int B>
 __global__ __launch_bounds__(kFewThreads, 4) void k_few_down(FewArgs a) {
     extern __shared__ __attribute__((aligned(16))) int32_t few_smem[];
-    few_down_body<MX>(a, few_smem);
+    few_down_body<MX, B>(a, few_smem);
 }
 
 template <bool F32, int CH>
@@ -1621,6 +1621,10 @@ int few_check(const moe_desc *d, int32_t Is) {
     if (d->num_batches != 1 || Is < 0) return MOE_EINVAL;
     if ((int64_t)d->P * d->Np * d->K > kFewMaxRoutes) return MOE_EUNSUPPORTED;
     if (Is % 128 || 768ll * Is >= (1ll << 30)) return MOE_EUNSUPPORTED;
+    // X, the activations and 16 rows of weights are addressed with 32-bit byte offsets
+    if (2ll * d->P * d->Np * d->H >= (1ll << 32) || 2ll * few_rows(d, Is) * std::max(d->I, Is) >= (1ll << 32) ||
+        32ll * std::max(d->H, std::max(d->I, Is)) >= (1ll << 31))
+        return MOE_EUNSUPPORTED;
     return MOE_OK;
 }
 
@@ -1644,11 +1648,16 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     a.plan = static_cast<int32_t *>(ws);
     a.act = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + few_plan_bytes(d));
     const int rows = few_rows(d, Is);
-    // parts of the reduction dimension in the down launch: 8 while the sums of
-    // all rows and parts stay within 64 KiB of LDS (two workgroups per CU)
-    a.S = std::max(1, std::min(kFewWaves, 1024 / rows));
-    const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R), lds_down = 4 * (size_t)few_down_words(a.L, a.R, rows, a.S);
-    if (lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
+    // down launch: parts of at least 256 elements of the smaller reduction
+    // dimension, a power of two; 32 KiB of LDS for the parts' sums, less where
+    // the sums of all rows leave less
+    const int inner = Is > 0 ? std::min(d->I, Is) : d->I, C = 16;
+    a.S = inner >= 2048 ? 8 : inner >= 1024 ? 4 : inner >= 512 ? 2 : 1;
+    const int room = (int)(kMaxLds / 4) - few_down_words(a.L, a.R, rows, a.S, 0, C);
+    a.cap = std::min(rows, std::min(8192, room) / (a.S * C));
+    const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R);
+    const size_t lds_down = 4 * (size_t)few_down_words(a.L, a.R, rows, a.S, a.cap, C);
+    if (a.cap < 1 || lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + Is / kFewRows;
     {
         TraceScope tr("few_gateup", s);
@@ -1657,7 +1666,7 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     }
     if (launch_status() != MOE_OK) return MOE_EHIP;
     TraceScope tr("few_down", s);
-    hipLaunchKernelGGL(k_few_down<MX>, dim3(a.H / kFewRows), dim3(kFewThreads), lds_down, s, a);
+    hipLaunchKernelGGL((k_few_down<MX, 2>), dim3(a.H / C), dim3(kFewThreads), lds_down, s, a);
     return launch_status();
 }
 
