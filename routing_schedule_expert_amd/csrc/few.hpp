@@ -32,6 +32,8 @@ constexpr int kFewWaves = 8;
 constexpr int kFewThreads = 64 * kFewWaves;
 constexpr int kFewMaxRoutes = 1024;  // routes of one call (P * Np * K)
 constexpr int kFewRows = 16;         // activation columns of a gate/up unit
+constexpr int kFewGateupRegs = 100;  // registers for a wave's sums and steps in flight
+constexpr int kFewDownRegs = 48;
 
 struct FewArgs {
     const int32_t *routes;
@@ -43,14 +45,17 @@ struct FewArgs {
     uint16_t *out, *act;
     int32_t *plan;
     int T, K, R, E, L, base, H, I, Is, ld;  // ld: elements of an activation row, max(I, Is)
-    int S, cap;                             // down: parts of the reduction dimension; places of a round
+    int room;                               // down: places (times parts) of a round
 };
 
 // The list of a call's local routes grouped by expert, in the workspace
 // (written by the gate/up launch's first workgroup, read by the down launch).
 //   [0] ids outside [0, E)  [1] experts with a route (A)  [2] local routes (n)
+//   [3], [4] of the A experts, how many have over 16 and over 8 routes
 //   [kFewHead ...]       A expert ids, then A + 1 offsets
 //   then n route numbers in expert order, then the place of each route (-1)
+// The experts stand by their number of routes: over 16, 9 to 16, up to 8, by id
+// within each kind.
 constexpr int kFewHead = 64;
 __host__ __device__ inline int few_max_experts(int L, int R) { return L < R ? L : R; }
 __host__ __device__ inline int few_plan_words(int L, int R) { return kFewHead + 2 * few_max_experts(L, R) + 1 + 2 * R; }
@@ -67,28 +72,28 @@ struct FewPlan {
 };
 
 // Words of LDS of the gate/up launch: the waves' sums, one count per local
-// expert, 4 words for the head, and the list; and of the down launch: the
+// expert, 8 words for the head, and the list; and of the down launch: the
 // routes' sums and the list.
 constexpr int kFewRedLd = 36;  // 32 sums of a column and 4 words that spread the columns over the banks
 constexpr int kFewRedWords = kFewWaves * 32 * kFewRedLd;
 __host__ __device__ inline int few_gateup_words(int L, int R) {
-    return kFewRedWords + L + 4 + few_plan_words(L, R) - kFewHead;
+    return kFewRedWords + L + 8 + few_plan_words(L, R) - kFewHead;
 }
-__host__ __device__ inline int few_down_words(int L, int R, int rows, int S, int cap, int C) {
-    return (rows + S * cap) * C + few_plan_words(L, R) - kFewHead;
+__host__ __device__ inline int few_down_words(int L, int R, int rows, int room, int C) {
+    return (rows + room) * C + few_plan_words(L, R) - kFewHead;
 }
 
 // Builds the list in LDS: count the routes of each expert (a route's rank is
 // the order in which the LDS atomics answer: it only says which MFMA column
-// computes the route, and columns are independent), take the experts with a
-// route in ascending order and their offsets, place the routes.
-// Returns A; head[0..2] as in the plan.
+// computes the route, and columns are independent), take the experts of each
+// kind in ascending order and their offsets, place the routes.
+// Returns A; head[0..4] as in the plan.
 __device__ __forceinline__ int few_build(const FewArgs &a, int *cnt, const FewPlan &p, int *head) {
     const int t = threadIdx.x;
     constexpr int kPer = kFewMaxRoutes / kFewThreads;
     int lid[kPer], rank[kPer], bad = 0;
     for (int i = t; i < a.L; i += kFewThreads) cnt[i] = 0;
-    if (t < 3) head[t] = 0;
+    if (t < 5) head[t] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -107,23 +112,30 @@ __device__ __forceinline__ int few_build(const FewArgs &a, int *cnt, const FewPl
     __syncthreads();
     if (t < kWave) {
         int na = 0, n = 0;
-        for (int l0 = 0; l0 < a.L; l0 += kWave) {
-            const int l = l0 + t, c = l < a.L ? cnt[l] : 0;
-            int incl = c;
+        for (int kind = 0; kind < 3; ++kind) {
+            const int least = kind == 0 ? 17 : kind == 1 ? 9 : 1, most = kind == 0 ? kFewMaxRoutes : kind == 1 ? 16 : 8;
+            for (int l0 = 0; l0 < a.L; l0 += kWave) {
+                const int l = l0 + t, all = l < a.L ? cnt[l] : 0;
+                // an expert already placed holds -1 - its offset
+                const int c = all >= least && all <= most ? all : 0;
+                const uint64_t some = ballot(c > 0);
+                if (!some) continue;
+                int incl = c;
 #pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) {
-                const int v = __shfl_up(incl, o, kWave);
-                if (t >= o) incl += v;
+                for (int o = 1; o < kWave; o <<= 1) {
+                    const int v = __shfl_up(incl, o, kWave);
+                    if (t >= o) incl += v;
+                }
+                if (c > 0) {
+                    const int k = na + lanes_below(some);
+                    p.expert[k] = l;
+                    p.off[k] = n + incl - c;
+                    cnt[l] = -1 - (n + incl - c);
+                }
+                na += __popcll(some);
+                n += __shfl(incl, kWave - 1, kWave);
             }
-            const uint64_t some = ballot(c > 0);
-            if (c > 0) {
-                const int k = na + lanes_below(some);
-                p.expert[k] = l;
-                p.off[k] = n + incl - c;
-            }
-            if (l < a.L) cnt[l] = n + incl - c;
-            na += __popcll(some);
-            n += __shfl(incl, kWave - 1, kWave);
+            if (t == 0 && kind < 2) head[3 + kind] = na;
         }
         if (t == 0) p.off[na] = n, head[1] = na, head[2] = n;
     }
@@ -132,7 +144,7 @@ __device__ __forceinline__ int few_build(const FewArgs &a, int *cnt, const FewPl
     for (int i = 0; i < kPer; ++i) {
         const int r = t + i * kFewThreads;
         if (r < a.R) {
-            const int at = lid[i] >= 0 ? cnt[lid[i]] + rank[i] : -1;
+            const int at = lid[i] >= 0 ? -1 - cnt[lid[i]] + rank[i] : -1;
             p.place[r] = at;
             if (at >= 0) p.route[at] = r;
         }
@@ -238,40 +250,73 @@ struct FewStep {
     }
 };
 
-// acc[m][t] = block m's rows times tile t's tokens over the elements [e0, e1)
-// of the reduction dimension (multiples of kStep from 0).  D steps are in
-// flight: a step's registers are loaded again as soon as they are used.
-template <bool MX, int V, int M, int NT>
-__device__ __forceinline__ void few_product(const FewLane<MX, V> &l, const uint8_t *const (&wp)[M], const uint8_t *const (&ws)[M],
-                                            int cols, const uint8_t *xb, const uint32_t (&xo)[NT], int k0, int k1,
-                                            f32x4 (&acc)[M][NT]) {
-    using Step = FewStep<MX, V, M, NT>;
-    constexpr int per = (MX ? 5 : 4) * M + (MX ? 8 : 4) * NT, left = 92 - 4 * M * NT;  // registers of a step; for all steps
-    constexpr int D = left >= 4 * per ? 4 : left >= 3 * per ? 3 : left >= 2 * per ? 2 : 1;
+// Where an item's operands start: its M blocks of weight rows (wave-uniform
+// pointers) and this lane's token of each tile (bytes from the tokens' matrix).
+template <int M, int NT>
+struct FewItem {
+    const uint8_t *wp[M], *ws[M];
+    uint32_t xo[NT];
+};
+
+// Streams `items` products through one wave: for each, block m's rows times
+// tile t's tokens over the steps [k0, k0 + n) of the reduction dimension go to
+// emit(item, acc).  item(i) gives the operands' places.  D steps are in flight:
+// a step's registers are loaded again as soon as they are used, the last ones of
+// an item with the first steps of the next, so the wave's loads never run dry
+// between items.
+template <bool MX, int V, int M, int NT, int D, class Item, class Emit>
+__device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, int cols, const void *tokens, int k0, int n, int items, Item item,
+                                           Emit emit) {
+    if (items <= 0) return;
     const uint32_t wo = (uint32_t)(l.row * cols * (MX ? 1 : 2) + l.group * 16), so = (uint32_t)(l.row * (cols / 32));
+    const uint8_t *xb = static_cast<const uint8_t *>(tokens);
+    FewStep<MX, V, M, NT> st[D];
+    FewItem<M, NT> cur, next;
+    item(0, cur);
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int j = 0; j < D; ++j)
+        if (j < n) st[j].load(cur.wp, cur.ws, wo, so, xb, cur.xo, k0 + j);
+    for (int it = 0; it < items; ++it) {
+        const bool more = it + 1 < items;
+        if (more) item(it + 1, next);
+        f32x4 acc[M][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Step st[D];
-    int k = k0;
-    if (k + D <= k1) {
+        for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < D; ++j) st[j].load(wp, ws, wo, so, xb, xo, k + j);
-        for (; k + 2 * D <= k1; k += D)
+            for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int k = 0;
+        for (; k + 2 * D <= n; k += D)
 #pragma unroll
             for (int j = 0; j < D; ++j) {
                 st[j].mul(l, acc);
-                st[j].load(wp, ws, wo, so, xb, xo, k + D + j);
+                st[j].load(cur.wp, cur.ws, wo, so, xb, cur.xo, k0 + k + D + j);
+            }
+        // fewer than 2 D steps are left, the first D of them in flight
+#pragma unroll
+        for (int j = 0; j < D; ++j)
+            if (k + j < n) {
+                st[j].mul(l, acc);
+                if (k + D + j < n)
+                    st[j].load(cur.wp, cur.ws, wo, so, xb, cur.xo, k0 + k + D + j);
+                else if (more)
+                    st[j].load(next.wp, next.ws, wo, so, xb, next.xo, k0 + j);
             }
 #pragma unroll
-        for (int j = 0; j < D; ++j) st[j].mul(l, acc);
-        k += D;
+        for (int j = 0; j < D; ++j)
+            if (k + D + j < n) {
+                st[j].mul(l, acc);
+                if (more) st[j].load(next.wp, next.ws, wo, so, xb, next.xo, k0 + j);
+            }
+        emit(it, acc);
+        cur = next;
     }
-    for (; k < k1; ++k) {
-        st[0].load(wp, ws, wo, so, xb, xo, k);
-        st[0].mul(l, acc);
-    }
+}
+
+// Steps in flight that fit `regs` registers beside the sums.
+template <bool MX, int M, int NT>
+constexpr int few_depth(int regs) {
+    const int per = (MX ? 5 : 4) * M + (MX ? 8 : 4) * NT, d = (regs - 4 * M * NT) / per;
+    return d < 1 ? 1 : d > 8 ? 8 : d;
 }
 
 // The sums of a block and tile that this lane keeps: row r(i) of the block and
@@ -293,37 +338,44 @@ __device__ __forceinline__ void few_sums(const f32x4 &acc, Put put) {
 
 __device__ __forceinline__ int wave_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Gate/up of activation columns [i0, i0 + 16) of one expert for up to
-// NT tiles of its routes from `first` on: the workgroup's waves split H; their
-// sums meet in LDS (red), 32 tokens at a time, added in wave order.  The
-// routes' tokens are route[..] / K, their activations go to row route[..] of
-// act; route null: the tokens themselves (shared expert), rows R + token.
+// A unit of the gate/up launch: activation columns [i0, i0 + 16) of one expert
+// (W, with `inner` activation columns) for its `n` routes.  The routes' tokens
+// are route[..] / K, their activations go to row route[..] of act; route null:
+// the tokens themselves (shared expert), rows R + token.
+struct FewUnit {
+    FewMatrix W;
+    int inner, i0, n;
+    const int *route;
+};
+
+__device__ __forceinline__ int few_token(const FewArgs &a, const int *route, int k) { return route ? route[k] / a.K : k; }
+__device__ __forceinline__ int few_act_row(const FewArgs &a, const int *route, int k) { return route ? route[k] : a.R + k; }
+
+// Operands of a unit's routes from `first` on: V gate blocks, V up blocks.
 template <bool MX, int V, int NT>
-__device__ __forceinline__ void few_gateup_pass(const FewArgs &a, const FewMatrix &W, int inner, int i0, const int *route,
-                                                int first, int n, float *red) {
+__device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX, V> &l,
+                                                FewItem<2 * V, NT> &it) {
     using L = FewLane<MX, V>;
-    constexpr int M = 2 * V;  // gate blocks, then up blocks
-    const L l;
-    const int t = threadIdx.x, wave = wave_uniform(t >> 6);
-    const uint8_t *wp[M], *ws[M];
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        const int64_t row = (m < V ? 0 : inner) + i0 + (m % V) * L::kRows;
-        wp[m] = W.p + row * W.cols * (MX ? 1 : 2);
-        ws[m] = W.s + row * (W.cols / 32);
+    for (int m = 0; m < 2 * V; ++m) {
+        const int64_t row = (m < V ? 0 : u.inner) + u.i0 + (m % V) * L::kRows;
+        it.wp[m] = u.W.p + row * u.W.cols * (MX ? 1 : 2);
+        it.ws[m] = u.W.s + row * (u.W.cols / 32);
     }
-    uint32_t xo[NT];
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-        const int k = min(first + q * L::kTokens + l.token, n - 1);
-        const int tok = route ? route[k] / a.K : k;
-        xo[q] = (uint32_t)tok * (uint32_t)(a.H * 2) + l.group * (L::kGroup * 2);
-    }
-    f32x4 acc[M][NT];
-    const int steps = a.H / L::kStep;
-    few_product<MX, V, M, NT>(l, wp, ws, W.cols, reinterpret_cast<const uint8_t *>(a.X), xo, wave * steps / kFewWaves,
-                              (wave + 1) * steps / kFewWaves, acc);
+    for (int q = 0; q < NT; ++q)
+        it.xo[q] = (uint32_t)few_token(a, u.route, min(first + q * L::kTokens + l.token, u.n - 1)) * (uint32_t)(a.H * 2) +
+                   l.group * (L::kGroup * 2);
+}
+
+// The waves' sums of a unit meet in LDS (red), 32 tokens at a time, and are
+// added in wave order; then the activation, rounded once.
+template <bool MX, int V, int NT>
+__device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX, V> &l,
+                                                const f32x4 (&acc)[2 * V][NT], float *red) {
+    using L = FewLane<MX, V>;
     constexpr int per = 32 / L::kTokens;  // tiles that meet at a time
+    const int t = threadIdx.x, wave = t >> 6;
 #pragma unroll
     for (int q0 = 0; q0 < NT; q0 += per) {
         __syncthreads();  // the previous sums have been read
@@ -331,11 +383,11 @@ __device__ __forceinline__ void few_gateup_pass(const FewArgs &a, const FewMatri
         for (int q = q0; q < (q0 + per < NT ? q0 + per : NT); ++q) {
             float *dst = red + (wave * 32 + (q - q0) * L::kTokens + l.token) * kFewRedLd;
 #pragma unroll
-            for (int m = 0; m < M; ++m) few_sums<V>(acc[m][q], [&](int r, float v) { dst[m * L::kRows + r] = v; });
+            for (int m = 0; m < 2 * V; ++m) few_sums<V>(acc[m][q], [&](int r, float v) { dst[m * L::kRows + r] = v; });
         }
         __syncthreads();
         const int tok = t >> 4, i = t & 15, k = first + q0 * L::kTokens + tok;
-        if (tok < (NT - q0) * L::kTokens && k < n) {
+        if (tok < (NT - q0) * L::kTokens && k < u.n) {
             float gate = 0.f, up = 0.f;
 #pragma unroll
             for (int v = 0; v < kFewWaves; ++v) {
@@ -343,37 +395,49 @@ __device__ __forceinline__ void few_gateup_pass(const FewArgs &a, const FewMatri
                 gate += src[0];
                 up += src[16];
             }
-            const int row = route ? route[k] : a.R + k;
-            a.act[(int64_t)row * a.ld + i0 + i] = f2bf(gate / (1.0f + __expf(-gate)) * up);
+            a.act[(int64_t)few_act_row(a, u.route, k) * a.ld + u.i0 + i] = f2bf(gate / (1.0f + __expf(-gate)) * up);
         }
     }
 }
 
+// `count` units (unit(i) for i in turn), all with at most NT tiles of routes
+// from `first` on, the waves splitting H.
+template <bool MX, int V, int NT, class Unit>
+__device__ __forceinline__ void few_gateup_run(const FewArgs &a, int count, int first, Unit unit, float *red) {
+    using L = FewLane<MX, V>;
+    const L l;
+    const int wave = wave_uniform(threadIdx.x >> 6), steps = a.H / L::kStep;
+    const int k0 = wave * steps / kFewWaves, n = (wave + 1) * steps / kFewWaves - k0;
+    few_stream<MX, V, 2 * V, NT, few_depth<MX, 2 * V, NT>(kFewGateupRegs)>(
+        l, a.H, a.X, k0, n, count, [&](int i, FewItem<2 * V, NT> &it) { few_gateup_item<MX, V, NT>(a, unit(i), first, l, it); },
+        [&](int i, const f32x4(&acc)[2 * V][NT]) { few_gateup_join<MX, V, NT>(a, unit(i), first, l, acc, red); });
+}
+
+// A unit with any number of routes, 64 at a time.
 template <bool MX>
-__device__ __forceinline__ void few_gateup_unit(const FewArgs &a, const FewMatrix &W, int inner, int i0, const int *route, int n,
-                                                float *red) {
-    if (n <= 8) return few_gateup_pass<MX, 2, 1>(a, W, inner, i0, route, 0, n, red);
-    if (n <= 16) return few_gateup_pass<MX, 2, 2>(a, W, inner, i0, route, 0, n, red);
-    for (int first = 0; first < n; first += 64) {
-        if (n - first <= 32)
-            few_gateup_pass<MX, 1, 2>(a, W, inner, i0, route, first, n, red);
+__device__ __forceinline__ void few_gateup_wide(const FewArgs &a, const FewUnit &u, float *red) {
+    for (int first = 0; first < u.n; first += 64) {
+        if (u.n - first <= 16)
+            few_gateup_run<MX, 2, 2>(a, 1, first, [&](int) { return u; }, red);
+        else if (u.n - first <= 32)
+            few_gateup_run<MX, 1, 2>(a, 1, first, [&](int) { return u; }, red);
         else
-            few_gateup_pass<MX, 1, 4>(a, W, inner, i0, route, first, n, red);
+            few_gateup_run<MX, 1, 4>(a, 1, first, [&](int) { return u; }, red);
     }
 }
 
-// Persistent over (expert, block of 16 activation columns): the shared
-// expert's blocks first (they have every token's column, so they are the
-// longest), then those of the experts that have a route.
+// Persistent over the units, the heaviest first: the shared expert's blocks
+// (every token's columns), the experts with over 16 routes, then in two streams
+// those with up to 16 and up to 8.
 template <bool MX>
 __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
     float *red = reinterpret_cast<float *>(lds);
     int *cnt = lds + kFewRedWords, *head = cnt + a.L;
-    const FewPlan p(head + 4, a.L, a.R);
+    const FewPlan p(head + 8, a.L, a.R);
     const int na = wave_uniform(few_build(a, cnt, p, head));
     if (blockIdx.x == 0) {
         const FewPlan o(a.plan + kFewHead, a.L, a.R);
-        if (threadIdx.x < 3) a.plan[threadIdx.x] = head[threadIdx.x];
+        if (threadIdx.x < 5) a.plan[threadIdx.x] = head[threadIdx.x];
         for (int i = threadIdx.x; i <= na; i += kFewThreads) {
             if (i < na) o.expert[i] = p.expert[i];
             o.off[i] = p.off[i];
@@ -383,87 +447,113 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
             o.place[i] = p.place[i];
         }
     }
-    const int blocks = a.I / kFewRows, shared = a.Is / kFewRows;
-    const int64_t units = (int64_t)na * blocks + shared;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        if (u < shared) {
-            const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S13), nullptr, a.H};
-            few_gateup_unit<false>(a, W, a.Is, (int)u * kFewRows, nullptr, a.T, red);
-        } else {
-            const int k = (int)((u - shared) / blocks), i0 = (int)((u - shared) % blocks) * kFewRows;
-            const int64_t row = (int64_t)wave_uniform(p.expert[k]) * 2 * a.I;
-            const int off = wave_uniform(p.off[k]), n = wave_uniform(p.off[k + 1]) - off;
-            const FewMatrix W{static_cast<const uint8_t *>(a.W13) + row * a.H * (MX ? 1 : 2), MX ? a.W13s + row * (a.H / 32) : nullptr,
-                              a.H};
-            few_gateup_unit<MX>(a, W, a.I, i0, p.route + off, n, red);
-        }
+    const int blocks = a.I / kFewRows, shared = a.Is / kFewRows, step = gridDim.x;
+    const int wide = wave_uniform(head[3]) * blocks, mid = wave_uniform(head[4]) * blocks, all = na * blocks;
+    auto routed = [&](int u) {  // unit u of the experts in the list's order
+        const int k = u / blocks, off = wave_uniform(p.off[k]);
+        const int64_t row = (int64_t)wave_uniform(p.expert[k]) * 2 * a.I;
+        return FewUnit{{static_cast<const uint8_t *>(a.W13) + row * a.H * (MX ? 1 : 2), MX ? a.W13s + row * (a.H / 32) : nullptr, a.H},
+                       a.I, u % blocks * kFewRows, wave_uniform(p.off[k + 1]) - off, p.route + off};
+    };
+    int u = blockIdx.x;
+    for (; u < shared; u += step) {
+        const FewUnit s{{reinterpret_cast<const uint8_t *>(a.S13), nullptr, a.H}, a.Is, u * kFewRows, a.T, nullptr};
+        if (a.T <= 8)
+            few_gateup_run<false, 2, 1>(a, 1, 0, [&](int) { return s; }, red);
+        else
+            few_gateup_wide<false>(a, s, red);
     }
+    for (u -= shared; u < wide; u += step) few_gateup_wide<MX>(a, routed(u), red);
+    const int nmid = u < mid ? (mid - u + step - 1) / step : 0;
+    few_gateup_run<MX, 2, 2>(a, nmid, 0, [&](int i) { return routed(u + i * step); }, red);
+    u += nmid * step;
+    const int nlow = u < all ? (all - u + step - 1) / step : 0;
+    few_gateup_run<MX, 2, 1>(a, nlow, 0, [&](int i) { return routed(u + i * step); }, red);
 }
 
-// Down of output columns [h0, h0 + 8 B) for the routes [first, n) of one
-// expert, at most NT tiles, over one part of its activations: one wave, no
-// barrier; the sums go to y[.. - first][8 B].  act rows as in few_gateup_pass.
-template <bool MX, int V, int B, int NT>
-__device__ __forceinline__ void few_down_pass(const FewArgs &a, const FewMatrix &W, int h0, const int *route, int first, int n,
-                                              int part, float *y) {
+// Parts of a reduction dimension of `inner` elements: at least 256 each, a
+// power of two up to `most`.
+__host__ __device__ inline int few_parts(int inner, int most) {
+    int S = most;
+    while (S > 1 && inner < 256 * S) S /= 2;
+    return S;
+}
+
+// An item of the down launch: output columns [h0, h0 + 8 B) of one expert for
+// its routes [first, n), whose sums go to y[.. - first][8 B].
+struct FewSlice {
+    FewMatrix W;
+    const int *route;
+    int first, n;
+    float *y;
+};
+
+// `count` items (slice(i) for i in turn) with at most NT tiles each, over part
+// `part` of S of their activations: one wave, no barrier.
+template <bool MX, int V, int B, int NT, class Slice>
+__device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols, int part, int S, int count, Slice slice) {
     using L = FewLane<MX, V>;
     constexpr int M = B * V / 2;
     const L l;
-    const uint8_t *wp[M], *ws[M];
+    const int steps = cols / L::kStep, k0 = part * steps / S, n = (part + 1) * steps / S - k0;
+    few_stream<MX, V, M, NT, few_depth<MX, M, NT>(kFewDownRegs)>(
+        l, cols, a.act, k0, n, count,
+        [&](int i, FewItem<M, NT> &it) {
+            const FewSlice s = slice(i);
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        const int64_t row = h0 + m * L::kRows;
-        wp[m] = W.p + row * W.cols * (MX ? 1 : 2);
-        ws[m] = W.s + row * (W.cols / 32);
-    }
-    uint32_t xo[NT];
+            for (int m = 0; m < M; ++m) {
+                const int64_t row = h0 + m * L::kRows;
+                it.wp[m] = s.W.p + row * cols * (MX ? 1 : 2);
+                it.ws[m] = s.W.s + row * (cols / 32);
+            }
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-        const int k = min(first + q * L::kTokens + l.token, n - 1);
-        xo[q] = (uint32_t)(route ? route[k] : a.R + k) * (uint32_t)(a.ld * 2) + l.group * (L::kGroup * 2);
-    }
-    f32x4 acc[M][NT];
-    const int steps = W.cols / L::kStep;
-    few_product<MX, V, M, NT>(l, wp, ws, W.cols, reinterpret_cast<const uint8_t *>(a.act), xo, part * steps / a.S,
-                              (part + 1) * steps / a.S, acc);
+            for (int q = 0; q < NT; ++q)
+                it.xo[q] = (uint32_t)few_act_row(a, s.route, min(s.first + q * L::kTokens + l.token, s.n - 1)) * (uint32_t)(a.ld * 2) +
+                           l.group * (L::kGroup * 2);
+        },
+        [&](int i, const f32x4(&acc)[M][NT]) {
+            const FewSlice s = slice(i);
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-        const int k = q * L::kTokens + l.token;
+            for (int q = 0; q < NT; ++q) {
+                const int k = q * L::kTokens + l.token;
+                const bool in = s.first + k < s.n;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-            few_sums<V>(acc[m][q], [&](int r, float v) {
-                if (first + k < n) y[k * 8 * B + m * L::kRows + r] = v;
-            });
-    }
+                for (int m = 0; m < M; ++m)
+                    few_sums<V>(acc[m][q], [&](int r, float v) {
+                        if (in) s.y[k * 8 * B + m * L::kRows + r] = v;
+                    });
+            }
+        });
 }
 
+// An item with any number of routes, 64 at a time.
 template <bool MX, int B>
-__device__ __forceinline__ void few_down_unit(const FewArgs &a, const FewMatrix &W, int h0, const int *route, int first, int n, int part,
-                                              float *y) {
-    if (n - first <= 8) return few_down_pass<MX, 2, B, 1>(a, W, h0, route, first, n, part, y);
-    if (n - first <= 16) return few_down_pass<MX, 2, B, 2>(a, W, h0, route, first, n, part, y);
-    for (; first < n; first += 64, y += 64 * 8 * B) {
-        if (n - first <= 32)
-            few_down_pass<MX, 1, B, 2>(a, W, h0, route, first, n, part, y);
+__device__ __forceinline__ void few_down_wide(const FewArgs &a, int h0, int part, int S, FewSlice s) {
+    for (; s.first < s.n; s.first += 64, s.y += 64 * 8 * B) {
+        if (s.n - s.first <= 16)
+            few_down_run<MX, 2, B, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
+        else if (s.n - s.first <= 32)
+            few_down_run<MX, 1, B, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
         else
-            few_down_pass<MX, 1, B, 4>(a, W, h0, route, first, n, part, y);
+            few_down_run<MX, 1, B, 4>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
     }
 }
 
 // One workgroup per 8 B output columns.  Its waves form S parts of the
-// reduction dimension times 8 / S groups that take the experts in turn, so
-// each wave has its share of every expert's bytes; the routes (in expert
-// order, the shared expert's tokens after them) are taken `cap` places at a
-// time: their parts' sums (part[S][cap][8 B]) are added in part order into
-// y[place].  Then every output element adds its token's routes in ascending
-// slot order, the shared expert last, and is rounded once.
+// reduction dimension times 8 / S groups that take the experts in turn: with
+// many experts few parts (a wave then streams long stretches of a few experts),
+// with few experts many.  The routes (in expert order, the shared expert's
+// tokens after them) are taken in rounds of as many places as their parts' sums
+// have room; those are added in part order into y[place].  Then every output
+// element adds its token's routes in ascending slot order, the shared expert
+// last, and is rounded once.
 template <bool MX, int B>
 __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
     constexpr int C = 8 * B;
     const int t = threadIdx.x, wave = wave_uniform(t >> 6), h0 = blockIdx.x * C;
     const int rows = a.R + (a.Is ? a.T : 0);
     float *y = reinterpret_cast<float *>(lds), *sums = y + rows * C;
-    const FewPlan p(lds + rows * C + a.S * a.cap * C, a.L, a.R), src(a.plan + kFewHead, a.L, a.R);
+    const FewPlan p(lds + (rows + a.room) * C, a.L, a.R), src(a.plan + kFewHead, a.L, a.R);
     const int na = wave_uniform(a.plan[1]), n = wave_uniform(a.plan[2]);
     for (int i = t; i <= na; i += kFewThreads) {
         if (i < na) p.expert[i] = src.expert[i];
@@ -474,32 +564,55 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         p.place[i] = src.place[i];
     }
     __syncthreads();
-    const int part = wave % a.S, group = wave / a.S, groups = kFewWaves / a.S, all = n + (a.Is ? a.T : 0);
-    for (int base = 0; base < all; base += a.cap) {
-        const int end = min(base + a.cap, all);
-        for (int k = group; k < na + (a.Is ? 1 : 0); k += groups) {
-            // places [lo, hi) of expert k in this round (na: the shared expert)
-            const int off = k < na ? wave_uniform(p.off[k]) : n, past = k < na ? wave_uniform(p.off[k + 1]) : all;
-            const int lo = max(off, base), hi = min(past, end);
-            if (lo >= hi) continue;
-            float *dst = sums + (part * a.cap + lo - base) * C;
-            if (k < na) {
-                const int64_t row = (int64_t)wave_uniform(p.expert[k]) * a.H;
-                const FewMatrix W{static_cast<const uint8_t *>(a.W2) + row * a.I * (MX ? 1 : 2), MX ? a.W2s + row * (a.I / 32) : nullptr,
-                                  a.I};
-                few_down_unit<MX, B>(a, W, h0, p.route + off, lo - off, hi - off, part, dst);
-            } else {
-                const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S2), nullptr, a.Is};
-                few_down_unit<false, B>(a, W, h0, nullptr, lo - off, hi - off, part, dst);
-            }
-        }
+    // the sums of places [base, end) from S parts
+    auto join = [&](int base, int end, int S, int cap) {
         __syncthreads();
         for (int i = t; i < (end - base) * C; i += kFewThreads) {
             float v = 0.f;
-            for (int s = 0; s < a.S; ++s) v += sums[s * a.cap * C + i];
+            for (int s = 0; s < S; ++s) v += sums[s * cap * C + i];
             y[base * C + i] = v;
         }
         __syncthreads();
+    };
+    if (a.Is) {  // every token's column: all waves share it
+        const int S = few_parts(a.Is, kFewWaves), cap = a.room / S;
+        const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S2), nullptr, a.Is};
+        for (int base = 0; base < a.T; base += cap) {
+            const int end = min(base + cap, a.T);
+            if (wave < S) {
+                const FewSlice s{W, nullptr, base, end, sums + wave * cap * C};
+                if (end - base <= 8)
+                    few_down_run<false, 2, B, 1>(a, h0, a.Is, wave, S, 1, [&](int) { return s; });
+                else
+                    few_down_wide<false, B>(a, h0, wave, S, s);
+            }
+            join(n + base, n + end, S, cap);
+        }
+    }
+    int S = few_parts(a.I, kFewWaves);
+    while (S > 1 && na * S >= 16 * kFewWaves) S /= 2;
+    const int part = wave % S, group = wave / S, groups = kFewWaves / S, cap = a.room / S;
+    const int wide = wave_uniform(a.plan[3]), mid = wave_uniform(a.plan[4]);
+    for (int base = 0, from = 0; base < n; base += cap) {
+        // the experts [from, to) have places in [base, end); the first and the last may have others too
+        const int end = min(base + cap, n);
+        while (wave_uniform(p.off[from + 1]) <= base) ++from;
+        int to = from + 1;
+        while (wave_uniform(p.off[to]) < end) ++to;
+        auto slice = [&](int k) {
+            const int off = wave_uniform(p.off[k]), lo = max(off, base), hi = min(wave_uniform(p.off[k + 1]), end);
+            const int64_t row = (int64_t)wave_uniform(p.expert[k]) * a.H;
+            return FewSlice{{static_cast<const uint8_t *>(a.W2) + row * a.I * (MX ? 1 : 2), MX ? a.W2s + row * (a.I / 32) : nullptr, a.I},
+                            p.route + off, lo - off, hi - off, sums + (part * cap + lo - base) * C};
+        };
+        int k = from + group;
+        for (; k < min(wide, to); k += groups) few_down_wide<MX, B>(a, h0, part, S, slice(k));
+        const int nmid = k < min(mid, to) ? (min(mid, to) - k + groups - 1) / groups : 0;
+        few_down_run<MX, 2, B, 2>(a, h0, a.I, part, S, nmid, [&](int i) { return slice(k + i * groups); });
+        k += nmid * groups;
+        const int nlow = k < to ? (to - k + groups - 1) / groups : 0;
+        few_down_run<MX, 2, B, 1>(a, h0, a.I, part, S, nlow, [&](int i) { return slice(k + i * groups); });
+        join(base, end, S, cap);
     }
     for (int i = t; i < a.T * C; i += kFewThreads) {
         const int tok = i / C, h = i % C;

@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kFwdThreads) void k_wgrad(WgradArgs a, WindowCombin
 }
 
 template <bool MX>
-__global__ __launch_bounds__(kFewThreads, 4) void k_few_gateup(FewArgs a) {
+__global__ __launch_bounds__(kFewThreads, 2) void k_few_gateup(FewArgs a) {
     extern __shared__ __attribute__((aligned(16))) int32_t few_smem[];
     few_gateup_body<MX>(a, few_smem);
 }
@@ -1648,20 +1648,19 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     a.plan = static_cast<int32_t *>(ws);
     a.act = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + few_plan_bytes(d));
     const int rows = few_rows(d, Is);
-    // down launch: parts of at least 256 elements of the smaller reduction
-    // dimension, a power of two; 32 KiB of LDS for the parts' sums, less where
-    // the sums of all rows leave less
-    const int inner = Is > 0 ? std::min(d->I, Is) : d->I, C = 16;
-    a.S = inner >= 2048 ? 8 : inner >= 1024 ? 4 : inner >= 512 ? 2 : 1;
-    const int room = (int)(kMaxLds / 4) - few_down_words(a.L, a.R, rows, a.S, 0, C);
-    a.cap = std::min(rows, std::min(8192, room) / (a.S * C));
+    // down launch: 32 KiB of LDS for the parts' sums of a round, less where the
+    // sums of all rows leave less
+    constexpr int C = 16;
+    const int left = (int)(kMaxLds / 4) - few_down_words(a.L, a.R, rows, 0, C);
+    a.room = std::min(8192, left) / C;
     const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R);
-    const size_t lds_down = 4 * (size_t)few_down_words(a.L, a.R, rows, a.S, a.cap, C);
-    if (a.cap < 1 || lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
+    if (a.room < kFewWaves || lds_gu > kMaxLds) return MOE_EUNSUPPORTED;
+    a.room = std::min(a.room, rows * kFewWaves);
+    const size_t lds_down = 4 * (size_t)few_down_words(a.L, a.R, rows, a.room, C);
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + Is / kFewRows;
     {
         TraceScope tr("few_gateup", s);
-        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, 2ll * device_cus())), dim3(kFewThreads),
+        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, device_cus())), dim3(kFewThreads),
                            lds_gu, s, a);
     }
     if (launch_status() != MOE_OK) return MOE_EHIP;
