@@ -32,7 +32,7 @@ constexpr int kFewWaves = 8;
 constexpr int kFewThreads = 64 * kFewWaves;
 constexpr int kFewMaxRoutes = 1024;  // routes of one call (P * Np * K)
 constexpr int kFewRows = 16;         // activation columns of a gate/up unit
-constexpr int kFewGateupRegs = 100;  // registers for a wave's sums and steps in flight
+constexpr int kFewGateupRegs = 200;  // registers for a wave's sums and steps in flight
 constexpr int kFewDownRegs = 48;
 
 struct FewArgs {
@@ -171,32 +171,33 @@ __device__ __forceinline__ void few_mx_frags(const u32x4 &c, uint32_t sbyte, bf1
     }
 }
 
-// How a wave's 64 x 16 bytes of weights lie in one load (and in one MFMA, whose
-// lane i + 16 g holds row or column i, group g of its operand):
-//   dense  (V = 1)  16 rows x 64 consecutive bytes: lane i + 16 g reads group g
-//                   of row i, a tile is 16 tokens;
-//   halves (V = 2)  8 rows x 128 consecutive bytes: lane i + 16 g reads group
-//                   4 (i & 1) + g of row i / 2, a tile is 8 tokens laid out
-//                   alike.  MFMA row (r, p) times column (c, q) is then row r
-//                   half p times token c half q: the wanted sum is the p = q
-//                   entries of both halves, the other half of the products is
-//                   dropped.
-// Whole 128-byte lines are worth it: a kernel that only reads gets 7.1 TB/s
-// with 128 (or 256) bytes of a row per load and 5.5 TB/s with 64.  The dropped
-// products cost nothing while the matrix cores wait for HBM, but a tile holds
-// half the tokens, so more than 16 routes of an expert take the dense form.
+// A step takes 128 consecutive bytes of every weight row of a block (64 bf16
+// elements or 128 codes of the reduction dimension): eight 16-byte groups, of
+// which the MFMA's lane i + 16 g (row or column i, group g of its operand) takes
+//   dense  (V = 1)  groups g and 4 + g of row i, in two loads and two MFMAs:
+//                   blocks of 16 rows, tiles of 16 tokens;
+//   halves (V = 2)  group 4 (i & 1) + g of row i / 2, in one: blocks of 8 rows,
+//                   tiles of 8 tokens laid out alike.  MFMA row (r, p) times
+//                   column (c, q) is then row r half p times token c half q: the
+//                   wanted sum is the p = q entries of both halves, the other
+//                   half of the products is dropped.
+// Whole 128-byte lines in one load are worth it: a kernel that only reads gets
+// 7.1 TB/s with 128 (or 256) bytes of a row per load and 5.5 TB/s with 64.  The
+// dropped products cost nothing while the matrix cores wait for HBM, but a tile
+// holds half the tokens, so more than 16 routes of an expert take the dense form.
 template <bool MX, int V>
 struct FewLane {
-    int row, group, token;  // of the weights' block; 16-byte group of a row; of a tile
+    static constexpr int kLoads = 2 / V;                // loads of a block's (or tile's) step
+    static constexpr int kTokens = 16 / V;              // tokens of a tile
+    static constexpr int kRows = 16 / V;                // rows of a block
+    static constexpr int kStep = MX ? 128 : 64;         // elements of the reduction dimension per step
+    static constexpr int kGroup = MX ? 16 : 8;          // elements of a group
+    int row, group, token;  // of the block; the first load's group (the second: 4 more); of the tile
     __device__ __forceinline__ FewLane() {
         const int lane = lane_id(), i = lane & 15, g = lane >> 4;
         row = token = i / V;
         group = V == 2 ? 4 * (i & 1) + g : g;
     }
-    static constexpr int kTokens = 16 / V;
-    static constexpr int kRows = 16 / V;                    // rows of a block
-    static constexpr int kStep = V * (MX ? 64 : 32);        // elements of the reduction dimension per step
-    static constexpr int kGroup = MX ? 16 : 8;              // elements of a group
 };
 
 // A weight matrix of an expert: rows of `cols` elements, bf16 or MX (codes p,
@@ -206,56 +207,90 @@ struct FewMatrix {
     int cols;
 };
 
-// One step's operands: M blocks of weight rows and NT tiles of tokens.  With
-// MX, the first MFMA takes each group's first 8 codes and the second its last
-// 8; both operands use the same order, so the sum is over the same elements.
-template <bool MX, int V, int M, int NT>
-struct FewStep {
-    u32x4 w[M];
-    uint32_t sb[M];
-    bf16x8 x[NT][MX ? 2 : 1];
+// Raw buffer over [base, base + bytes) (base wave-uniform; word 3 as for every
+// raw buffer on gfx9 parts): a load's address is the lane's 32-bit offset plus a
+// wave-uniform one, so the streams below need no vector arithmetic for it.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 few_load16(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
+}
+__device__ __forceinline__ u32x4 few_load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 2));  // 2: nontemporal
+}
+constexpr uint32_t kFewBytes = 0x7fffffffu;  // the host keeps every offset below
 
-    // wp[m], ws[m]: block m's first row at the step's first element (wave-
-    // uniform), wo / so this lane's bytes from there; xb the tokens' matrix at
-    // the step's first element, xo[t] this lane's bytes from there
-    __device__ __forceinline__ void load(const uint8_t *const (&wp)[M], const uint8_t *const (&ws)[M], uint32_t wo, uint32_t so,
-                                         const uint8_t *xb, const uint32_t (&xo)[NT], int k) {
-        using L = FewLane<MX, V>;
-        const uint8_t *xk = xb + (int64_t)k * L::kStep * 2;
+// Where an item's operands start: its M blocks of weight rows, G runs of
+// consecutive blocks each from wp[.] / ws[.] (wave-uniform) on, and this lane's
+// token of each tile (bytes from the tokens' matrix).
+template <int G, int NT>
+struct FewItem {
+    const uint8_t *wp[G], *ws[G];
+    uint32_t xo[NT];
+};
+
+// What the steps of a run of items share: the tokens' matrix, bytes of a weight
+// row and of its scale bytes, and this lane's bytes from a block's first row.
+struct FewRun {
+    __amdgpu_buffer_rsrc_t tokens;
+    uint32_t row, srow, wo, so;
+    template <bool MX, int V>
+    __device__ __forceinline__ static FewRun make(const FewLane<MX, V> &l, int cols, const void *tokens) {
+        const uint32_t row = (uint32_t)cols * (MX ? 1 : 2), srow = (uint32_t)cols / 32;
+        return {few_rsrc(tokens, kFewBytes), row, srow, l.row * row + l.group * 16, l.row * srow};
+    }
+};
+
+// One step's operands: M blocks of weight rows and NT tiles of tokens.  With
+// MX a load's 16 codes take two MFMAs, the first for each group's first 8 codes;
+// both operands use the same order, so the sum is over the same elements.
+template <bool MX, int V, int M, int G, int NT>
+struct FewStep {
+    using L = FewLane<MX, V>;
+    static constexpr int N = L::kLoads, X = MX ? 2 : 1;  // 16-byte loads of 8 elements of a token's group
+    u32x4 w[M][N];
+    uint32_t sb[M];
+    u32x4 x[NT][N][X];
+
+    __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k) {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            w[m] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[m] + (int64_t)k * V * 64 + wo));
-            if constexpr (MX && V == 2) sb[m] = *reinterpret_cast<const uint32_t *>(ws[m] + (int64_t)k * 4 + so);
-            if constexpr (MX && V == 1) sb[m] = *reinterpret_cast<const uint16_t *>(ws[m] + (int64_t)k * 2 + so);
+            constexpr int per = M / G;
+            const __amdgpu_buffer_rsrc_t b = few_rsrc(it.wp[m / per], kFewBytes);
+#pragma unroll
+            for (int h = 0; h < N; ++h)
+                w[m][h] = few_load16_nt(b, r.wo + 64 * h, (m % per) * L::kRows * r.row + k * 128);
+            if constexpr (MX)
+                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], kFewBytes), r.so,
+                                                             (m % per) * L::kRows * r.srow + k * 4, 0);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < (MX ? 2 : 1); ++h) x[t][h] = *reinterpret_cast<const bf16x8 *>(xk + xo[t] + 16 * h);
+            for (int h = 0; h < N; ++h)
+#pragma unroll
+                for (int e = 0; e < X; ++e)
+                    x[t][h][e] = few_load16(r.tokens, it.xo[t] + (4 * h * X + e) * 16, k * (L::kStep * 2));
     }
-    __device__ __forceinline__ void mul(const FewLane<MX, V> &l, f32x4 (&acc)[M][NT]) const {
+    __device__ __forceinline__ void mul(const L &l, f32x4 (&acc)[M][NT]) const {
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            bf16x8 f[2];
-            if constexpr (MX)
-                few_mx_frags(w[m], (sb[m] >> (8 * (l.group >> 1))) & 0xffu, f[0], f[1]);
-            else
-                f[0] = __builtin_bit_cast(bf16x8, w[m]);
+        for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int h = 0; h < N; ++h) {
+                bf16x8 f[2];
+                if constexpr (MX)
+                    few_mx_frags(w[m][h], (sb[m] >> (8 * ((l.group + 4 * h) >> 1))) & 0xffu, f[0], f[1]);
+                else
+                    f[0] = __builtin_bit_cast(bf16x8, w[m][h]);
 #pragma unroll
-                for (int h = 0; h < (MX ? 2 : 1); ++h)
-                    acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], x[t][h], acc[m][t], 0, 0, 0);
-        }
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < X; ++e)
+                        acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[e], __builtin_bit_cast(bf16x8, x[t][h][e]),
+                                                                            acc[m][t], 0, 0, 0);
+            }
     }
-};
-
-// Where an item's operands start: its M blocks of weight rows (wave-uniform
-// pointers) and this lane's token of each tile (bytes from the tokens' matrix).
-template <int M, int NT>
-struct FewItem {
-    const uint8_t *wp[M], *ws[M];
-    uint32_t xo[NT];
 };
 
 // Streams `items` products through one wave: for each, block m's rows times
@@ -264,18 +299,19 @@ struct FewItem {
 // a step's registers are loaded again as soon as they are used, the last ones of
 // an item with the first steps of the next, so the wave's loads never run dry
 // between items.
-template <bool MX, int V, int M, int NT, int D, class Item, class Emit>
-__device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, int cols, const void *tokens, int k0, int n, int items, Item item,
-                                           Emit emit) {
+// The scheduling barriers keep the loads where they are written: left alone,
+// the compiler moves them next to their use.
+template <bool MX, int V, int M, int G, int NT, int D, class Item, class Emit>
+__device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, const FewRun &r, int k0, int n, int items, Item item, Emit emit) {
     if (items <= 0) return;
-    const uint32_t wo = (uint32_t)(l.row * cols * (MX ? 1 : 2) + l.group * 16), so = (uint32_t)(l.row * (cols / 32));
-    const uint8_t *xb = static_cast<const uint8_t *>(tokens);
-    FewStep<MX, V, M, NT> st[D];
-    FewItem<M, NT> cur, next;
+    FewStep<MX, V, M, G, NT> st[D];
+    FewItem<G, NT> cur, next;
     item(0, cur);
 #pragma unroll
-    for (int j = 0; j < D; ++j)
-        if (j < n) st[j].load(cur.wp, cur.ws, wo, so, xb, cur.xo, k0 + j);
+    for (int j = 0; j < D; ++j) {
+        if (j < n) st[j].load(r, cur, k0 + j);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     for (int it = 0; it < items; ++it) {
         const bool more = it + 1 < items;
         if (more) item(it + 1, next);
@@ -289,23 +325,29 @@ __device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, int cols, co
 #pragma unroll
             for (int j = 0; j < D; ++j) {
                 st[j].mul(l, acc);
-                st[j].load(cur.wp, cur.ws, wo, so, xb, cur.xo, k0 + k + D + j);
+                __builtin_amdgcn_sched_barrier(0);
+                st[j].load(r, cur, k0 + k + D + j);
+                __builtin_amdgcn_sched_barrier(0);
             }
         // fewer than 2 D steps are left, the first D of them in flight
 #pragma unroll
         for (int j = 0; j < D; ++j)
             if (k + j < n) {
                 st[j].mul(l, acc);
+                __builtin_amdgcn_sched_barrier(0);
                 if (k + D + j < n)
-                    st[j].load(cur.wp, cur.ws, wo, so, xb, cur.xo, k0 + k + D + j);
+                    st[j].load(r, cur, k0 + k + D + j);
                 else if (more)
-                    st[j].load(next.wp, next.ws, wo, so, xb, next.xo, k0 + j);
+                    st[j].load(r, next, k0 + j);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
         for (int j = 0; j < D; ++j)
             if (k + D + j < n) {
                 st[j].mul(l, acc);
-                if (more) st[j].load(next.wp, next.ws, wo, so, xb, next.xo, k0 + j);
+                __builtin_amdgcn_sched_barrier(0);
+                if (more) st[j].load(r, next, k0 + j);
+                __builtin_amdgcn_sched_barrier(0);
             }
         emit(it, acc);
         cur = next;
@@ -313,9 +355,9 @@ __device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, int cols, co
 }
 
 // Steps in flight that fit `regs` registers beside the sums.
-template <bool MX, int M, int NT>
+template <bool MX, int V, int M, int NT>
 constexpr int few_depth(int regs) {
-    const int per = (MX ? 5 : 4) * M + (MX ? 8 : 4) * NT, d = (regs - 4 * M * NT) / per;
+    const int n = 4 * FewLane<MX, V>::kLoads, per = (n + (MX ? 1 : 0)) * M + n * (MX ? 2 : 1) * NT, d = (regs - 4 * M * NT) / per;
     return d < 1 ? 1 : d > 8 ? 8 : d;
 }
 
@@ -354,13 +396,13 @@ __device__ __forceinline__ int few_act_row(const FewArgs &a, const int *route, i
 // Operands of a unit's routes from `first` on: V gate blocks, V up blocks.
 template <bool MX, int V, int NT>
 __device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX, V> &l,
-                                                FewItem<2 * V, NT> &it) {
+                                                FewItem<2, NT> &it) {
     using L = FewLane<MX, V>;
 #pragma unroll
-    for (int m = 0; m < 2 * V; ++m) {
-        const int64_t row = (m < V ? 0 : u.inner) + u.i0 + (m % V) * L::kRows;
-        it.wp[m] = u.W.p + row * u.W.cols * (MX ? 1 : 2);
-        it.ws[m] = u.W.s + row * (u.W.cols / 32);
+    for (int g = 0; g < 2; ++g) {
+        const int64_t row = (int64_t)g * u.inner + u.i0;
+        it.wp[g] = u.W.p + row * u.W.cols * (MX ? 1 : 2);
+        it.ws[g] = u.W.s + row * (u.W.cols / 32);
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q)
@@ -408,8 +450,8 @@ __device__ __forceinline__ void few_gateup_run(const FewArgs &a, int count, int 
     const L l;
     const int wave = wave_uniform(threadIdx.x >> 6), steps = a.H / L::kStep;
     const int k0 = wave * steps / kFewWaves, n = (wave + 1) * steps / kFewWaves - k0;
-    few_stream<MX, V, 2 * V, NT, few_depth<MX, 2 * V, NT>(kFewGateupRegs)>(
-        l, a.H, a.X, k0, n, count, [&](int i, FewItem<2 * V, NT> &it) { few_gateup_item<MX, V, NT>(a, unit(i), first, l, it); },
+    few_stream<MX, V, 2 * V, 2, NT, few_depth<MX, V, 2 * V, NT>(kFewGateupRegs)>(
+        l, FewRun::make(l, a.H, a.X), k0, n, count, [&](int i, FewItem<2, NT> &it) { few_gateup_item<MX, V, NT>(a, unit(i), first, l, it); },
         [&](int i, const f32x4(&acc)[2 * V][NT]) { few_gateup_join<MX, V, NT>(a, unit(i), first, l, acc, red); });
 }
 
@@ -471,11 +513,12 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
     few_gateup_run<MX, 2, 1>(a, nlow, 0, [&](int i) { return routed(u + i * step); }, red);
 }
 
-// Parts of a reduction dimension of `inner` elements: at least 256 each, a
-// power of two up to `most`.
-__host__ __device__ inline int few_parts(int inner, int most) {
-    int S = most;
-    while (S > 1 && inner < 256 * S) S /= 2;
+// Parts of a reduction dimension of `inner` elements: at least 512 bytes of a
+// row each, a power of two up to the waves.
+template <bool MX>
+__device__ __forceinline__ int few_parts(int inner) {
+    int S = kFewWaves;
+    while (S > 1 && inner < (MX ? 512 : 256) * S) S /= 2;
     return S;
 }
 
@@ -496,16 +539,12 @@ __device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols,
     constexpr int M = B * V / 2;
     const L l;
     const int steps = cols / L::kStep, k0 = part * steps / S, n = (part + 1) * steps / S - k0;
-    few_stream<MX, V, M, NT, few_depth<MX, M, NT>(kFewDownRegs)>(
-        l, cols, a.act, k0, n, count,
-        [&](int i, FewItem<M, NT> &it) {
+    few_stream<MX, V, M, 1, NT, few_depth<MX, V, M, NT>(kFewDownRegs)>(
+        l, FewRun::make(l, cols, a.act), k0, n, count,
+        [&](int i, FewItem<1, NT> &it) {
             const FewSlice s = slice(i);
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const int64_t row = h0 + m * L::kRows;
-                it.wp[m] = s.W.p + row * cols * (MX ? 1 : 2);
-                it.ws[m] = s.W.s + row * (cols / 32);
-            }
+            it.wp[0] = s.W.p + (int64_t)h0 * cols * (MX ? 1 : 2);
+            it.ws[0] = s.W.s + (int64_t)h0 * (cols / 32);
 #pragma unroll
             for (int q = 0; q < NT; ++q)
                 it.xo[q] = (uint32_t)few_act_row(a, s.route, min(s.first + q * L::kTokens + l.token, s.n - 1)) * (uint32_t)(a.ld * 2) +
@@ -526,10 +565,15 @@ __device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols,
         });
 }
 
-// An item with any number of routes, 64 at a time.
+// An item with any number of routes: 64 at a time with 16 columns, 16 with 8.
 template <bool MX, int B>
 __device__ __forceinline__ void few_down_wide(const FewArgs &a, int h0, int part, int S, FewSlice s) {
-    for (; s.first < s.n; s.first += 64, s.y += 64 * 8 * B) {
+    if constexpr (B == 1) {
+        for (; s.first < s.n; s.first += 16, s.y += 16 * 8)
+            few_down_run<MX, 2, 1, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
+        return;
+    }
+    else for (; s.first < s.n; s.first += 64, s.y += 64 * 8 * B) {
         if (s.n - s.first <= 16)
             few_down_run<MX, 2, B, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
         else if (s.n - s.first <= 32)
@@ -554,15 +598,9 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
     const int rows = a.R + (a.Is ? a.T : 0);
     float *y = reinterpret_cast<float *>(lds), *sums = y + rows * C;
     const FewPlan p(lds + (rows + a.room) * C, a.L, a.R), src(a.plan + kFewHead, a.L, a.R);
+    // the whole list, entries past its counts too (never used), so that no load waits for the counts
+    for (int i = t; i < few_plan_words(a.L, a.R) - kFewHead; i += kFewThreads) p.expert[i] = src.expert[i];
     const int na = wave_uniform(a.plan[1]), n = wave_uniform(a.plan[2]);
-    for (int i = t; i <= na; i += kFewThreads) {
-        if (i < na) p.expert[i] = src.expert[i];
-        p.off[i] = src.off[i];
-    }
-    for (int i = t; i < a.R; i += kFewThreads) {
-        if (i < n) p.route[i] = src.route[i];
-        p.place[i] = src.place[i];
-    }
     __syncthreads();
     // the sums of places [base, end) from S parts
     auto join = [&](int base, int end, int S, int cap) {
@@ -575,7 +613,7 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         __syncthreads();
     };
     if (a.Is) {  // every token's column: all waves share it
-        const int S = few_parts(a.Is, kFewWaves), cap = a.room / S;
+        const int S = few_parts<false>(a.Is), cap = a.room / S;
         const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S2), nullptr, a.Is};
         for (int base = 0; base < a.T; base += cap) {
             const int end = min(base + cap, a.T);
@@ -589,7 +627,7 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
             join(n + base, n + end, S, cap);
         }
     }
-    int S = few_parts(a.I, kFewWaves);
+    int S = few_parts<MX>(a.I);
     while (S > 1 && na * S >= 16 * kFewWaves) S /= 2;
     const int part = wave % S, group = wave / S, groups = kFewWaves / S, cap = a.room / S;
     const int wide = wave_uniform(a.plan[3]), mid = wave_uniform(a.plan[4]);
@@ -597,8 +635,9 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         // the experts [from, to) have places in [base, end); the first and the last may have others too
         const int end = min(base + cap, n);
         while (wave_uniform(p.off[from + 1]) <= base) ++from;
-        int to = from + 1;
-        while (wave_uniform(p.off[to]) < end) ++to;
+        int to = na;
+        if (end < n)
+            for (to = from + 1; wave_uniform(p.off[to]) < end;) ++to;
         auto slice = [&](int k) {
             const int off = wave_uniform(p.off[k]), lo = max(off, base), hi = min(wave_uniform(p.off[k + 1]), end);
             const int64_t row = (int64_t)wave_uniform(p.expert[k]) * a.H;

@@ -1621,8 +1621,8 @@ int few_check(const moe_desc *d, int32_t Is) {
     if (d->num_batches != 1 || Is < 0) return MOE_EINVAL;
     if ((int64_t)d->P * d->Np * d->K > kFewMaxRoutes) return MOE_EUNSUPPORTED;
     if (Is % 128 || 768ll * Is >= (1ll << 30)) return MOE_EUNSUPPORTED;
-    // X, the activations and 16 rows of weights are addressed with 32-bit byte offsets
-    if (2ll * d->P * d->Np * d->H >= (1ll << 32) || 2ll * few_rows(d, Is) * std::max(d->I, Is) >= (1ll << 32) ||
+    // X, the activations and 16 rows of weights are addressed with byte offsets below 2 GiB
+    if (2ll * d->P * d->Np * d->H >= (1ll << 31) || 2ll * few_rows(d, Is) * std::max(d->I, Is) >= (1ll << 31) ||
         32ll * std::max(d->H, std::max(d->I, Is)) >= (1ll << 31))
         return MOE_EUNSUPPORTED;
     return MOE_OK;
@@ -1648,9 +1648,10 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     a.plan = static_cast<int32_t *>(ws);
     a.act = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + few_plan_bytes(d));
     const int rows = few_rows(d, Is);
-    // down launch: 32 KiB of LDS for the parts' sums of a round, less where the
-    // sums of all rows leave less
-    constexpr int C = 16;
+    // down launch: 16 output columns a workgroup, 8 where that leaves CUs without
+    // one; 32 KiB of LDS for the parts' sums of a round, less where the sums of
+    // all rows leave less
+    const int C = a.H / 16 < device_cus() ? 8 : 16;
     const int left = (int)(kMaxLds / 4) - few_down_words(a.L, a.R, rows, 0, C);
     a.room = std::min(8192, left) / C;
     const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R);
@@ -1660,12 +1661,13 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + Is / kFewRows;
     {
         TraceScope tr("few_gateup", s);
-        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, device_cus())), dim3(kFewThreads),
-                           lds_gu, s, a);
+        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, device_cus())), dim3(kFewThreads), lds_gu,
+                           s, a);
     }
     if (launch_status() != MOE_OK) return MOE_EHIP;
     TraceScope tr("few_down", s);
-    hipLaunchKernelGGL((k_few_down<MX, 2>), dim3(a.H / C), dim3(kFewThreads), lds_down, s, a);
+    auto *down = C == 8 ? k_few_down<MX, 1> : k_few_down<MX, 2>;
+    hipLaunchKernelGGL(down, dim3(a.H / C), dim3(kFewThreads), lds_down, s, a);
     return launch_status();
 }
 
