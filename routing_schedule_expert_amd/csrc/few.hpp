@@ -33,7 +33,14 @@ constexpr int kFewThreads = 64 * kFewWaves;
 constexpr int kFewMaxRoutes = 1024;  // routes of one call (P * Np * K)
 constexpr int kFewRows = 16;         // activation columns of a gate/up unit
 constexpr int kFewGateupRegs = 200;  // registers for a wave's sums and steps in flight
-constexpr int kFewDownRegs = 48;
+// Down launch, B blocks of 8 output columns a workgroup: its waves, and the
+// registers as above.  Two workgroups of four waves per CU with twice the loads
+// in flight beat two of eight at 16 columns (MX down of 24 experts: 62 us against
+// 100); at 8 columns there is one workgroup per CU, which takes eight waves (48 us
+// against 62 for 64 experts of H = 2048, I = 1024).
+constexpr int few_down_waves(int B) { return B == 1 ? 8 : 4; }
+constexpr int few_down_threads(int B) { return 64 * few_down_waves(B); }
+constexpr int few_down_regs(int B) { return B == 1 ? 88 : 120; }
 
 struct FewArgs {
     const int32_t *routes;
@@ -45,7 +52,7 @@ struct FewArgs {
     uint16_t *out, *act;
     int32_t *plan;
     int T, K, R, E, L, base, H, I, Is, ld;  // ld: elements of an activation row, max(I, Is)
-    int room;                               // down: places (times parts) of a round
+    int words;                              // down: words of LDS for sums
 };
 
 // The list of a call's local routes grouped by expert, in the workspace
@@ -72,16 +79,14 @@ struct FewPlan {
 };
 
 // Words of LDS of the gate/up launch: the waves' sums, one count per local
-// expert, 8 words for the head, and the list; and of the down launch: the
-// routes' sums and the list.
+// expert, 8 words for the head, and the list.
 constexpr int kFewRedLd = 36;  // 32 sums of a column and 4 words that spread the columns over the banks
 constexpr int kFewRedWords = kFewWaves * 32 * kFewRedLd;
 __host__ __device__ inline int few_gateup_words(int L, int R) {
     return kFewRedWords + L + 8 + few_plan_words(L, R) - kFewHead;
 }
-__host__ __device__ inline int few_down_words(int L, int R, int rows, int room, int C) {
-    return (rows + room) * C + few_plan_words(L, R) - kFewHead;
-}
+// The list in the down launch's LDS: numbers of routes and places in 16 bits.
+__host__ __device__ inline int few_list_words(int L, int R) { return 2 * few_max_experts(L, R) + 1 + R; }
 
 // Builds the list in LDS: count the routes of each expert (a route's rank is
 // the order in which the LDS atomics answer: it only says which MFMA column
@@ -201,9 +206,9 @@ struct FewLane {
 };
 
 // A weight matrix of an expert: rows of `cols` elements, bf16 or MX (codes p,
-// scale bytes s).
+// scale bytes s; the array that holds them ends at s_end).
 struct FewMatrix {
-    const uint8_t *p, *s;
+    const uint8_t *p, *s, *s_end;
     int cols;
 };
 
@@ -227,7 +232,16 @@ constexpr uint32_t kFewBytes = 0x7fffffffu;  // the host keeps every offset belo
 template <int G, int NT>
 struct FewItem {
     const uint8_t *wp[G], *ws[G];
+    uint32_t s_bytes[G];  // from ws[.] to the end of the scale bytes
     uint32_t xo[NT];
+    template <bool MX>
+    __device__ __forceinline__ void rows(int g, const FewMatrix &W, int64_t row) {
+        wp[g] = W.p + row * W.cols * (MX ? 1 : 2);
+        if constexpr (MX) {
+            ws[g] = W.s + row * (W.cols / 32);
+            s_bytes[g] = (uint32_t)min(W.s_end - ws[g], (ptrdiff_t)kFewBytes);
+        }
+    }
 };
 
 // What the steps of a run of items share: the tokens' matrix, bytes of a weight
@@ -245,12 +259,13 @@ struct FewRun {
 // One step's operands: M blocks of weight rows and NT tiles of tokens.  With
 // MX a load's 16 codes take two MFMAs, the first for each group's first 8 codes;
 // both operands use the same order, so the sum is over the same elements.
-template <bool MX, int V, int M, int G, int NT>
+// (SC: the step loads its own scale bytes; otherwise they come from FewScales)
+template <bool MX, int V, int M, int G, int NT, bool SC>
 struct FewStep {
     using L = FewLane<MX, V>;
     static constexpr int N = L::kLoads, X = MX ? 2 : 1;  // 16-byte loads of 8 elements of a token's group
     u32x4 w[M][N];
-    uint32_t sb[M];
+    uint32_t sb[SC ? M : 1];
     u32x4 x[NT][N][X];
 
     __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k) {
@@ -261,8 +276,8 @@ struct FewStep {
 #pragma unroll
             for (int h = 0; h < N; ++h)
                 w[m][h] = few_load16_nt(b, r.wo + 64 * h, (m % per) * L::kRows * r.row + k * 128);
-            if constexpr (MX)
-                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], kFewBytes), r.so,
+            if constexpr (SC)
+                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so,
                                                              (m % per) * L::kRows * r.srow + k * 4, 0);
         }
 #pragma unroll
@@ -273,14 +288,16 @@ struct FewStep {
                 for (int e = 0; e < X; ++e)
                     x[t][h][e] = few_load16(r.tokens, it.xo[t] + (4 * h * X + e) * 16, k * (L::kStep * 2));
     }
-    __device__ __forceinline__ void mul(const L &l, f32x4 (&acc)[M][NT]) const {
+    // scale(m): block m's four scale bytes of this step
+    template <class Scale>
+    __device__ __forceinline__ void mul(const L &l, Scale scale, f32x4 (&acc)[M][NT]) const {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
             for (int h = 0; h < N; ++h) {
                 bf16x8 f[2];
                 if constexpr (MX)
-                    few_mx_frags(w[m][h], (sb[m] >> (8 * ((l.group + 4 * h) >> 1))) & 0xffu, f[0], f[1]);
+                    few_mx_frags(w[m][h], (scale(m) >> (8 * ((l.group + 4 * h) >> 1))) & 0xffu, f[0], f[1]);
                 else
                     f[0] = __builtin_bit_cast(bf16x8, w[m][h]);
 #pragma unroll
@@ -293,25 +310,77 @@ struct FewStep {
     }
 };
 
+// The scale bytes of four steps (512 codes) in one load per block: a load of
+// one step's four bytes per row costs as much address work as 128 bytes of the
+// row's codes (gate/up of 24 experts took 124 us with one such load per step
+// and block, 103 us without any).  A chunk may reach past its row, into bytes
+// that no step uses, but not past the array: the buffer's size ends there.
+template <int V, int M, int G>
+struct FewScales {
+    u32x4 v[M];
+    template <int NT>
+    __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k) {
+        constexpr int per = M / G;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            v[m] = few_load16(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so, (m % per) * (16 / V) * r.srow + k * 4);
+    }
+};
+
+// Steps in flight that fit `regs` registers beside the sums; with MX four and
+// the scale bytes of four steps where that fits.
+template <bool MX, int V, int M, int NT>
+constexpr int few_step_regs() {
+    return 4 * FewLane<MX, V>::kLoads * (M + (MX ? 2 : 1) * NT);
+}
+template <bool MX, int V, int M, int NT>
+constexpr bool few_chunked(int regs) {
+    return MX && 4 * few_step_regs<MX, V, M, NT>() + 8 * M + 4 * M * NT <= regs;
+}
+template <bool MX, int V, int M, int NT>
+constexpr int few_depth(int regs) {
+    if (few_chunked<MX, V, M, NT>(regs)) return 4;
+    const int d = (regs - 4 * M * NT) / (few_step_regs<MX, V, M, NT>() + (MX ? M : 0));
+    return d < 1 ? 1 : d > 8 ? 8 : d;
+}
+
 // Streams `items` products through one wave: for each, block m's rows times
 // tile t's tokens over the steps [k0, k0 + n) of the reduction dimension go to
 // emit(item, acc).  item(i) gives the operands' places.  D steps are in flight:
 // a step's registers are loaded again as soon as they are used, the last ones of
 // an item with the first steps of the next, so the wave's loads never run dry
-// between items.
+// between items. 
 // The scheduling barriers keep the loads where they are written: left alone,
 // the compiler moves them next to their use.
-template <bool MX, int V, int M, int G, int NT, int D, class Item, class Emit>
+template <bool MX, int V, int M, int G, int NT, int REGS, class Item, class Emit>
 __device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, const FewRun &r, int k0, int n, int items, Item item, Emit emit) {
     if (items <= 0) return;
-    FewStep<MX, V, M, G, NT> st[D];
+    constexpr bool chunks = few_chunked<MX, V, M, NT>(REGS), own = MX && !chunks;  // scale bytes: of four steps, of one
+    constexpr int D = few_depth<MX, V, M, NT>(REGS);
+    FewStep<MX, V, M, G, NT, own> st[D];
+    FewScales<V, chunks ? M : G, G> now, then;
     FewItem<G, NT> cur, next;
+    auto mul = [&](int j, f32x4(&acc)[M][NT]) {
+        st[j].mul(
+            l,
+            [&](int m) -> uint32_t {
+                if constexpr (chunks) return now.v[m][j & 3];
+                return st[j].sb[own ? m : 0];
+            },
+            acc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load = [&](int j, const FewItem<G, NT> &it, int step) {
+        st[j].load(r, it, k0 + step);
+        if constexpr (chunks)
+            if (j == 0) then.load(r, it, k0 + step);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     item(0, cur);
 #pragma unroll
-    for (int j = 0; j < D; ++j) {
-        if (j < n) st[j].load(r, cur, k0 + j);
-        __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int j = 0; j < D; ++j)
+        if (j < n) load(j, cur, j);
+    now = then;
     for (int it = 0; it < items; ++it) {
         const bool more = it + 1 < items;
         if (more) item(it + 1, next);
@@ -321,44 +390,37 @@ __device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, const FewRun
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         int k = 0;
-        for (; k + 2 * D <= n; k += D)
+        for (; k + 2 * D <= n; k += D) {
 #pragma unroll
             for (int j = 0; j < D; ++j) {
-                st[j].mul(l, acc);
-                __builtin_amdgcn_sched_barrier(0);
-                st[j].load(r, cur, k0 + k + D + j);
-                __builtin_amdgcn_sched_barrier(0);
+                mul(j, acc);
+                load(j, cur, k + D + j);
             }
+            now = then;
+        }
         // fewer than 2 D steps are left, the first D of them in flight
 #pragma unroll
         for (int j = 0; j < D; ++j)
             if (k + j < n) {
-                st[j].mul(l, acc);
-                __builtin_amdgcn_sched_barrier(0);
+                mul(j, acc);
                 if (k + D + j < n)
-                    st[j].load(r, cur, k0 + k + D + j);
+                    load(j, cur, k + D + j);
                 else if (more)
-                    st[j].load(r, next, k0 + j);
-                __builtin_amdgcn_sched_barrier(0);
+                    load(j, next, j);
             }
+        now = then;
+        if (k + D < n) {
 #pragma unroll
-        for (int j = 0; j < D; ++j)
-            if (k + D + j < n) {
-                st[j].mul(l, acc);
-                __builtin_amdgcn_sched_barrier(0);
-                if (more) st[j].load(r, next, k0 + j);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int j = 0; j < D; ++j)
+                if (k + D + j < n) {
+                    mul(j, acc);
+                    if (more) load(j, next, j);
+                }
+            now = then;
+        }
         emit(it, acc);
         cur = next;
     }
-}
-
-// Steps in flight that fit `regs` registers beside the sums.
-template <bool MX, int V, int M, int NT>
-constexpr int few_depth(int regs) {
-    const int n = 4 * FewLane<MX, V>::kLoads, per = (n + (MX ? 1 : 0)) * M + n * (MX ? 2 : 1) * NT, d = (regs - 4 * M * NT) / per;
-    return d < 1 ? 1 : d > 8 ? 8 : d;
 }
 
 // The sums of a block and tile that this lane keeps: row r(i) of the block and
@@ -391,7 +453,8 @@ struct FewUnit {
 };
 
 __device__ __forceinline__ int few_token(const FewArgs &a, const int *route, int k) { return route ? route[k] / a.K : k; }
-__device__ __forceinline__ int few_act_row(const FewArgs &a, const int *route, int k) { return route ? route[k] : a.R + k; }
+template <class T>
+__device__ __forceinline__ int few_act_row(const FewArgs &a, const T *route, int k) { return route ? (int)route[k] : a.R + k; }
 
 // Operands of a unit's routes from `first` on: V gate blocks, V up blocks.
 template <bool MX, int V, int NT>
@@ -399,11 +462,7 @@ __device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit 
                                                 FewItem<2, NT> &it) {
     using L = FewLane<MX, V>;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const int64_t row = (int64_t)g * u.inner + u.i0;
-        it.wp[g] = u.W.p + row * u.W.cols * (MX ? 1 : 2);
-        it.ws[g] = u.W.s + row * (u.W.cols / 32);
-    }
+    for (int g = 0; g < 2; ++g) it.template rows<MX>(g, u.W, (int64_t)g * u.inner + u.i0);
 #pragma unroll
     for (int q = 0; q < NT; ++q)
         it.xo[q] = (uint32_t)few_token(a, u.route, min(first + q * L::kTokens + l.token, u.n - 1)) * (uint32_t)(a.H * 2) +
@@ -450,7 +509,7 @@ __device__ __forceinline__ void few_gateup_run(const FewArgs &a, int count, int 
     const L l;
     const int wave = wave_uniform(threadIdx.x >> 6), steps = a.H / L::kStep;
     const int k0 = wave * steps / kFewWaves, n = (wave + 1) * steps / kFewWaves - k0;
-    few_stream<MX, V, 2 * V, 2, NT, few_depth<MX, V, 2 * V, NT>(kFewGateupRegs)>(
+    few_stream<MX, V, 2 * V, 2, NT, kFewGateupRegs>(
         l, FewRun::make(l, a.H, a.X), k0, n, count, [&](int i, FewItem<2, NT> &it) { few_gateup_item<MX, V, NT>(a, unit(i), first, l, it); },
         [&](int i, const f32x4(&acc)[2 * V][NT]) { few_gateup_join<MX, V, NT>(a, unit(i), first, l, acc, red); });
 }
@@ -494,12 +553,13 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
     auto routed = [&](int u) {  // unit u of the experts in the list's order
         const int k = u / blocks, off = wave_uniform(p.off[k]);
         const int64_t row = (int64_t)wave_uniform(p.expert[k]) * 2 * a.I;
-        return FewUnit{{static_cast<const uint8_t *>(a.W13) + row * a.H * (MX ? 1 : 2), MX ? a.W13s + row * (a.H / 32) : nullptr, a.H},
+        return FewUnit{{static_cast<const uint8_t *>(a.W13) + row * a.H * (MX ? 1 : 2), MX ? a.W13s + row * (a.H / 32) : nullptr,
+                        MX ? a.W13s + (int64_t)a.L * 2 * a.I * (a.H / 32) : nullptr, a.H},
                        a.I, u % blocks * kFewRows, wave_uniform(p.off[k + 1]) - off, p.route + off};
     };
     int u = blockIdx.x;
     for (; u < shared; u += step) {
-        const FewUnit s{{reinterpret_cast<const uint8_t *>(a.S13), nullptr, a.H}, a.Is, u * kFewRows, a.T, nullptr};
+        const FewUnit s{{reinterpret_cast<const uint8_t *>(a.S13), nullptr, nullptr, a.H}, a.Is, u * kFewRows, a.T, nullptr};
         if (a.T <= 8)
             few_gateup_run<false, 2, 1>(a, 1, 0, [&](int) { return s; }, red);
         else
@@ -516,8 +576,8 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
 // Parts of a reduction dimension of `inner` elements: at least 512 bytes of a
 // row each, a power of two up to the waves.
 template <bool MX>
-__device__ __forceinline__ int few_parts(int inner) {
-    int S = kFewWaves;
+__device__ __forceinline__ int few_parts(int inner, int waves) {
+    int S = waves;
     while (S > 1 && inner < (MX ? 512 : 256) * S) S /= 2;
     return S;
 }
@@ -526,7 +586,7 @@ __device__ __forceinline__ int few_parts(int inner) {
 // its routes [first, n), whose sums go to y[.. - first][8 B].
 struct FewSlice {
     FewMatrix W;
-    const int *route;
+    const uint16_t *route;
     int first, n;
     float *y;
 };
@@ -539,12 +599,11 @@ __device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols,
     constexpr int M = B * V / 2;
     const L l;
     const int steps = cols / L::kStep, k0 = part * steps / S, n = (part + 1) * steps / S - k0;
-    few_stream<MX, V, M, 1, NT, few_depth<MX, V, M, NT>(kFewDownRegs)>(
+    few_stream<MX, V, M, 1, NT, few_down_regs(B)>(
         l, FewRun::make(l, cols, a.act), k0, n, count,
         [&](int i, FewItem<1, NT> &it) {
             const FewSlice s = slice(i);
-            it.wp[0] = s.W.p + (int64_t)h0 * cols * (MX ? 1 : 2);
-            it.ws[0] = s.W.s + (int64_t)h0 * (cols / 32);
+            it.template rows<MX>(0, s.W, h0);
 #pragma unroll
             for (int q = 0; q < NT; ++q)
                 it.xo[q] = (uint32_t)few_act_row(a, s.route, min(s.first + q * L::kTokens + l.token, s.n - 1)) * (uint32_t)(a.ld * 2) +
@@ -584,28 +643,31 @@ __device__ __forceinline__ void few_down_wide(const FewArgs &a, int h0, int part
 }
 
 // One workgroup per 8 B output columns.  Its waves form S parts of the
-// reduction dimension times 8 / S groups that take the experts in turn: with
-// many experts few parts (a wave then streams long stretches of a few experts),
-// with few experts many.  The routes (in expert order, the shared expert's
-// tokens after them) are taken in rounds of as many places as their parts' sums
-// have room; those are added in part order into y[place].  Then every output
-// element adds its token's routes in ascending slot order, the shared expert
-// last, and is rounded once.
+// reduction dimension times waves / S groups that take the experts in turn.
+// One part is best (a wave then streams whole rows, and its sums go straight to
+// y[place], the routes in expert order and the shared expert's tokens after
+// them), as long as every wave gets at least four experts and none has over a
+// sixteenth more than its share; otherwise as few parts as do.  Parts' sums meet
+// in LDS, as many places a round as there is room for, and are added in part
+// order into y.  At the end every output element adds its token's routes in
+// ascending slot order, the shared expert last, and is rounded once.
 template <bool MX, int B>
 __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
-    constexpr int C = 8 * B;
+    constexpr int C = 8 * B, kWaves = few_down_waves(B), kThreads = few_down_threads(B);
     const int t = threadIdx.x, wave = wave_uniform(t >> 6), h0 = blockIdx.x * C;
-    const int rows = a.R + (a.Is ? a.T : 0);
-    float *y = reinterpret_cast<float *>(lds), *sums = y + rows * C;
-    const FewPlan p(lds + (rows + a.room) * C, a.L, a.R), src(a.plan + kFewHead, a.L, a.R);
+    int *expert = lds + a.words, *offset = expert + few_max_experts(a.L, a.R);
+    uint16_t *route = reinterpret_cast<uint16_t *>(offset + few_max_experts(a.L, a.R) + 1), *place = route + a.R;
+    const FewPlan src(a.plan + kFewHead, a.L, a.R);
     // the whole list, entries past its counts too (never used), so that no load waits for the counts
-    for (int i = t; i < few_plan_words(a.L, a.R) - kFewHead; i += kFewThreads) p.expert[i] = src.expert[i];
-    const int na = wave_uniform(a.plan[1]), n = wave_uniform(a.plan[2]);
+    for (int i = t; i < 2 * few_max_experts(a.L, a.R) + 1; i += kThreads) expert[i] = src.expert[i];
+    for (int i = t; i < 2 * a.R; i += kThreads) route[i] = (uint16_t)src.route[i];  // and the places: 65535 for none
+    const int na = wave_uniform(a.plan[1]), n = wave_uniform(a.plan[2]), all = n + (a.Is ? a.T : 0);
+    float *y = reinterpret_cast<float *>(lds), *sums = y + all * C;
+    const int room = a.words / C - all;
     __syncthreads();
-    // the sums of places [base, end) from S parts
-    auto join = [&](int base, int end, int S, int cap) {
+    auto join = [&](int base, int end, int S, int cap) {  // the sums of places [base, end)
         __syncthreads();
-        for (int i = t; i < (end - base) * C; i += kFewThreads) {
+        for (int i = t; i < (end - base) * C; i += kThreads) {
             float v = 0.f;
             for (int s = 0; s < S; ++s) v += sums[s * cap * C + i];
             y[base * C + i] = v;
@@ -613,36 +675,41 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         __syncthreads();
     };
     if (a.Is) {  // every token's column: all waves share it
-        const int S = few_parts<false>(a.Is), cap = a.room / S;
-        const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S2), nullptr, a.Is};
+        int S = few_parts<false>(a.Is, kWaves);
+        while (S > 1 && room < 8 * S) S /= 2;
+        const int cap = S > 1 ? room / S : a.T;
+        const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S2), nullptr, nullptr, a.Is};
         for (int base = 0; base < a.T; base += cap) {
             const int end = min(base + cap, a.T);
             if (wave < S) {
-                const FewSlice s{W, nullptr, base, end, sums + wave * cap * C};
+                const FewSlice s{W, nullptr, base, end, S > 1 ? sums + wave * cap * C : y + n * C};
                 if (end - base <= 8)
                     few_down_run<false, 2, B, 1>(a, h0, a.Is, wave, S, 1, [&](int) { return s; });
                 else
                     few_down_wide<false, B>(a, h0, wave, S, s);
             }
-            join(n + base, n + end, S, cap);
+            if (S > 1) join(n + base, n + end, S, cap);
         }
     }
-    int S = few_parts<MX>(a.I);
-    while (S > 1 && na * S >= 16 * kFewWaves) S /= 2;
-    const int part = wave % S, group = wave / S, groups = kFewWaves / S, cap = a.room / S;
+    const int most = few_parts<MX>(a.I, kWaves);
+    int S = 1;
+    while (S < most && (na * S < 4 * kWaves || 15 * ((na * S + kWaves - 1) / kWaves) * kWaves > 16 * na * S)) S *= 2;
+    while (S > 1 && room < 8 * S) S /= 2;
+    const int part = wave % S, group = wave / S, groups = kWaves / S, cap = S > 1 ? room / S : n;
     const int wide = wave_uniform(a.plan[3]), mid = wave_uniform(a.plan[4]);
     for (int base = 0, from = 0; base < n; base += cap) {
         // the experts [from, to) have places in [base, end); the first and the last may have others too
         const int end = min(base + cap, n);
-        while (wave_uniform(p.off[from + 1]) <= base) ++from;
+        while (wave_uniform(offset[from + 1]) <= base) ++from;
         int to = na;
         if (end < n)
-            for (to = from + 1; wave_uniform(p.off[to]) < end;) ++to;
+            for (to = from + 1; wave_uniform(offset[to]) < end;) ++to;
         auto slice = [&](int k) {
-            const int off = wave_uniform(p.off[k]), lo = max(off, base), hi = min(wave_uniform(p.off[k + 1]), end);
-            const int64_t row = (int64_t)wave_uniform(p.expert[k]) * a.H;
-            return FewSlice{{static_cast<const uint8_t *>(a.W2) + row * a.I * (MX ? 1 : 2), MX ? a.W2s + row * (a.I / 32) : nullptr, a.I},
-                            p.route + off, lo - off, hi - off, sums + (part * cap + lo - base) * C};
+            const int off = wave_uniform(offset[k]), lo = max(off, base), hi = min(wave_uniform(offset[k + 1]), end);
+            const int64_t row = (int64_t)wave_uniform(expert[k]) * a.H;
+            return FewSlice{{static_cast<const uint8_t *>(a.W2) + row * a.I * (MX ? 1 : 2), MX ? a.W2s + row * (a.I / 32) : nullptr,
+                             MX ? a.W2s + (int64_t)a.L * a.H * (a.I / 32) : nullptr, a.I},
+                            route + off, lo - off, hi - off, S > 1 ? sums + (part * cap + lo - base) * C : y + lo * C};
         };
         int k = from + group;
         for (; k < min(wide, to); k += groups) few_down_wide<MX, B>(a, h0, part, S, slice(k));
@@ -651,14 +718,15 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         k += nmid * groups;
         const int nlow = k < to ? (to - k + groups - 1) / groups : 0;
         few_down_run<MX, 2, B, 1>(a, h0, a.I, part, S, nlow, [&](int i) { return slice(k + i * groups); });
-        join(base, end, S, cap);
+        if (S > 1) join(base, end, S, cap);
     }
-    for (int i = t; i < a.T * C; i += kFewThreads) {
+    __syncthreads();
+    for (int i = t; i < a.T * C; i += kThreads) {
         const int tok = i / C, h = i % C;
         float sum = 0.f;
         for (int j = 0; j < a.K; ++j) {
-            const int at = p.place[tok * a.K + j];
-            if (at >= 0) sum = fmaf(a.w[tok * a.K + j], y[at * C + h], sum);
+            const int at = place[tok * a.K + j];
+            if (at != 0xffff) sum = fmaf(a.w[tok * a.K + j], y[at * C + h], sum);
         }
         if (a.Is) sum += y[(n + tok) * C + h];
         a.out[(int64_t)tok * a.H + h0 + h] = f2bf(sum);

@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_few_gateup(FewArgs a) {
 }
 
 template <bool MX, int B>
-__global__ __launch_bounds__(kFewThreads, 4) void k_few_down(FewArgs a) {
+__global__ __launch_bounds__(few_down_threads(B), B == 1 ? 4 : 2) void k_few_down(FewArgs a) {
     extern __shared__ __attribute__((aligned(16))) int32_t few_smem[];
     few_down_body<MX, B>(a, few_smem);
 }
@@ -1649,15 +1649,17 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     a.act = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + few_plan_bytes(d));
     const int rows = few_rows(d, Is);
     // down launch: 16 output columns a workgroup, 8 where that leaves CUs without
-    // one; 32 KiB of LDS for the parts' sums of a round, less where the sums of
-    // all rows leave less
-    const int C = a.H / 16 < device_cus() ? 8 : 16;
-    const int left = (int)(kMaxLds / 4) - few_down_words(a.L, a.R, rows, 0, C);
-    a.room = std::min(8192, left) / C;
+    // one.  LDS: the sums of every row and 32 KiB for their parts, but no more than
+    // half a CU's where the rows fit that (the calls' routes are rarely all local:
+    // the parts then have the rows' unused space)
+    const int C = a.H / 16 < device_cus() ? 8 : 16, waves = few_down_waves(C / 8);
+    const size_t list = 4 * (size_t)few_list_words(a.L, a.R), sums = 4 * (size_t)rows * C;
     const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R);
-    if (a.room < kFewWaves || lds_gu > kMaxLds) return MOE_EUNSUPPORTED;
-    a.room = std::min(a.room, rows * kFewWaves);
-    const size_t lds_down = 4 * (size_t)few_down_words(a.L, a.R, rows, a.room, C);
+    size_t lds_down = list + sums + std::min<size_t>(32 << 10, sums * (waves - 1));
+    if (lds_down > kMaxLds / 2) lds_down = std::max(list + sums, kMaxLds / 2);
+    if (lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
+    a.words = (int)((lds_down - list) / 16) * 4;
+    lds_down = list + 4 * (size_t)a.words;
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + Is / kFewRows;
     {
         TraceScope tr("few_gateup", s);
@@ -1667,7 +1669,7 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     if (launch_status() != MOE_OK) return MOE_EHIP;
     TraceScope tr("few_down", s);
     auto *down = C == 8 ? k_few_down<MX, 1> : k_few_down<MX, 2>;
-    hipLaunchKernelGGL(down, dim3(a.H / C), dim3(kFewThreads), lds_down, s, a);
+    hipLaunchKernelGGL(down, dim3(a.H / C), dim3(64 * waves), lds_down, s, a);
     return launch_status();
 }
 
