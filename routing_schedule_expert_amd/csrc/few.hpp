@@ -176,32 +176,28 @@ __device__ __forceinline__ void few_mx_frags(const u32x4 &c, uint32_t sbyte, bf1
     }
 }
 
-// A step takes 128 consecutive bytes of every weight row of a block (64 bf16
-// elements or 128 codes of the reduction dimension): eight 16-byte groups, of
-// which the MFMA's lane i + 16 g (row or column i, group g of its operand) takes
-//   dense  (V = 1)  groups g and 4 + g of row i, in two loads and two MFMAs:
-//                   blocks of 16 rows, tiles of 16 tokens;
-//   halves (V = 2)  group 4 (i & 1) + g of row i / 2, in one: blocks of 8 rows,
-//                   tiles of 8 tokens laid out alike.  MFMA row (r, p) times
-//                   column (c, q) is then row r half p times token c half q: the
-//                   wanted sum is the p = q entries of both halves, the other
-//                   half of the products is dropped.
-// Whole 128-byte lines in one load are worth it: a kernel that only reads gets
-// 7.1 TB/s with 128 (or 256) bytes of a row per load and 5.5 TB/s with 64.  The
-// dropped products cost nothing while the matrix cores wait for HBM, but a tile
-// holds half the tokens, so more than 16 routes of an expert take the dense form.
-template <bool MX, int V>
+// A step takes 128 consecutive bytes (64 bf16 elements or 128 codes of the
+// reduction dimension) of each of a block's 8 weight rows, in one load: the
+// MFMA's lane i + 16 g (row or column i, group g of its operand) reads 16-byte
+// group 4 (i & 1) + g of row i / 2, and a tile is 8 tokens laid out alike.  MFMA
+// row (r, p) times column (c, q) is then row r half p times token c half q: the
+// wanted sum is the p = q entries of both halves, the other half of the products
+// is dropped.  That costs nothing while the matrix cores wait for HBM, and whole
+// 128-byte lines per load are worth it: a kernel that only reads gets 7.1 TB/s
+// with 128 (or 256) bytes of a row per load and 5.5 TB/s with the 64 of a plain
+// 16-row operand, and 64 tokens of 8 experts (H = 7168, I = 2048) took 179 + 161 us
+// with plain operands against 130 + 107 us.
+template <bool MX>
 struct FewLane {
-    static constexpr int kLoads = 2 / V;                // loads of a block's (or tile's) step
-    static constexpr int kTokens = 16 / V;              // tokens of a tile
-    static constexpr int kRows = 16 / V;                // rows of a block
+    static constexpr int kTokens = 8;                   // tokens of a tile
+    static constexpr int kRows = 8;                     // rows of a block
     static constexpr int kStep = MX ? 128 : 64;         // elements of the reduction dimension per step
     static constexpr int kGroup = MX ? 16 : 8;          // elements of a group
-    int row, group, token;  // of the block; the first load's group (the second: 4 more); of the tile
+    int row, group, token;                              // of the block; of the 128 bytes; of the tile
     __device__ __forceinline__ FewLane() {
         const int lane = lane_id(), i = lane & 15, g = lane >> 4;
-        row = token = i / V;
-        group = V == 2 ? 4 * (i & 1) + g : g;
+        row = token = i / 2;
+        group = 4 * (i & 1) + g;
     }
 };
 
@@ -249,64 +245,56 @@ struct FewItem {
 struct FewRun {
     __amdgpu_buffer_rsrc_t tokens;
     uint32_t row, srow, wo, so;
-    template <bool MX, int V>
-    __device__ __forceinline__ static FewRun make(const FewLane<MX, V> &l, int cols, const void *tokens) {
+    template <bool MX>
+    __device__ __forceinline__ static FewRun make(const FewLane<MX> &l, int cols, const void *tokens) {
         const uint32_t row = (uint32_t)cols * (MX ? 1 : 2), srow = (uint32_t)cols / 32;
         return {few_rsrc(tokens, kFewBytes), row, srow, l.row * row + l.group * 16, l.row * srow};
     }
 };
 
-// One step's operands: M blocks of weight rows and NT tiles of tokens.  With
-// MX a load's 16 codes take two MFMAs, the first for each group's first 8 codes;
-// both operands use the same order, so the sum is over the same elements.
-// (SC: the step loads its own scale bytes; otherwise they come from FewScales)
-template <bool MX, int V, int M, int G, int NT, bool SC>
+// One step's operands: M blocks of weight rows and NT tiles of tokens.  With MX
+// a load's 16 codes take two MFMAs, the first for each group's first 8 codes;
+// both operands use the same order, so the sum is over the same elements.  OWN:
+// the step loads its own scale bytes (MX; otherwise they come from FewScales).
+template <bool MX, int M, int G, int NT, bool OWN>
 struct FewStep {
-    using L = FewLane<MX, V>;
-    static constexpr int N = L::kLoads, X = MX ? 2 : 1;  // 16-byte loads of 8 elements of a token's group
-    u32x4 w[M][N];
-    uint32_t sb[SC ? M : 1];
-    u32x4 x[NT][N][X];
+    using L = FewLane<MX>;
+    static constexpr int X = MX ? 2 : 1;  // 16-byte loads of 8 elements of a token's group
+    u32x4 w[M];
+    uint32_t sb[OWN ? M : 1];
+    u32x4 x[NT][X];
 
     __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k) {
+        constexpr int per = M / G;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            constexpr int per = M / G;
-            const __amdgpu_buffer_rsrc_t b = few_rsrc(it.wp[m / per], kFewBytes);
-#pragma unroll
-            for (int h = 0; h < N; ++h)
-                w[m][h] = few_load16_nt(b, r.wo + 64 * h, (m % per) * L::kRows * r.row + k * 128);
-            if constexpr (SC)
+            w[m] = few_load16_nt(few_rsrc(it.wp[m / per], kFewBytes), r.wo, (m % per) * L::kRows * r.row + k * 128);
+            if constexpr (OWN)
                 sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so,
                                                              (m % per) * L::kRows * r.srow + k * 4, 0);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < N; ++h)
-#pragma unroll
-                for (int e = 0; e < X; ++e)
-                    x[t][h][e] = few_load16(r.tokens, it.xo[t] + (4 * h * X + e) * 16, k * (L::kStep * 2));
+            for (int e = 0; e < X; ++e) x[t][e] = few_load16(r.tokens, it.xo[t] + e * 16, k * (L::kStep * 2));
     }
     // scale(m): block m's four scale bytes of this step
     template <class Scale>
     __device__ __forceinline__ void mul(const L &l, Scale scale, f32x4 (&acc)[M][NT]) const {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+        for (int m = 0; m < M; ++m) {
+            bf16x8 f[2];
+            if constexpr (MX)
+                few_mx_frags(w[m], (scale(m) >> (8 * (l.group >> 1))) & 0xffu, f[0], f[1]);
+            else
+                f[0] = __builtin_bit_cast(bf16x8, w[m]);
 #pragma unroll
-            for (int h = 0; h < N; ++h) {
-                bf16x8 f[2];
-                if constexpr (MX)
-                    few_mx_frags(w[m][h], (scale(m) >> (8 * ((l.group + 4 * h) >> 1))) & 0xffu, f[0], f[1]);
-                else
-                    f[0] = __builtin_bit_cast(bf16x8, w[m][h]);
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < X; ++e)
-                        acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[e], __builtin_bit_cast(bf16x8, x[t][h][e]),
-                                                                            acc[m][t], 0, 0, 0);
-            }
+                for (int e = 0; e < X; ++e)
+                    acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[e], __builtin_bit_cast(bf16x8, x[t][e]), acc[m][t], 0,
+                                                                        0, 0);
+        }
     }
 };
 
@@ -315,7 +303,7 @@ struct FewStep {
 // row's codes (gate/up of 24 experts took 124 us with one such load per step
 // and block, 103 us without any).  A chunk may reach past its row, into bytes
 // that no step uses, but not past the array: the buffer's size ends there.
-template <int V, int M, int G>
+template <int M, int G>
 struct FewScales {
     u32x4 v[M];
     template <int NT>
@@ -323,24 +311,24 @@ struct FewScales {
         constexpr int per = M / G;
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            v[m] = few_load16(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so, (m % per) * (16 / V) * r.srow + k * 4);
+            v[m] = few_load16(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so, (m % per) * 8 * r.srow + k * 4);
     }
 };
 
 // Steps in flight that fit `regs` registers beside the sums; with MX four and
 // the scale bytes of four steps where that fits.
-template <bool MX, int V, int M, int NT>
+template <bool MX, int M, int NT>
 constexpr int few_step_regs() {
-    return 4 * FewLane<MX, V>::kLoads * (M + (MX ? 2 : 1) * NT);
+    return 4 * (M + (MX ? 2 : 1) * NT);
 }
-template <bool MX, int V, int M, int NT>
+template <bool MX, int M, int NT>
 constexpr bool few_chunked(int regs) {
-    return MX && 4 * few_step_regs<MX, V, M, NT>() + 8 * M + 4 * M * NT <= regs;
+    return MX && 4 * few_step_regs<MX, M, NT>() + 8 * M + 4 * M * NT <= regs;
 }
-template <bool MX, int V, int M, int NT>
+template <bool MX, int M, int NT>
 constexpr int few_depth(int regs) {
-    if (few_chunked<MX, V, M, NT>(regs)) return 4;
-    const int d = (regs - 4 * M * NT) / (few_step_regs<MX, V, M, NT>() + (MX ? M : 0));
+    if (few_chunked<MX, M, NT>(regs)) return 4;
+    const int d = (regs - 4 * M * NT) / (few_step_regs<MX, M, NT>() + (MX ? M : 0));
     return d < 1 ? 1 : d > 8 ? 8 : d;
 }
 
@@ -352,13 +340,13 @@ constexpr int few_depth(int regs) {
 // between items. 
 // The scheduling barriers keep the loads where they are written: left alone,
 // the compiler moves them next to their use.
-template <bool MX, int V, int M, int G, int NT, int REGS, class Item, class Emit>
-__device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, const FewRun &r, int k0, int n, int items, Item item, Emit emit) {
+template <bool MX, int M, int G, int NT, int REGS, class Item, class Emit>
+__device__ __forceinline__ void few_stream(const FewLane<MX> &l, const FewRun &r, int k0, int n, int items, Item item, Emit emit) {
     if (items <= 0) return;
-    constexpr bool chunks = few_chunked<MX, V, M, NT>(REGS), own = MX && !chunks;  // scale bytes: of four steps, of one
-    constexpr int D = few_depth<MX, V, M, NT>(REGS);
-    FewStep<MX, V, M, G, NT, own> st[D];
-    FewScales<V, chunks ? M : G, G> now, then;
+    constexpr bool chunks = few_chunked<MX, M, NT>(REGS), own = MX && !chunks;  // scale bytes: of four steps, of one
+    constexpr int D = few_depth<MX, M, NT>(REGS);
+    FewStep<MX, M, G, NT, own> st[D];
+    FewScales<chunks ? M : G, G> now, then;
     FewItem<G, NT> cur, next;
     auto mul = [&](int j, f32x4(&acc)[M][NT]) {
         st[j].mul(
@@ -423,21 +411,14 @@ __device__ __forceinline__ void few_stream(const FewLane<MX, V> &l, const FewRun
     }
 }
 
-// The sums of a block and tile that this lane keeps: row r(i) of the block and
-// the lane's token.  Dense: four rows 4 g + i.  Halves: both halves' entries
-// meet (lane ^ 1), then the even lane keeps row 2 g and the odd lane 2 g + 1.
-template <int V, class Put>
-__device__ __forceinline__ void few_sums(const f32x4 &acc, Put put) {
-    const int lane = lane_id(), g = lane >> 4;
-    if constexpr (V == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) put(4 * g + i, acc[i]);
-    } else {
-        const bool odd = lane & 1;
-        const float a = odd ? acc[1] : acc[0], b = odd ? acc[3] : acc[2];
-        const float sa = a + __shfl_xor(a, 1, kWave), sb = b + __shfl_xor(b, 1, kWave);
-        put(2 * g + (odd ? 1 : 0), odd ? sb : sa);
-    }
+// A block's and tile's sums: both halves' entries meet (lane ^ 1), then the even
+// lane has row 2 g of the block and the odd lane row 2 g + 1, for the lane's token.
+__device__ __forceinline__ int few_sum_row() { return 2 * (lane_id() >> 4) + (lane_id() & 1); }
+__device__ __forceinline__ float few_sum(const f32x4 &acc) {
+    const bool odd = lane_id() & 1;
+    const float a = odd ? acc[1] : acc[0], b = odd ? acc[3] : acc[2];
+    const float sa = a + __shfl_xor(a, 1, kWave), sb = b + __shfl_xor(b, 1, kWave);
+    return odd ? sb : sa;
 }
 
 __device__ __forceinline__ int wave_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -456,11 +437,13 @@ __device__ __forceinline__ int few_token(const FewArgs &a, const int *route, int
 template <class T>
 __device__ __forceinline__ int few_act_row(const FewArgs &a, const T *route, int k) { return route ? (int)route[k] : a.R + k; }
 
-// Operands of a unit's routes from `first` on: V gate blocks, V up blocks.
-template <bool MX, int V, int NT>
-__device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX, V> &l,
+constexpr int kFewGateupBlocks = 4;  // two of gate rows, two of up rows
+
+// Operands of a unit's routes from `first` on.
+template <bool MX, int NT>
+__device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX> &l,
                                                 FewItem<2, NT> &it) {
-    using L = FewLane<MX, V>;
+    using L = FewLane<MX>;
 #pragma unroll
     for (int g = 0; g < 2; ++g) it.template rows<MX>(g, u.W, (int64_t)g * u.inner + u.i0);
 #pragma unroll
@@ -471,10 +454,10 @@ __device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit 
 
 // The waves' sums of a unit meet in LDS (red), 32 tokens at a time, and are
 // added in wave order; then the activation, rounded once.
-template <bool MX, int V, int NT>
-__device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX, V> &l,
-                                                const f32x4 (&acc)[2 * V][NT], float *red) {
-    using L = FewLane<MX, V>;
+template <bool MX, int NT>
+__device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX> &l,
+                                                const f32x4 (&acc)[kFewGateupBlocks][NT], float *red) {
+    using L = FewLane<MX>;
     constexpr int per = 32 / L::kTokens;  // tiles that meet at a time
     const int t = threadIdx.x, wave = t >> 6;
 #pragma unroll
@@ -482,9 +465,9 @@ __device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit 
         __syncthreads();  // the previous sums have been read
 #pragma unroll
         for (int q = q0; q < (q0 + per < NT ? q0 + per : NT); ++q) {
-            float *dst = red + (wave * 32 + (q - q0) * L::kTokens + l.token) * kFewRedLd;
+            float *dst = red + (wave * 32 + (q - q0) * L::kTokens + l.token) * kFewRedLd + few_sum_row();
 #pragma unroll
-            for (int m = 0; m < 2 * V; ++m) few_sums<V>(acc[m][q], [&](int r, float v) { dst[m * L::kRows + r] = v; });
+            for (int m = 0; m < kFewGateupBlocks; ++m) dst[m * L::kRows] = few_sum(acc[m][q]);
         }
         __syncthreads();
         const int tok = t >> 4, i = t & 15, k = first + q0 * L::kTokens + tok;
@@ -503,33 +486,35 @@ __device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit 
 
 // `count` units (unit(i) for i in turn), all with at most NT tiles of routes
 // from `first` on, the waves splitting H.
-template <bool MX, int V, int NT, class Unit>
+template <bool MX, int NT, class Unit>
 __device__ __forceinline__ void few_gateup_run(const FewArgs &a, int count, int first, Unit unit, float *red) {
-    using L = FewLane<MX, V>;
+    using L = FewLane<MX>;
+    constexpr int M = kFewGateupBlocks;
     const L l;
     const int wave = wave_uniform(threadIdx.x >> 6), steps = a.H / L::kStep;
     const int k0 = wave * steps / kFewWaves, n = (wave + 1) * steps / kFewWaves - k0;
-    few_stream<MX, V, 2 * V, 2, NT, kFewGateupRegs>(
-        l, FewRun::make(l, a.H, a.X), k0, n, count, [&](int i, FewItem<2, NT> &it) { few_gateup_item<MX, V, NT>(a, unit(i), first, l, it); },
-        [&](int i, const f32x4(&acc)[2 * V][NT]) { few_gateup_join<MX, V, NT>(a, unit(i), first, l, acc, red); });
+    few_stream<MX, M, 2, NT, kFewGateupRegs>(
+        l, FewRun::make(l, a.H, a.X), k0, n, count, [&](int i, FewItem<2, NT> &it) { few_gateup_item<MX, NT>(a, unit(i), first, l, it); },
+        [&](int i, const f32x4(&acc)[M][NT]) { few_gateup_join<MX, NT>(a, unit(i), first, l, acc, red); });
 }
 
-// A unit with any number of routes, 64 at a time.
+// The routes [first, min(n, first + 64)) of a unit.
 template <bool MX>
-__device__ __forceinline__ void few_gateup_wide(const FewArgs &a, const FewUnit &u, float *red) {
-    for (int first = 0; first < u.n; first += 64) {
-        if (u.n - first <= 16)
-            few_gateup_run<MX, 2, 2>(a, 1, first, [&](int) { return u; }, red);
-        else if (u.n - first <= 32)
-            few_gateup_run<MX, 1, 2>(a, 1, first, [&](int) { return u; }, red);
-        else
-            few_gateup_run<MX, 1, 4>(a, 1, first, [&](int) { return u; }, red);
-    }
+__device__ __forceinline__ void few_gateup_pass(const FewArgs &a, const FewUnit &u, int first, float *red) {
+    const int left = u.n - first;
+    if (left <= 16)
+        few_gateup_run<MX, 2>(a, 1, first, [&](int) { return u; }, red);
+    else if (left <= 32)
+        few_gateup_run<MX, 4>(a, 1, first, [&](int) { return u; }, red);
+    else
+        few_gateup_run<MX, 8>(a, 1, first, [&](int) { return u; }, red);
 }
 
-// Persistent over the units, the heaviest first: the shared expert's blocks
-// (every token's columns), the experts with over 16 routes, then in two streams
-// those with up to 16 and up to 8.
+// Persistent over the units in order, every workgroup taking each gridDim.x-th
+// one (runs of neighbours instead read 256 far-apart places at a time: 520 us
+// against 433 for 43 experts): the shared expert's blocks, 64 tokens at a time,
+// the experts with over 16 routes, then in two streams those with up to 16 and
+// up to 8.
 template <bool MX>
 __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
     float *red = reinterpret_cast<float *>(lds);
@@ -548,29 +533,32 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
             o.place[i] = p.place[i];
         }
     }
-    const int blocks = a.I / kFewRows, shared = a.Is / kFewRows, step = gridDim.x;
+    const int blocks = a.I / kFewRows, sblocks = a.Is / kFewRows, shared = sblocks * ((a.T + 63) / 64), step = gridDim.x;
     const int wide = wave_uniform(head[3]) * blocks, mid = wave_uniform(head[4]) * blocks, all = na * blocks;
-    auto routed = [&](int u) {  // unit u of the experts in the list's order
-        const int k = u / blocks, off = wave_uniform(p.off[k]);
+    int u = blockIdx.x;
+    for (; u < shared; u += step) {
+        const FewUnit s{{reinterpret_cast<const uint8_t *>(a.S13), nullptr, nullptr, a.H}, a.Is, u % sblocks * kFewRows, a.T, nullptr};
+        if (a.T <= 8)
+            few_gateup_run<false, 1>(a, 1, 0, [&](int) { return s; }, red);
+        else
+            few_gateup_pass<false>(a, s, u / sblocks * 64, red);
+    }
+    auto routed = [&](int v) {  // unit v of the experts in the list's order
+        const int k = v / blocks, off = wave_uniform(p.off[k]);
         const int64_t row = (int64_t)wave_uniform(p.expert[k]) * 2 * a.I;
         return FewUnit{{static_cast<const uint8_t *>(a.W13) + row * a.H * (MX ? 1 : 2), MX ? a.W13s + row * (a.H / 32) : nullptr,
                         MX ? a.W13s + (int64_t)a.L * 2 * a.I * (a.H / 32) : nullptr, a.H},
-                       a.I, u % blocks * kFewRows, wave_uniform(p.off[k + 1]) - off, p.route + off};
+                       a.I, v % blocks * kFewRows, wave_uniform(p.off[k + 1]) - off, p.route + off};
     };
-    int u = blockIdx.x;
-    for (; u < shared; u += step) {
-        const FewUnit s{{reinterpret_cast<const uint8_t *>(a.S13), nullptr, nullptr, a.H}, a.Is, u * kFewRows, a.T, nullptr};
-        if (a.T <= 8)
-            few_gateup_run<false, 2, 1>(a, 1, 0, [&](int) { return s; }, red);
-        else
-            few_gateup_wide<false>(a, s, red);
+    for (u -= shared; u < wide; u += step) {
+        const FewUnit r = routed(u);
+        for (int first = 0; first < r.n; first += 64) few_gateup_pass<MX>(a, r, first, red);
     }
-    for (u -= shared; u < wide; u += step) few_gateup_wide<MX>(a, routed(u), red);
     const int nmid = u < mid ? (mid - u + step - 1) / step : 0;
-    few_gateup_run<MX, 2, 2>(a, nmid, 0, [&](int i) { return routed(u + i * step); }, red);
+    few_gateup_run<MX, 2>(a, nmid, 0, [&](int i) { return routed(u + i * step); }, red);
     u += nmid * step;
     const int nlow = u < all ? (all - u + step - 1) / step : 0;
-    few_gateup_run<MX, 2, 1>(a, nlow, 0, [&](int i) { return routed(u + i * step); }, red);
+    few_gateup_run<MX, 1>(a, nlow, 0, [&](int i) { return routed(u + i * step); }, red);
 }
 
 // Parts of a reduction dimension of `inner` elements: at least 512 bytes of a
@@ -593,13 +581,12 @@ struct FewSlice {
 
 // `count` items (slice(i) for i in turn) with at most NT tiles each, over part
 // `part` of S of their activations: one wave, no barrier.
-template <bool MX, int V, int B, int NT, class Slice>
+template <bool MX, int B, int NT, class Slice>
 __device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols, int part, int S, int count, Slice slice) {
-    using L = FewLane<MX, V>;
-    constexpr int M = B * V / 2;
+    using L = FewLane<MX>;
     const L l;
     const int steps = cols / L::kStep, k0 = part * steps / S, n = (part + 1) * steps / S - k0;
-    few_stream<MX, V, M, 1, NT, few_down_regs(B)>(
+    few_stream<MX, B, 1, NT, few_down_regs(B)>(
         l, FewRun::make(l, cols, a.act), k0, n, count,
         [&](int i, FewItem<1, NT> &it) {
             const FewSlice s = slice(i);
@@ -609,36 +596,33 @@ __device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols,
                 it.xo[q] = (uint32_t)few_act_row(a, s.route, min(s.first + q * L::kTokens + l.token, s.n - 1)) * (uint32_t)(a.ld * 2) +
                            l.group * (L::kGroup * 2);
         },
-        [&](int i, const f32x4(&acc)[M][NT]) {
+        [&](int i, const f32x4(&acc)[B][NT]) {
             const FewSlice s = slice(i);
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 const int k = q * L::kTokens + l.token;
-                const bool in = s.first + k < s.n;
 #pragma unroll
-                for (int m = 0; m < M; ++m)
-                    few_sums<V>(acc[m][q], [&](int r, float v) {
-                        if (in) s.y[k * 8 * B + m * L::kRows + r] = v;
-                    });
+                for (int m = 0; m < B; ++m) {
+                    const float v = few_sum(acc[m][q]);
+                    if (s.first + k < s.n) s.y[k * 8 * B + m * L::kRows + few_sum_row()] = v;
+                }
             }
         });
 }
 
-// An item with any number of routes: 64 at a time with 16 columns, 16 with 8.
+// An item with any number of routes: 64 at a time, 32 where the waves have
+// fewer registers.
 template <bool MX, int B>
 __device__ __forceinline__ void few_down_wide(const FewArgs &a, int h0, int part, int S, FewSlice s) {
-    if constexpr (B == 1) {
-        for (; s.first < s.n; s.first += 16, s.y += 16 * 8)
-            few_down_run<MX, 2, 1, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
-        return;
-    }
-    else for (; s.first < s.n; s.first += 64, s.y += 64 * 8 * B) {
-        if (s.n - s.first <= 16)
-            few_down_run<MX, 2, B, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
-        else if (s.n - s.first <= 32)
-            few_down_run<MX, 1, B, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
-        else
-            few_down_run<MX, 1, B, 4>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
+    constexpr int most = B == 1 ? 32 : 64;
+    for (; s.first < s.n; s.first += most, s.y += most * 8 * B) {
+        const int left = s.n - s.first;
+        if (left <= 16)
+            few_down_run<MX, B, 2>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
+        else if (B == 1 || left <= 32)
+            few_down_run<MX, B, 4>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
+        else if constexpr (B > 1)
+            few_down_run<MX, B, 8>(a, h0, s.W.cols, part, S, 1, [&](int) { return s; });
     }
 }
 
@@ -684,7 +668,7 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
             if (wave < S) {
                 const FewSlice s{W, nullptr, base, end, S > 1 ? sums + wave * cap * C : y + n * C};
                 if (end - base <= 8)
-                    few_down_run<false, 2, B, 1>(a, h0, a.Is, wave, S, 1, [&](int) { return s; });
+                    few_down_run<false, B, 1>(a, h0, a.Is, wave, S, 1, [&](int) { return s; });
                 else
                     few_down_wide<false, B>(a, h0, wave, S, s);
             }
@@ -714,10 +698,10 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         int k = from + group;
         for (; k < min(wide, to); k += groups) few_down_wide<MX, B>(a, h0, part, S, slice(k));
         const int nmid = k < min(mid, to) ? (min(mid, to) - k + groups - 1) / groups : 0;
-        few_down_run<MX, 2, B, 2>(a, h0, a.I, part, S, nmid, [&](int i) { return slice(k + i * groups); });
+        few_down_run<MX, B, 2>(a, h0, a.I, part, S, nmid, [&](int i) { return slice(k + i * groups); });
         k += nmid * groups;
         const int nlow = k < to ? (to - k + groups - 1) / groups : 0;
-        few_down_run<MX, 2, B, 1>(a, h0, a.I, part, S, nlow, [&](int i) { return slice(k + i * groups); });
+        few_down_run<MX, B, 1>(a, h0, a.I, part, S, nlow, [&](int i) { return slice(k + i * groups); });
         if (S > 1) join(base, end, S, cap);
     }
     __syncthreads();

@@ -1660,7 +1660,7 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     if (lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
     a.words = (int)((lds_down - list) / 16) * 4;
     lds_down = list + 4 * (size_t)a.words;
-    const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + Is / kFewRows;
+    const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + (a.T + 63) / 64 * (Is / kFewRows);
     {
         TraceScope tr("few_gateup", s);
         hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, device_cus())), dim3(kFewThreads), lds_gu,
