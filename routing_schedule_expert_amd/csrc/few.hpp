@@ -40,7 +40,7 @@ constexpr int kFewGateupRegs = 200;  // registers for a wave's sums and steps in
 // against 62 for 64 experts of H = 2048, I = 1024).
 constexpr int few_down_waves(int B) { return B == 1 ? 8 : 4; }
 constexpr int few_down_threads(int B) { return 64 * few_down_waves(B); }
-constexpr int few_down_regs(int B) { return B == 1 ? 88 : 120; }
+constexpr int few_down_regs(int B) { return B == 1 ? 72 : 104; }
 
 struct FewArgs {
     const int32_t *routes;
@@ -220,7 +220,7 @@ __device__ __forceinline__ u32x4 few_load16(__amdgpu_buffer_rsrc_t r, uint32_t l
 __device__ __forceinline__ u32x4 few_load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 2));  // 2: nontemporal
 }
-constexpr uint32_t kFewBytes = 0x7fffffffu;  // the host keeps every offset below
+constexpr uint32_t kFewBytes = 0x7fffffffu;  // the host keeps every offset below; a buffer of 0 bytes reads as zeros
 
 // Where an item's operands start: its M blocks of weight rows, G runs of
 // consecutive blocks each from wp[.] / ws[.] (wave-uniform) on, and this lane's
@@ -243,12 +243,12 @@ struct FewItem {
 // What the steps of a run of items share: the tokens' matrix, bytes of a weight
 // row and of its scale bytes, and this lane's bytes from a block's first row.
 struct FewRun {
-    __amdgpu_buffer_rsrc_t tokens;
+    const void *tokens;
     uint32_t row, srow, wo, so;
     template <bool MX>
     __device__ __forceinline__ static FewRun make(const FewLane<MX> &l, int cols, const void *tokens) {
         const uint32_t row = (uint32_t)cols * (MX ? 1 : 2), srow = (uint32_t)cols / 32;
-        return {few_rsrc(tokens, kFewBytes), row, srow, l.row * row + l.group * 16, l.row * srow};
+        return {tokens, row, srow, l.row * row + l.group * 16, l.row * srow};
     }
 };
 
@@ -264,19 +264,22 @@ struct FewStep {
     uint32_t sb[OWN ? M : 1];
     u32x4 x[NT][X];
 
-    __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k) {
+    // step k's loads; all out of range unless `in` (which is wave-uniform)
+    __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k, bool in) {
         constexpr int per = M / G;
+        if (!in) k = 0;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            w[m] = few_load16_nt(few_rsrc(it.wp[m / per], kFewBytes), r.wo, (m % per) * L::kRows * r.row + k * 128);
+            w[m] = few_load16_nt(few_rsrc(it.wp[m / per], in ? kFewBytes : 0), r.wo, in ? (m % per) * L::kRows * r.row + k * 128 : 0);
             if constexpr (OWN)
-                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so,
-                                                             (m % per) * L::kRows * r.srow + k * 4, 0);
+                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], in ? it.s_bytes[m / per] : 0), r.so,
+                                                             in ? (m % per) * L::kRows * r.srow + k * 4 : 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < X; ++e) x[t][e] = few_load16(r.tokens, it.xo[t] + e * 16, k * (L::kStep * 2));
+            for (int e = 0; e < X; ++e)
+                x[t][e] = few_load16(few_rsrc(r.tokens, in ? kFewBytes : 0), it.xo[t] + e * 16, k * (L::kStep * 2));
     }
     // scale(m): block m's four scale bytes of this step
     template <class Scale>
@@ -307,11 +310,12 @@ template <int M, int G>
 struct FewScales {
     u32x4 v[M];
     template <int NT>
-    __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k) {
+    __device__ __forceinline__ void load(const FewRun &r, const FewItem<G, NT> &it, int k, bool in) {
         constexpr int per = M / G;
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            v[m] = few_load16(few_rsrc(it.ws[m / per], it.s_bytes[m / per]), r.so, (m % per) * 8 * r.srow + k * 4);
+            v[m] = few_load16(few_rsrc(it.ws[m / per], in ? it.s_bytes[m / per] : 0), r.so,
+                              in ? (m % per) * 8 * r.srow + k * 4 : 0);
     }
 };
 
@@ -337,10 +341,17 @@ constexpr int few_depth(int regs) {
 // emit(item, acc).  item(i) gives the operands' places.  D steps are in flight:
 // a step's registers are loaded again as soon as they are used, the last ones of
 // an item with the first steps of the next, so the wave's loads never run dry
-// between items. 
-// The scheduling barriers keep the loads where they are written: left alone,
-// the compiler moves them next to their use.
-template <bool MX, int M, int G, int NT, int REGS, class Item, class Emit>
+// between items.  The scheduling barriers keep the loads where they are written:
+// left alone, the compiler moves them next to their use.
+//
+// The compiler counts the loads in flight to wait for no more than a step needs,
+// and loses count behind a branch around a load: it then waits for all D steps
+// once every D.  EVEN has no such branch: every turn issues the same loads, those
+// of steps that do not exist from an empty buffer.  That pays where a workgroup
+// has a CU for itself and its waves never meet (down, 8 columns: 59 us to 47 for
+// 64 experts of H = 2048, I = 1024) and not where few steps make many of the
+// loads empty (gate/up of the same: 90 us to 100).
+template <bool MX, int M, int G, int NT, int REGS, bool EVEN, class Item, class Emit>
 __device__ __forceinline__ void few_stream(const FewLane<MX> &l, const FewRun &r, int k0, int n, int items, Item item, Emit emit) {
     if (items <= 0) return;
     constexpr bool chunks = few_chunked<MX, M, NT>(REGS), own = MX && !chunks;  // scale bytes: of four steps, of one
@@ -348,7 +359,8 @@ __device__ __forceinline__ void few_stream(const FewLane<MX> &l, const FewRun &r
     FewStep<MX, M, G, NT, own> st[D];
     FewScales<chunks ? M : G, G> now, then;
     FewItem<G, NT> cur, next;
-    auto mul = [&](int j, f32x4(&acc)[M][NT]) {
+    f32x4 acc[M][NT];
+    auto mul = [&](int j) {
         st[j].mul(
             l,
             [&](int m) -> uint32_t {
@@ -358,56 +370,70 @@ __device__ __forceinline__ void few_stream(const FewLane<MX> &l, const FewRun &r
             acc);
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto load = [&](int j, const FewItem<G, NT> &it, int step) {
-        st[j].load(r, it, k0 + step);
+    auto load = [&](int j, const FewItem<G, NT> &it, int step, bool in) {
+        st[j].load(r, it, k0 + step, in);
         if constexpr (chunks)
-            if (j == 0) then.load(r, it, k0 + step);
+            if (j == 0) then.load(r, it, k0 + step, in);
         __builtin_amdgcn_sched_barrier(0);
     };
     item(0, cur);
 #pragma unroll
     for (int j = 0; j < D; ++j)
-        if (j < n) load(j, cur, j);
+        if (EVEN || j < n) load(j, cur, j, !EVEN || j < n);
     now = then;
     for (int it = 0; it < items; ++it) {
         const bool more = it + 1 < items;
         if (more) item(it + 1, next);
-        f32x4 acc[M][NT];
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        int k = 0;
-        for (; k + 2 * D <= n; k += D) {
+        if constexpr (EVEN) {
+            const int turns = max(1, (n + D - 1) / D);
+            for (int c = 0; c < turns; ++c) {
+                const bool last = c + 1 == turns;
+                if (last) cur = next;
+                const int base = last ? 0 : (c + 1) * D, steps = last && !more ? 0 : n;
 #pragma unroll
-            for (int j = 0; j < D; ++j) {
-                mul(j, acc);
-                load(j, cur, k + D + j);
+                for (int j = 0; j < D; ++j) {
+                    if (c * D + j < n) mul(j);
+                    load(j, cur, base + j, base + j < steps);
+                }
+                now = then;
             }
-            now = then;
-        }
-        // fewer than 2 D steps are left, the first D of them in flight
+        } else {
+            int k = 0;
+            for (; k + 2 * D <= n; k += D) {
 #pragma unroll
-        for (int j = 0; j < D; ++j)
-            if (k + j < n) {
-                mul(j, acc);
-                if (k + D + j < n)
-                    load(j, cur, k + D + j);
-                else if (more)
-                    load(j, next, j);
+                for (int j = 0; j < D; ++j) {
+                    mul(j);
+                    load(j, cur, k + D + j, true);
+                }
+                now = then;
             }
-        now = then;
-        if (k + D < n) {
+            // fewer than 2 D steps are left, the first D of them in flight
 #pragma unroll
             for (int j = 0; j < D; ++j)
-                if (k + D + j < n) {
-                    mul(j, acc);
-                    if (more) load(j, next, j);
+                if (k + j < n) {
+                    mul(j);
+                    if (k + D + j < n)
+                        load(j, cur, k + D + j, true);
+                    else if (more)
+                        load(j, next, j, true);
                 }
             now = then;
+            if (k + D < n) {
+#pragma unroll
+                for (int j = 0; j < D; ++j)
+                    if (k + D + j < n) {
+                        mul(j);
+                        if (more) load(j, next, j, true);
+                    }
+                now = then;
+            }
+            cur = next;
         }
         emit(it, acc);
-        cur = next;
     }
 }
 
@@ -493,7 +519,7 @@ __device__ __forceinline__ void few_gateup_run(const FewArgs &a, int count, int 
     const L l;
     const int wave = wave_uniform(threadIdx.x >> 6), steps = a.H / L::kStep;
     const int k0 = wave * steps / kFewWaves, n = (wave + 1) * steps / kFewWaves - k0;
-    few_stream<MX, M, 2, NT, kFewGateupRegs>(
+    few_stream<MX, M, 2, NT, kFewGateupRegs, false>(
         l, FewRun::make(l, a.H, a.X), k0, n, count, [&](int i, FewItem<2, NT> &it) { few_gateup_item<MX, NT>(a, unit(i), first, l, it); },
         [&](int i, const f32x4(&acc)[M][NT]) { few_gateup_join<MX, NT>(a, unit(i), first, l, acc, red); });
 }
@@ -586,7 +612,7 @@ __device__ __forceinline__ void few_down_run(const FewArgs &a, int h0, int cols,
     using L = FewLane<MX>;
     const L l;
     const int steps = cols / L::kStep, k0 = part * steps / S, n = (part + 1) * steps / S - k0;
-    few_stream<MX, B, 1, NT, few_down_regs(B)>(
+    few_stream<MX, B, 1, NT, few_down_regs(B), true>(
         l, FewRun::make(l, cols, a.act), k0, n, count,
         [&](int i, FewItem<1, NT> &it) {
             const FewSlice s = slice(i);
