@@ -23,6 +23,7 @@
 // No atomics touch a float: the result does not depend on timing.
 #pragma once
 
+#include "buffer.hpp"
 #include "common.hpp"
 #include "gemm.hpp"
 
@@ -208,18 +209,6 @@ struct FewMatrix {
     int cols;
 };
 
-// Raw buffer over [base, base + bytes) (base wave-uniform; word 3 as for every
-// raw buffer on gfx9 parts): a load's address is the lane's 32-bit offset plus a
-// wave-uniform one, so the streams below need no vector arithmetic for it.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void *base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
-}
-__device__ __forceinline__ u32x4 few_load16(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
-}
-__device__ __forceinline__ u32x4 few_load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 2));  // 2: nontemporal
-}
 constexpr uint32_t kFewBytes = 0x7fffffffu;  // the host keeps every offset below; a buffer of 0 bytes reads as zeros
 
 // Where an item's operands start: its M blocks of weight rows, G runs of
@@ -270,16 +259,16 @@ struct FewStep {
         if (!in) k = 0;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            w[m] = few_load16_nt(few_rsrc(it.wp[m / per], in ? kFewBytes : 0), r.wo, in ? (m % per) * L::kRows * r.row + k * 128 : 0);
+            w[m] = buffer_load16_nt(raw_buffer(it.wp[m / per], in ? kFewBytes : 0), r.wo, in ? (m % per) * L::kRows * r.row + k * 128 : 0);
             if constexpr (OWN)
-                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(it.ws[m / per], in ? it.s_bytes[m / per] : 0), r.so,
+                sb[m] = __builtin_amdgcn_raw_buffer_load_b32(raw_buffer(it.ws[m / per], in ? it.s_bytes[m / per] : 0), r.so,
                                                              in ? (m % per) * L::kRows * r.srow + k * 4 : 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < X; ++e)
-                x[t][e] = few_load16(few_rsrc(r.tokens, in ? kFewBytes : 0), it.xo[t] + e * 16, k * (L::kStep * 2));
+                x[t][e] = buffer_load16(raw_buffer(r.tokens, in ? kFewBytes : 0), it.xo[t] + e * 16, k * (L::kStep * 2));
     }
     // scale(m): block m's four scale bytes of this step
     template <class Scale>
@@ -314,7 +303,7 @@ struct FewScales {
         constexpr int per = M / G;
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            v[m] = few_load16(few_rsrc(it.ws[m / per], in ? it.s_bytes[m / per] : 0), r.so,
+            v[m] = buffer_load16(raw_buffer(it.ws[m / per], in ? it.s_bytes[m / per] : 0), r.so,
                               in ? (m % per) * 8 * r.srow + k * 4 : 0);
     }
 };

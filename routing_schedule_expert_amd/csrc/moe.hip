@@ -10,6 +10,7 @@
 #include <mutex>
 #include <vector>
 
+#include "buffer.hpp"
 #include "ckpt.hpp"
 #include "common.hpp"
 #include "few.hpp"
@@ -220,15 +221,15 @@ __global__ __launch_bounds__(few_down_threads(B), B == 1 ? 4 : 2) void k_few_dow
 }
 
 template <bool F32, int CH>
-__global__ __launch_bounds__(CH <= 1 ? 256 : CH == 2 ? 512 : 1024) void k_norm_fwd(NormArgs a) {
-    __shared__ float lds[2 * 16];
-    norm_fwd_body<F32, CH>(a, lds);
+__global__ __launch_bounds__(kNormMaxThreads) void k_norm_fwd(NormArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float norm_smem[];
+    norm_fwd_body<F32, CH>(a, norm_smem);
 }
 
 template <bool F32, int CH>
-__global__ __launch_bounds__(CH <= 1 ? 256 : CH == 2 ? 512 : 1024) void k_norm_bwd(NormBwdArgs a) {
-    __shared__ float lds[2 * 2 * 16];
-    norm_bwd_body<F32, CH>(a, lds);
+__global__ __launch_bounds__(kNormMaxThreads) void k_norm_bwd(NormBwdArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float norm_smem[];
+    norm_bwd_body<F32, CH>(a, norm_smem);
 }
 
 __global__ __launch_bounds__(1024) void k_norm_dg(const float *part, int groups, int H, float *dg_post, float *dg_pre) {
@@ -1754,8 +1755,10 @@ int norm_check(const moe_norm_desc *n) {
 int64_t norm_groups(const moe_norm_desc *n) { return std::min<int64_t>(n->rows, kNormGroups); }
 int64_t norm_ws_bytes(const moe_norm_desc *n) { return align256(norm_groups(n) * 2 * n->H * 4); }
 
-// Chunks of 8 elements per thread, and the threads of a row's workgroup.
-int norm_chunks(const moe_norm_desc *n) { return n->H <= 2048 ? 1 : n->H <= 8192 ? 2 : 4; }
+// Chunks of 8 elements per thread, the threads of a row's workgroup, and its LDS
+// (the sums' slots, and the gains with one chunk per thread).
+int norm_chunks(const moe_norm_desc *n) { return n->H <= kNormLdsH ? 1 : n->H <= 2 * kNormLdsH ? 2 : 4; }
+size_t norm_lds_bytes(const moe_norm_desc *n) { return 256 + (norm_chunks(n) == 1 ? 8 * (size_t)n->H : 0); }
 int norm_threads(const moe_norm_desc *n) {
     const int per = 8 * 64 * norm_chunks(n);
     return 64 * ((n->H + per - 1) / per);
@@ -1802,11 +1805,11 @@ int moe_block_norm_fwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     a.r_out = r_out;
     a.xn = xn;
     const int threads = norm_threads(n);
-    const int grid = (int)std::min<int64_t>(n->rows, std::max<int64_t>(1, 1024 / threads) * device_cus());
+    const int grid = (int)std::min<int64_t>(n->rows, std::max<int64_t>(1, 2048 / threads) * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);
     TraceScope tr("block_norm_fwd", s);
     auto *fn = norm_fwd_kernel(n);
-    hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), 0, s, a);
+    hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), norm_lds_bytes(n), s, a);
     return launch_status();
 }
 
@@ -1835,7 +1838,7 @@ int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     if (some) {
         TraceScope tr("block_norm_bwd", s);
         auto *fn = norm_bwd_kernel(n);
-        hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), 0, s, b);
+        hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), norm_lds_bytes(n), s, b);
         if (launch_status() != MOE_OK) return MOE_EHIP;
     }
     if (!sums) return MOE_OK;

@@ -13,13 +13,21 @@
 //   dg_post = sum_t dp yh,  dg_pre = sum_t dx' xh
 //
 // Both are one pass over the rows, bound by HBM: a workgroup takes a row at a
-// time, holds it in registers (CH chunks of 8 elements per thread) through
-// both reductions and writes it once; r' enters the pre-norm before it is
-// rounded.  The backward recomputes r' from y, r and z rather than reading
-// it, from the same bytes.  All arithmetic is fp32; every output is rounded
-// once.  The next row's loads are issued before this row's reductions.
+// time, one thread per 8 elements (two or four such chunks past H = 8192), holds it
+// in registers through both reductions and writes it once; r' enters the pre-norm
+// before it is rounded.  The backward recomputes r' from y, r and z rather than
+// reading it, from the same bytes.  All arithmetic is fp32; every output is
+// rounded once.
+//   - The next row's loads are issued before this row's reductions.  Loads return
+//     in order, so nothing else may be loaded from memory in the loop: g_post and
+//     g_pre lie in LDS.  (Both only while the registers last: up to H = 8192, the
+//     forward's loads ahead up to 16384.)
+//   - Rows are raw buffers: absent tensors are empty buffers and the last chunk's
+//     spare lanes read zeros, so the loop has no branch around a memory access and
+//     the compiler waits for exactly the loads it needs.
 #pragma once
 
+#include "buffer.hpp"
 #include "common.hpp"
 
 namespace moe {
@@ -48,47 +56,93 @@ struct NormBwdArgs {
     float *part;  // [workgroups][2][H]: each workgroup's sums of dg_post and dg_pre
 };
 
-// Eight elements as they lie in memory.
+// A row of a tensor: element size ES bytes, empty where the tensor is absent.
+template <int ES>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void *p, int64_t row, int H) {
+    return raw_buffer(static_cast<const char *>(p) + (p ? row * H * ES : 0), p ? (uint32_t)(H * ES) : 0u);
+}
+
+// The word of a row (0 where the tensor is absent).
+__device__ __forceinline__ float row_word(const void *p, int64_t i) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(raw_buffer(static_cast<const float *>(p) + (p ? i : 0), p ? 4u : 0u), 0, 0, 0));
+}
+
+// Eight elements (a chunk) as they lie in memory.
 template <bool F32>
 struct Raw8;
 template <>
 struct Raw8<false> {
     u32x4 v;
-    __device__ __forceinline__ void load(const void *p, int64_t chunk) { v = __builtin_nontemporal_load(static_cast<const u32x4 *>(p) + chunk); }
-    __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int chunk) { v = buffer_load16_nt(b, chunk * 16); }
     __device__ __forceinline__ float operator[](int i) const {
         return __uint_as_float((i & 1) ? (v[i >> 1] & 0xffff0000u) : (v[i >> 1] << 16));
     }
 };
 template <>
 struct Raw8<true> {
-    f32x4 v[2];
-    __device__ __forceinline__ void load(const void *p, int64_t chunk) {
-        v[0] = __builtin_nontemporal_load(static_cast<const f32x4 *>(p) + 2 * chunk);
-        v[1] = __builtin_nontemporal_load(static_cast<const f32x4 *>(p) + 2 * chunk + 1);
+    u32x4 v[2];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int chunk) {
+        v[0] = buffer_load16_nt(b, chunk * 32);
+        v[1] = buffer_load16_nt(b, chunk * 32 + 16);
     }
-    __device__ __forceinline__ void zero() { v[0] = v[1] = f32x4{0.f, 0.f, 0.f, 0.f}; }
-    __device__ __forceinline__ float operator[](int i) const { return v[i >> 2][i & 3]; }
+    __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(v[i >> 2][i & 3]); }
 };
 
-__device__ __forceinline__ void store8(uint16_t *p, int64_t chunk, const float (&v)[8]) {
-    reinterpret_cast<u32x4 *>(p)[chunk] =
-        u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])};
-}
-__device__ __forceinline__ void store8(float *p, int64_t chunk, const float (&v)[8]) {
-    f32x4 *o = reinterpret_cast<f32x4 *>(p) + 2 * chunk;
-    o[0] = f32x4{v[0], v[1], v[2], v[3]};
-    o[1] = f32x4{v[4], v[5], v[6], v[7]};
-}
 template <bool F32>
-__device__ __forceinline__ void store_res(void *p, int64_t chunk, const float (&v)[8]) {
-    if constexpr (F32)
-        store8(static_cast<float *>(p), chunk, v);
-    else
-        store8(static_cast<uint16_t *>(p), chunk, v);
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t b, int chunk, const float (&v)[8]) {
+    if constexpr (F32) {
+        buffer_store16(b, chunk * 32, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+        buffer_store16(b, chunk * 32 + 16, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
+    } else {
+        buffer_store16(b, chunk * 16, u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])});
+    }
 }
 
+// g_post and g_pre in LDS (1 where absent) up to H = 8192; read from L2 above.
+constexpr int kNormLdsH = 8192;
+struct NormGains {
+    const float *post, *pre;  // of global memory
+    float *lds;               // [2][H] or null
+    int H;
+    __device__ __forceinline__ void fill() const {
+        if (!lds) return;
+        for (int i = threadIdx.x; i < H; i += blockDim.x) {
+            lds[i] = post ? post[i] : 1.0f;
+            lds[H + i] = pre ? pre[i] : 1.0f;
+        }
+    }
+    template <bool LDS>
+    __device__ __forceinline__ void load(int which, int chunk, float (&g)[8]) const {
+        const float *p = which ? pre : post;
+        const f32x4 *s = reinterpret_cast<const f32x4 *>(LDS ? lds + which * H : p) + 2 * chunk;
+        if ((!LDS && !p) || chunk * 8 >= H) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = 1.0f;
+            return;
+        }
+        const f32x4 a = s[0], b = s[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = a[e], g[4 + e] = b[e];
+    }
+};
+
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+// The sum over a wave, on every lane: within rows of 16 lanes by rotations, then
+// across the four rows.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = dpp_add<0x128>(v);  // row_ror:8
+    v = dpp_add<0x124>(v);
+    v = dpp_add<0x122>(v);
+    v = dpp_add<0x121>(v);
+    v += __shfl_xor(v, 16, kWave);
+    v += __shfl_xor(v, 32, kWave);
+    return v;
+}
 
 // Sums of N values over the workgroup, in a fixed order, on every thread.  Two
 // LDS buffers in turn: a buffer is written again only after the barrier of the
@@ -100,11 +154,7 @@ struct RowSum {
     __device__ __forceinline__ explicit RowSum(float *p) : lds(p) {}
     __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-            for (int o = kWave / 2; o >= 1; o >>= 1) v[n] += __shfl_xor(v[n], o, kWave);
-        const int waves = blockDim.x / kWave;
-        if (waves == 1) return;
+        for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
         float *b = lds + turn * N * 16;
         turn ^= 1;
         if (threadIdx.x % kWave == 0)
@@ -113,41 +163,54 @@ struct RowSum {
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < N; ++n) {
+            // the 16 slots, those past the last wave zero (norm_clear)
             float s = 0.f;
-            for (int w = 0; w < waves; ++w) s += b[n * 16 + w];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const f32x4 q = reinterpret_cast<const f32x4 *>(b + n * 16)[w];
+                s += (q[0] + q[1]) + (q[2] + q[3]);
+            }
             v[n] = s;
         }
     }
 };
+__device__ __forceinline__ void norm_clear(float *red, int words) {
+    for (int i = threadIdx.x; i < words; i += blockDim.x) red[i] = 0.f;
+}
 
+// CH chunks per thread; lds: RowSum's words, then the gains.
 template <bool F32, int CH>
 __device__ __forceinline__ void norm_fwd_body(const NormArgs &a, float *lds) {
-    const int t = threadIdx.x, nt = blockDim.x, chunks = a.H / 8;
+    constexpr bool in_lds = CH == 1, ahead = CH <= 2;  // gains in LDS; the next row's loads ahead
+    constexpr int RS = F32 ? 4 : 2;
+    const int t = threadIdx.x, nt = blockDim.x, H = a.H;
     const bool post = a.g_post, pre = a.g_pre, elem = a.gate == MOE_GATE_ELEM, token = a.gate == MOE_GATE_TOKEN;
-    const float inv_h = 1.0f / (float)a.H;
+    const float inv_h = 1.0f / (float)H, alpha = a.y ? a.alpha : 1.0f;
+    const void *ze = elem ? a.z : nullptr;
     RowSum<1> sum(lds);
+    const NormGains gains{a.g_post, a.g_pre, in_lds ? lds + 32 : nullptr, H};
     Raw8<false> y[CH], z[CH];
     Raw8<F32> r[CH];
-    float zt = 0.f;
+    float zt;
     auto fetch = [&](int64_t row) {
-        const int64_t base = row * chunks;
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H), by = row_buffer<2>(a.y, row, H), bz = row_buffer<2>(ze, row, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = i * nt + t;
-            if (c < chunks) {
-                r[i].load(a.r, base + c);
-                if (a.y) y[i].load(a.y, base + c);
-                if (elem) z[i].load(a.z, base + c);
-            }
+            r[i].load(br, i * nt + t);
+            y[i].load(by, i * nt + t);
+            z[i].load(bz, i * nt + t);
         }
-        if (token) zt = static_cast<const float *>(a.z)[row];
+        zt = row_word(token ? a.z : nullptr, row);
     };
-#pragma unroll
-    for (int i = 0; i < CH; ++i) y[i].zero(), z[i].zero(), r[i].zero();
-    if (blockIdx.x < a.rows) fetch(blockIdx.x);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const int64_t base = row * chunks;
+    int64_t row = blockIdx.x;
+    if (row >= a.rows) return;
+    if (ahead) fetch(row);
+    norm_clear(lds, 32);
+    gains.fill();
+    __syncthreads();
+    for (; row < a.rows; row += gridDim.x) {
         float v[CH][8], p[CH][8], s[1] = {0.f};
+        if (!ahead) fetch(row);
         float scale = a.beta;
         if (token) scale *= sigmoid(zt);
 #pragma unroll
@@ -156,116 +219,116 @@ __device__ __forceinline__ void norm_fwd_body(const NormArgs &a, float *lds) {
             for (int e = 0; e < 8; ++e) {
                 const float yv = y[i][e];
                 s[0] = fmaf(yv, yv, s[0]);
-                p[i][e] = elem ? scale * sigmoid(z[i][e]) * yv : scale * yv;
-                v[i][e] = a.y ? a.alpha * r[i][e] : r[i][e];
+                p[i][e] = (elem ? scale * sigmoid(z[i][e]) : scale) * yv;
+                v[i][e] = alpha * r[i][e];
             }
-        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
-        float ystd = 0.f;
+        if (ahead) {
+            const int64_t next = row + gridDim.x;
+            fetch(next < a.rows ? next : row);
+        }
+        float ystd = 1.0f;
         if (post) {
             sum(s);
             ystd = __builtin_amdgcn_rsqf(fmaf(s[0], inv_h, a.eps));
         }
         s[0] = 0.f;
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r_out, row, H), bx = row_buffer<2>(a.xn, row, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = i * nt + t;
-            if (c >= chunks) continue;
-            if (post) {
-                Raw8<true> g;
-                g.load(a.g_post, c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[i][e] *= ystd * g[e];
-            }
+            float g[8];
+            gains.load<in_lds>(0, i * nt + t, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (a.y) v[i][e] += p[i][e];
+                v[i][e] = fmaf(p[i][e] * ystd, g[e], v[i][e]);
                 s[0] = fmaf(v[i][e], v[i][e], s[0]);
             }
-            if (a.r_out) store_res<F32>(a.r_out, base + c, v[i]);
+            store8<F32>(br, i * nt + t, v[i]);
         }
         float rstd = 0.f;
         if (pre) {
             sum(s);
             rstd = __builtin_amdgcn_rsqf(fmaf(s[0], inv_h, a.eps));
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = i * nt + t;
-                if (c >= chunks) continue;
-                Raw8<true> g;
-                g.load(a.g_pre, c);
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = v[i][e] * rstd * g[e];
-                store8(a.xn, base + c, x);
-            }
         }
-        if (t == 0) reinterpret_cast<float2 *>(a.stats)[row] = make_float2(ystd, rstd);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float g[8], x[8];
+            gains.load<in_lds>(1, i * nt + t, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[i][e] * rstd * g[e];
+            store8<false>(bx, i * nt + t, x);
+        }
+        if (t == 0) reinterpret_cast<float2 *>(a.stats)[row] = make_float2(post ? ystd : 0.f, rstd);
     }
 }
 
 template <bool F32, int CH>
 __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) {
+    constexpr bool in_lds = CH == 1, ahead = CH == 1;  // gains in LDS; the next row's loads ahead
+    constexpr int RS = F32 ? 4 : 2;
     const NormArgs &a = b.f;
-    const int t = threadIdx.x, nt = blockDim.x, chunks = a.H / 8;
+    const int t = threadIdx.x, nt = blockDim.x, H = a.H;
     const bool post = a.g_post, pre = a.g_pre, elem = a.gate == MOE_GATE_ELEM, token = a.gate == MOE_GATE_TOKEN;
-    const float inv_h = 1.0f / (float)a.H;
+    const float inv_h = 1.0f / (float)H, alpha = a.y ? a.alpha : 1.0f, beta = a.y ? a.beta : 0.0f;
+    const void *ze = elem ? a.z : nullptr;
     RowSum<2> sum(lds);
+    const NormGains gains{a.g_post, a.g_pre, in_lds ? lds + 64 : nullptr, H};
     Raw8<false> y[CH], z[CH], dx[CH];
     Raw8<F32> r[CH], up[CH];
-    float2 st = make_float2(0.f, 0.f);
-    float zt = 0.f;
+    float st_y, st_r, zt;
     auto fetch = [&](int64_t row) {
-        const int64_t base = row * chunks;
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H), by = row_buffer<2>(a.y, row, H), bz = row_buffer<2>(ze, row, H),
+                                     bu = row_buffer<RS>(b.dr_out, row, H), bd = row_buffer<2>(b.dxn, row, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
-            if (c < chunks) {
-                r[i].load(a.r, base + c);
-                if (a.y) y[i].load(a.y, base + c);
-                if (elem) z[i].load(a.z, base + c);
-                if (b.dr_out) up[i].load(b.dr_out, base + c);
-                if (pre) dx[i].load(b.dxn, base + c);
-            }
+            r[i].load(br, c);
+            y[i].load(by, c);
+            z[i].load(bz, c);
+            up[i].load(bu, c);
+            dx[i].load(bd, c);
         }
-        st = reinterpret_cast<const float2 *>(a.stats)[row];
-        if (token) zt = static_cast<const float *>(a.z)[row];
+        st_y = row_word(a.stats, 2 * row);
+        st_r = row_word(a.stats, 2 * row + 1);
+        zt = row_word(token ? a.z : nullptr, row);
     };
     float acc_post[CH][8], acc_pre[CH][8];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        y[i].zero(), z[i].zero(), dx[i].zero(), r[i].zero(), up[i].zero();
+    for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc_post[i][e] = acc_pre[i][e] = 0.f;
-    }
-    if (blockIdx.x < a.rows) fetch(blockIdx.x);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const int64_t base = row * chunks;
-        const float ystd = post ? st.x : 1.0f, rstd = st.y;
+    int64_t row = blockIdx.x;
+    if (row >= a.rows) return;
+    if (ahead) fetch(row);
+    norm_clear(lds, 64);
+    gains.fill();
+    __syncthreads();
+    for (; row < a.rows; row += gridDim.x) {
+        if (!ahead) fetch(row);
+        const float ystd = post ? st_y : 1.0f, rstd = st_r;
         const float gt = token ? sigmoid(zt) : 1.0f;
         // yh, the gate, D (first what arrives for r'), t and xh of the row
         float yh[CH][8], gv[CH][8], D[CH][8], tv[CH][8], xh[CH][8], s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = i * nt + t;
-            if (c >= chunks) continue;
-            Raw8<true> go, gi;
-            if (post) go.load(a.g_post, c);
-            if (pre) gi.load(a.g_pre, c);
+            float go[8], gi[8];
+            gains.load<in_lds>(0, i * nt + t, go);
+            gains.load<in_lds>(1, i * nt + t, gi);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 yh[i][e] = y[i][e] * ystd;
                 gv[i][e] = elem ? sigmoid(z[i][e]) : gt;
                 D[i][e] = up[i][e];
-                const float p = post ? yh[i][e] * go[e] : yh[i][e];
-                const float rn = a.y ? fmaf(a.beta * gv[i][e], p, a.alpha * r[i][e]) : r[i][e];
-                xh[i][e] = rn * rstd;
+                xh[i][e] = fmaf(beta * gv[i][e], yh[i][e] * go[e], alpha * r[i][e]) * rstd;
                 const float d = dx[i][e];
-                tv[i][e] = pre ? d * gi[e] : 0.f;
+                tv[i][e] = d * gi[e];
                 acc_pre[i][e] = fmaf(d, xh[i][e], acc_pre[i][e]);
                 s[0] = fmaf(tv[i][e], xh[i][e], s[0]);
             }
         }
-        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        if (ahead) {
+            const int64_t next = row + gridDim.x;
+            fetch(next < a.rows ? next : row);
+        }
         if (pre) {
             sum(s);
             const float c1 = s[0] * inv_h;
@@ -275,53 +338,46 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
                 for (int e = 0; e < 8; ++e) D[i][e] = fmaf(rstd, fmaf(-xh[i][e], c1, tv[i][e]), D[i][e]);
         }
         s[0] = s[1] = 0.f;
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(b.dr, row, H), by = row_buffer<2>(b.dy, row, H),
+                                     bz = row_buffer<2>(elem ? b.dz : nullptr, row, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
-            if (c >= chunks) continue;
-            float o[8];
+            float o[8], go[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = a.y ? a.alpha * D[i][e] : D[i][e];
-            store_res<F32>(b.dr, base + c, o);
-            if (!a.y) continue;
-            Raw8<true> go;
-            if (post) go.load(a.g_post, c);
+            for (int e = 0; e < 8; ++e) o[e] = alpha * D[i][e];
+            store8<F32>(br, c, o);
+            gains.load<in_lds>(0, c, go);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = a.beta * D[i][e];
-                const float p = post ? yh[i][e] * go[e] : yh[i][e];
+                const float d = beta * D[i][e], p = yh[i][e] * go[e];
                 o[e] = d * p * gv[i][e] * (1.0f - gv[i][e]);
                 s[1] = fmaf(d, p, s[1]);
                 const float dp = d * gv[i][e];
                 acc_post[i][e] = fmaf(dp, yh[i][e], acc_post[i][e]);
-                D[i][e] = post ? dp * go[e] : dp;  // q
+                D[i][e] = dp * go[e];  // q
                 s[0] = fmaf(D[i][e], yh[i][e], s[0]);
             }
-            if (elem) store8(static_cast<uint16_t *>(b.dz), base + c, o);
+            store8<false>(bz, c, o);
         }
         if (post || token) sum(s);
-        if (a.y) {
-            const float c2 = post ? s[0] * inv_h : 0.f;
+        const float c2 = post ? s[0] * inv_h : 0.f;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = i * nt + t;
-                if (c >= chunks) continue;
-                float o[8];
+        for (int i = 0; i < CH; ++i) {
+            float o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = ystd * fmaf(-yh[i][e], c2, D[i][e]);
-                store8(b.dy, base + c, o);
-            }
+            for (int e = 0; e < 8; ++e) o[e] = ystd * fmaf(-yh[i][e], c2, D[i][e]);
+            store8<false>(by, i * nt + t, o);
         }
         if (token && t == 0) static_cast<float *>(b.dz)[row] = s[1] * gt * (1.0f - gt);
     }
     if (post || pre) {
-        float *o = b.part + (int64_t)blockIdx.x * 2 * a.H;
+        const __amdgpu_buffer_rsrc_t bo = row_buffer<4>(post ? b.part : nullptr, 2 * (int64_t)blockIdx.x, H),
+                                     bi = row_buffer<4>(pre ? b.part : nullptr, 2 * (int64_t)blockIdx.x + 1, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = i * nt + t;
-            if (c >= chunks) continue;
-            if (post) store8(o, c, acc_post[i]);
-            if (pre) store8(o + a.H, c, acc_pre[i]);
+            store8<true>(bo, i * nt + t, acc_post[i]);
+            store8<true>(bi, i * nt + t, acc_pre[i]);
         }
     }
 }
