@@ -1742,8 +1742,6 @@ int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, c
 
 namespace {
 
-constexpr int kNormGroups = 512;  // workgroups of the backward at most: each leaves one row of partial sums
-
 int norm_check(const moe_norm_desc *n) {
     if (!n || n->rows < 0 || n->H < 1 || n->gate < MOE_GATE_NONE || n->gate > MOE_GATE_ELEM || !(n->eps >= 0.0f) ||
         (n->res_fp32 != 0 && n->res_fp32 != 1))
@@ -1752,17 +1750,20 @@ int norm_check(const moe_norm_desc *n) {
     return MOE_OK;
 }
 
-int64_t norm_groups(const moe_norm_desc *n) { return std::min<int64_t>(n->rows, kNormGroups); }
-int64_t norm_ws_bytes(const moe_norm_desc *n) { return align256(norm_groups(n) * 2 * n->H * 4); }
-
 // Chunks of 8 elements per thread, the threads of a row's workgroup, and its LDS
 // (the sums' slots, and the gains with one chunk per thread).
 int norm_chunks(const moe_norm_desc *n) { return n->H <= kNormLdsH ? 1 : n->H <= 2 * kNormLdsH ? 2 : 4; }
-size_t norm_lds_bytes(const moe_norm_desc *n) { return 256 + (norm_chunks(n) == 1 ? 8 * (size_t)n->H : 0); }
 int norm_threads(const moe_norm_desc *n) {
     const int per = 8 * 64 * norm_chunks(n);
     return 64 * ((n->H + per - 1) / per);
 }
+// Workgroups of the backward: those that a 256-CU part holds at once (16 waves per
+// CU at its registers), at most 512; each leaves one row of partial sums.
+int64_t norm_groups(const moe_norm_desc *n) {
+    return std::min<int64_t>(n->rows, 256 * std::max(1, std::min(2, 1024 / norm_threads(n))));
+}
+int64_t norm_ws_bytes(const moe_norm_desc *n) { return align256(norm_groups(n) * 2 * n->H * 4); }
+size_t norm_lds_bytes(const moe_norm_desc *n) { return 256 + (norm_chunks(n) == 1 ? 8 * (size_t)n->H : 0); }
 
 auto *norm_fwd_kernel(const moe_norm_desc *n) {
     const int ch = norm_chunks(n);
@@ -1805,7 +1806,7 @@ int moe_block_norm_fwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     a.r_out = r_out;
     a.xn = xn;
     const int threads = norm_threads(n);
-    const int grid = (int)std::min<int64_t>(n->rows, std::max<int64_t>(1, 2048 / threads) * device_cus());
+    const int grid = (int)std::min<int64_t>(n->rows, std::max<int64_t>(1, 1024 / threads) * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);
     TraceScope tr("block_norm_fwd", s);
     auto *fn = norm_fwd_kernel(n);

@@ -56,15 +56,18 @@ struct NormBwdArgs {
     float *part;  // [workgroups][2][H]: each workgroup's sums of dg_post and dg_pre
 };
 
-// A row of a tensor: element size ES bytes, empty where the tensor is absent.
+// A row of a tensor: element size ES bytes, empty where the tensor is absent
+// (or not `in` use).
 template <int ES>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void *p, int64_t row, int H) {
-    return raw_buffer(static_cast<const char *>(p) + (p ? row * H * ES : 0), p ? (uint32_t)(H * ES) : 0u);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void *p, int64_t row, int H, bool in = true) {
+    in = in && p;
+    return raw_buffer(static_cast<const char *>(p) + (in ? row * H * ES : 0), in ? (uint32_t)(H * ES) : 0u);
 }
 
 // The word of a row (0 where the tensor is absent).
-__device__ __forceinline__ float row_word(const void *p, int64_t i) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(raw_buffer(static_cast<const float *>(p) + (p ? i : 0), p ? 4u : 0u), 0, 0, 0));
+__device__ __forceinline__ float row_word(const void *p, int64_t i, bool in) {
+    in = in && p;
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(raw_buffer(static_cast<const float *>(p) + (in ? i : 0), in ? 4u : 0u), 0, 0, 0));
 }
 
 // Eight elements (a chunk) as they lie in memory.
@@ -104,12 +107,15 @@ struct NormGains {
     const float *post, *pre;  // of global memory
     float *lds;               // [2][H] or null
     int H;
+    // every thread its own chunk, which no other reads
     __device__ __forceinline__ void fill() const {
-        if (!lds) return;
-        for (int i = threadIdx.x; i < H; i += blockDim.x) {
-            lds[i] = post ? post[i] : 1.0f;
-            lds[H + i] = pre ? pre[i] : 1.0f;
-        }
+        const int c = threadIdx.x;
+        if (!lds || c * 8 >= H) return;
+        const f32x4 one = f32x4{1.f, 1.f, 1.f, 1.f};
+        f32x4 *o = reinterpret_cast<f32x4 *>(lds) + 2 * c, *p = reinterpret_cast<f32x4 *>(lds + H) + 2 * c;
+        const f32x4 *a = reinterpret_cast<const f32x4 *>(post) + 2 * c, *b = reinterpret_cast<const f32x4 *>(pre) + 2 * c;
+        const f32x4 v[4] = {post ? a[0] : one, post ? a[1] : one, pre ? b[0] : one, pre ? b[1] : one};
+        o[0] = v[0], o[1] = v[1], p[0] = v[2], p[1] = v[3];
     }
     template <bool LDS>
     __device__ __forceinline__ void load(int which, int chunk, float (&g)[8]) const {
@@ -192,25 +198,26 @@ __device__ __forceinline__ void norm_fwd_body(const NormArgs &a, float *lds) {
     Raw8<false> y[CH], z[CH];
     Raw8<F32> r[CH];
     float zt;
-    auto fetch = [&](int64_t row) {
-        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H), by = row_buffer<2>(a.y, row, H), bz = row_buffer<2>(ze, row, H);
+    auto fetch = [&](int64_t row, bool in) {
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H, in), by = row_buffer<2>(a.y, row, H, in),
+                                     bz = row_buffer<2>(ze, row, H, in);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             r[i].load(br, i * nt + t);
             y[i].load(by, i * nt + t);
             z[i].load(bz, i * nt + t);
         }
-        zt = row_word(token ? a.z : nullptr, row);
+        zt = row_word(token ? a.z : nullptr, row, in);
     };
     int64_t row = blockIdx.x;
     if (row >= a.rows) return;
-    if (ahead) fetch(row);
+    if (ahead) fetch(row, true);
     norm_clear(lds, 32);
     gains.fill();
     __syncthreads();
     for (; row < a.rows; row += gridDim.x) {
         float v[CH][8], p[CH][8], s[1] = {0.f};
-        if (!ahead) fetch(row);
+        if (!ahead) fetch(row, true);
         float scale = a.beta;
         if (token) scale *= sigmoid(zt);
 #pragma unroll
@@ -222,10 +229,7 @@ __device__ __forceinline__ void norm_fwd_body(const NormArgs &a, float *lds) {
                 p[i][e] = (elem ? scale * sigmoid(z[i][e]) : scale) * yv;
                 v[i][e] = alpha * r[i][e];
             }
-        if (ahead) {
-            const int64_t next = row + gridDim.x;
-            fetch(next < a.rows ? next : row);
-        }
+        if (ahead) fetch(row + gridDim.x, row + gridDim.x < a.rows);
         float ystd = 1.0f;
         if (post) {
             sum(s);
@@ -275,9 +279,10 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
     Raw8<false> y[CH], z[CH], dx[CH];
     Raw8<F32> r[CH], up[CH];
     float st_y, st_r, zt;
-    auto fetch = [&](int64_t row) {
-        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H), by = row_buffer<2>(a.y, row, H), bz = row_buffer<2>(ze, row, H),
-                                     bu = row_buffer<RS>(b.dr_out, row, H), bd = row_buffer<2>(b.dxn, row, H);
+    auto fetch = [&](int64_t row, bool in) {
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H, in), by = row_buffer<2>(a.y, row, H, in),
+                                     bz = row_buffer<2>(ze, row, H, in), bu = row_buffer<RS>(b.dr_out, row, H, in),
+                                     bd = row_buffer<2>(b.dxn, row, H, in);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
@@ -287,9 +292,9 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
             up[i].load(bu, c);
             dx[i].load(bd, c);
         }
-        st_y = row_word(a.stats, 2 * row);
-        st_r = row_word(a.stats, 2 * row + 1);
-        zt = row_word(token ? a.z : nullptr, row);
+        st_y = row_word(a.stats, 2 * row, in);
+        st_r = row_word(a.stats, 2 * row + 1, in);
+        zt = row_word(token ? a.z : nullptr, row, in);
     };
     float acc_post[CH][8], acc_pre[CH][8];
 #pragma unroll
@@ -298,12 +303,12 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
         for (int e = 0; e < 8; ++e) acc_post[i][e] = acc_pre[i][e] = 0.f;
     int64_t row = blockIdx.x;
     if (row >= a.rows) return;
-    if (ahead) fetch(row);
+    if (ahead) fetch(row, true);
     norm_clear(lds, 64);
     gains.fill();
     __syncthreads();
     for (; row < a.rows; row += gridDim.x) {
-        if (!ahead) fetch(row);
+        if (!ahead) fetch(row, true);
         const float ystd = post ? st_y : 1.0f, rstd = st_r;
         const float gt = token ? sigmoid(zt) : 1.0f;
         // yh, the gate, D (first what arrives for r'), t and xh of the row
@@ -325,10 +330,7 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
                 s[0] = fmaf(tv[i][e], xh[i][e], s[0]);
             }
         }
-        if (ahead) {
-            const int64_t next = row + gridDim.x;
-            fetch(next < a.rows ? next : row);
-        }
+        if (ahead) fetch(row + gridDim.x, row + gridDim.x < a.rows);
         if (pre) {
             sum(s);
             const float c1 = s[0] * inv_h;
@@ -383,15 +385,21 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
 }
 
 // dg[c] = the sum over the backward's workgroups of their partial sums:
-// 64 columns x 16 groups of workgroups, each group in ascending order, then
-// the groups in a fixed tree.
+// 64 columns x 16 groups of workgroups, each group in ascending order (eight
+// loads at a time), then the groups in a fixed tree.
 __device__ __forceinline__ void norm_dg_body(const float *part, int groups, int H, float *dg_post, float *dg_pre, float *lds) {
     const int col = blockIdx.x * 64 + threadIdx.x % 64, g0 = threadIdx.x / 64;
     float *out = blockIdx.y ? dg_pre : dg_post;
     if (!out) return;  // the whole workgroup
     float s = 0.f;
     if (col < H)
-        for (int g = g0; g < groups; g += 16) s += part[((int64_t)g * 2 + blockIdx.y) * H + col];
+        for (int g = g0; g < groups; g += 16 * 8) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = g + 16 * k < groups ? part[((int64_t)(g + 16 * k) * 2 + blockIdx.y) * H + col] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
     lds[threadIdx.x] = s;
     __syncthreads();
     for (int o = 8; o >= 1; o >>= 1) {
