@@ -144,16 +144,33 @@ def _dev(t):
 
 
 def _buf(name: str, t, dtype, n: int, ref=None):
-    """_dev with the size the call will touch: at least n elements of dtype on
-    ref's device (None stays NULL)."""
+    """Device pointer of a tensor that the call will touch n elements of: on
+    ref's device (a GPU), contiguous, of dtype, at least that large; None stays
+    NULL."""
     if t is None:
         return None
-    p = _dev(t)
-    if t.dtype != dtype or t.numel() < n:
-        raise ValueError(f"{name}: needs {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
-    if ref is not None and t.device != ref.device:
-        raise ValueError(f"{name}: on {t.device}, the other buffers on {ref.device}")
-    return p
+    if (t.dtype != dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda or
+            (ref is not None and t.get_device() != ref.get_device())):
+        _dev(t)
+        where = "" if ref is None else f" on {ref.device}"
+        raise ValueError(f"{name}: needs {n} elements of {dtype}{where}, got {t.numel()} of {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _run(where: str, ref: torch.Tensor, stream, *args) -> int:
+    """Calls entry point `where` with ref's device current, on `stream` or that
+    device's current stream."""
+    fn, dev = getattr(load(), where), ref.get_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    return _check(rc, where)
 
 
 def _stream(stream, ref: torch.Tensor):
@@ -583,20 +600,15 @@ def _few_args(d, Is, routes, w, X, S13, S2, out, ws):
 def moe_layer_fwd_few(d, Is, routes, w, X, W13, W2, S13, S2, out, ws, stream=None):
     head, tail = _few_args(d, Is, routes, w, X, S13, S2, out, ws)
     n, bf = d.L * d.I * d.H, torch.bfloat16
-    with torch.cuda.device(X.device):
-        rc = load().moe_layer_fwd_few(ctypes.byref(d), Is, *head, _buf("W13", W13, bf, 2 * n, X), _buf("W2", W2, bf, n, X),
-                                      *tail, _stream(stream, X))
-    return _check(rc, "moe_layer_fwd_few")
+    return _run("moe_layer_fwd_few", X, stream, ctypes.byref(d), Is, *head, _buf("W13", W13, bf, 2 * n, X),
+                _buf("W2", W2, bf, n, X), *tail)
 
 
 def moe_layer_fwd_few_mx(d, Is, routes, w, X, W13q, W13s, W2q, W2s, S13, S2, out, ws, stream=None):
     head, tail = _few_args(d, Is, routes, w, X, S13, S2, out, ws)
     n, u8 = d.L * d.I * d.H, torch.uint8
-    with torch.cuda.device(X.device):
-        rc = load().moe_layer_fwd_few_mx(ctypes.byref(d), Is, *head, _buf("W13q", W13q, u8, 2 * n, X),
-                                         _buf("W13s", W13s, u8, 2 * n // 32, X), _buf("W2q", W2q, u8, n, X),
-                                         _buf("W2s", W2s, u8, n // 32, X), *tail, _stream(stream, X))
-    return _check(rc, "moe_layer_fwd_few_mx")
+    return _run("moe_layer_fwd_few_mx", X, stream, ctypes.byref(d), Is, *head, _buf("W13q", W13q, u8, 2 * n, X),
+                _buf("W13s", W13s, u8, 2 * n // 32, X), _buf("W2q", W2q, u8, n, X), _buf("W2s", W2s, u8, n // 32, X), *tail)
 
 
 @dataclass
@@ -652,9 +664,7 @@ def moe_block_norm_fwd(n, y, r, z, g_post, g_pre, r_out, xn, stats, stream=None)
     args = _norm_inputs(n, y, r, z, g_post, g_pre)
     args += [_buf("r_out", r_out, r.dtype, e, r), _buf("xn", xn, torch.bfloat16, e, r),
              _buf("stats", stats, torch.float32, 2 * n.rows, r)]
-    with torch.cuda.device(r.device):
-        rc = load().moe_block_norm_fwd(ctypes.byref(n), *args, _stream(stream, r))
-    return _check(rc, "moe_block_norm_fwd")
+    return _run("moe_block_norm_fwd", r, stream, ctypes.byref(n), *args)
 
 
 def moe_block_norm_bwd(n, y, r, z, g_post, g_pre, stats, dr_out, dxn, dy, dr, dz, dg_post, dg_pre, ws, stream=None):
@@ -665,9 +675,7 @@ def moe_block_norm_bwd(n, y, r, z, g_post, g_pre, stats, dr_out, dxn, dy, dr, dz
              _buf("dy", dy, bf, e, r), _buf("dr", dr, r.dtype, e, r),
              _buf("dz", dz, bf if elem else f32, e if elem else n.rows, r), _buf("dg_post", dg_post, f32, n.H, r),
              _buf("dg_pre", dg_pre, f32, n.H, r), _buf("ws", ws, torch.uint8, 0, r)]
-    with torch.cuda.device(r.device):
-        rc = load().moe_block_norm_bwd(ctypes.byref(n), *args, 0 if ws is None else ws.numel(), _stream(stream, r))
-    return _check(rc, "moe_block_norm_bwd")
+    return _run("moe_block_norm_bwd", r, stream, ctypes.byref(n), *args, 0 if ws is None else ws.numel())
 
 
 @dataclass
@@ -712,9 +720,7 @@ def moe_ckpt_pack(src, q, scales, nrows=None, stream=None):
     rows, cols = src.shape
     args = [_buf("src", src, torch.bfloat16, 0), rows, cols, _buf("nrows", nrows, torch.int32, 1, src),
             _buf("q", q, torch.int8, rows * cols, src), _buf("scales", scales, torch.float32, rows * (cols // CKPT_BLOCK), src)]
-    with torch.cuda.device(src.device):
-        rc = load().moe_ckpt_pack(*args, _stream(stream, src))
-    return _check(rc, "moe_ckpt_pack")
+    return _run("moe_ckpt_pack", src, stream, *args)
 
 
 def ckpt_pack(src, nrows=None, stream=None):
@@ -731,9 +737,7 @@ def moe_ckpt_swiglu_bwd(q, scales, dA, wrow, dHU, A, dw, nrows=None, stream=None
     args = [_buf("q", q, torch.int8, 2 * rows * I, dA), _buf("scales", scales, f32, 2 * rows * I // CKPT_BLOCK, dA),
             _buf("dA", dA, bf, 0), _buf("wrow", wrow, f32, rows, dA), rows, I, _buf("nrows", nrows, torch.int32, 1, dA),
             _buf("dHU", dHU, bf, 2 * rows * I, dA), _buf("A", A, bf, rows * I, dA), _buf("dw", dw, f32, rows, dA)]
-    with torch.cuda.device(dA.device):
-        rc = load().moe_ckpt_swiglu_bwd(*args, _stream(stream, dA))
-    return _check(rc, "moe_ckpt_swiglu_bwd")
+    return _run("moe_ckpt_swiglu_bwd", dA, stream, *args)
 
 
 def moe_layer_bwd_ckpt(d, dOut, w, X, phi, route_row, seg_off, q, scales, W13, W2, dX, dW13, dW2, dw, ws, stream=None):
@@ -745,6 +749,4 @@ def moe_layer_bwd_ckpt(d, dOut, w, X, phi, route_row, seg_off, q, scales, W13, W
             _buf("scales", scales, f32, cap * 2 * I // CKPT_BLOCK, X), _buf("W13", W13, bf, d.L * 2 * I * H, X),
             _buf("W2", W2, bf, d.L * H * I, X), _buf("dX", dX, bf, n * H, X), _buf("dW13", dW13, f32, d.L * 2 * I * H, X),
             _buf("dW2", dW2, f32, d.L * H * I, X), _buf("dw", dw, f32, n * d.K, X), _buf("ws", ws, torch.uint8, 0, X)]
-    with torch.cuda.device(X.device):
-        rc = load().moe_layer_bwd_ckpt(ctypes.byref(d), *args, ws.numel(), _stream(stream, X))
-    return _check(rc, "moe_layer_bwd_ckpt")
+    return _run("moe_layer_bwd_ckpt", X, stream, ctypes.byref(d), *args, ws.numel())
