@@ -6,10 +6,10 @@
 //            ascending j, in fp32                -> out (bf16, one rounding)
 //
 // With a few routes per expert both products read each weight once and use it
-// for at most a few dozen columns, so the time is the weights' HBM read: a
-// 16 x 16 x 32 MFMA takes 1 KiB of weights in 16 cycles, some 25 times the
-// rate at which a CU's share of HBM delivers them.  Everything here is laid
-// out for that read:
+// for at most a few dozen columns, so the time is the weights' HBM read: the
+// MFMAs of a CU could take 1 KiB of weights every 4 cycles for 8 routes, some 20
+// times the rate at which its share of HBM delivers them.  Everything here is
+// laid out for that read:
 //   - the weights are the MFMA's A operand, straight from HBM to registers in
 //     whole 128-byte lines (FewLane); nothing is staged, so no barrier stands
 //     in the stream, and steps are loaded ahead in registers;
@@ -21,6 +21,21 @@
 //   - only experts that a route names are read: every gate/up workgroup builds
 //     the list of them from the routes, so no schedule launch comes first.
 // No atomics touch a float: the result does not depend on timing.
+//
+// The activations' rounding to bf16 is the layer forward's own (and one of two
+// roundings: the experts' sums stay fp32 to the output).  Keeping them as a high
+// and a low bf16, which halves the output's error variance, doubles the down
+// launch's token loads: 36.6 us against 36.2 for 8 tokens of the full-size share,
+// but 264 against 241 for 128 and 78 against 61 for 32 with MXFP8 weights.
+//
+// Measured (launches alone; a read-only kernel gets 7.1 TB/s; each launch spends
+// about 5 us before its stream flows and after it ends):
+//   full-size share (H = 7168, I = 2048, 48 local experts, top-8 of 384)
+//     8 tokens, 8 experts hit    gate/up 70 us (6.7 TB/s)   down 39 us (6.0 TB/s)
+//     128 tokens + shared expert gate/up 427 us (6.5 TB/s)  down 240 us (5.7 TB/s)
+//     32 tokens, MXFP8           gate/up 108 us (6.4 TB/s)  down 62 us (5.6 TB/s)
+//   H = 2048, I = 1024, 64 experts, 37 tokens + shared expert
+//                                gate/up 90 us (5.9 TB/s)   down 47 us (5.7 TB/s)
 #pragma once
 
 #include "buffer.hpp"
