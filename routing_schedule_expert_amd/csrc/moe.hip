@@ -232,9 +232,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_norm_bwd(NormBwdArgs a) {
     norm_bwd_body<F32, CH>(a, norm_smem);
 }
 
-__global__ __launch_bounds__(1024) void k_norm_dg(const float *part, int groups, int H, float *dg_post, float *dg_pre) {
+template <int COLS>
+__global__ __launch_bounds__(1024) void k_norm_dg(const float *part, int parts, int H, float *dg_post, float *dg_pre) {
     __shared__ float lds[1024];
-    norm_dg_body(part, groups, H, dg_post, dg_pre, lds);
+    norm_dg_body<COLS>(part, parts, H, dg_post, dg_pre, lds);
 }
 
 __global__ __launch_bounds__(kCkptThreads) void k_ckpt_pack(const uint16_t *src, int64_t rows, int cols,
@@ -1757,10 +1758,15 @@ int norm_threads(const moe_norm_desc *n) {
     const int per = 8 * 64 * norm_chunks(n);
     return 64 * ((n->H + per - 1) / per);
 }
-// Workgroups of the backward: those that a 256-CU part holds at once (16 waves per
-// CU at its registers), at most 512; each leaves one row of partial sums.
+// Workgroups of the backward, each leaving one row of partial sums.  At few waves
+// (H <= 1536) many, each with four rows at least, or the CUs run dry between rows
+// (30,000 rows of 640: 76 us with 2048, 140 with 512); above, those that a
+// 256-CU part holds at once, at most 512 (4,095 rows of 2,056, fp32: 44 us against 54
+// with 768 and 56 with 256).
 int64_t norm_groups(const moe_norm_desc *n) {
-    return std::min<int64_t>(n->rows, 256 * std::max(1, std::min(2, 1024 / norm_threads(n))));
+    const int waves = norm_threads(n) / 64;
+    if (waves <= 3) return std::min<int64_t>((n->rows + 3) / 4, waves <= 2 ? 2048 : 1024);
+    return std::min<int64_t>(n->rows, waves <= 8 ? 512 : 256);
 }
 int64_t norm_ws_bytes(const moe_norm_desc *n) { return align256(norm_groups(n) * 2 * n->H * 4); }
 size_t norm_lds_bytes(const moe_norm_desc *n) { return 256 + (norm_chunks(n) == 1 ? 8 * (size_t)n->H : 0); }
@@ -1844,13 +1850,22 @@ int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     }
     if (!sums) return MOE_OK;
     TraceScope tr("block_norm_dg", s);
-    hipLaunchKernelGGL(k_norm_dg, dim3((n->H + 63) / 64, 2), dim3(1024), 0, s, b.part, grid, n->H, dg_post, dg_pre);
+    if (n->H <= 1024)  // few columns: fewer of them and more partial rows to a workgroup
+        hipLaunchKernelGGL(k_norm_dg<16>, dim3((n->H + 15) / 16, 2), dim3(1024), 0, s, b.part, grid, n->H, dg_post, dg_pre);
+    else
+        hipLaunchKernelGGL(k_norm_dg<64>, dim3((n->H + 63) / 64, 2), dim3(1024), 0, s, b.part, grid, n->H, dg_post, dg_pre);
     return launch_status();
 }
 
 // ---------------------------------------------------------------------------
 // Activation checkpoints in 8 bits.
 // ---------------------------------------------------------------------------
+
+// Workgroups per CU of the two passes at most.  One pass without a loop streams
+// best (61,440 rows of I = 2048: pack 132 us, backward 244; 8 per CU, looping: 151
+// and 263; 64: 139 and 244), but rows past *nrows cost their workgroups all the same
+// (300 rows in buffers of 470,992: 100 and 28 us, against 6 and 6).
+static constexpr int64_t kCkptGrid = 64;
 
 int moe_ckpt_pack(const uint16_t *src, int64_t rows, int32_t cols, const int32_t *nrows, int8_t *q, float *scales,
                   void *stream) {
@@ -1859,7 +1874,7 @@ int moe_ckpt_pack(const uint16_t *src, int64_t rows, int32_t cols, const int32_t
     if (!src || !q || !scales || !aligned16(src) || !aligned16(q) || !aligned4(scales) || !aligned4(nrows))
         return MOE_EINVAL;
     const int64_t n = rows * (cols / 16);
-    const int grid = (int)std::min<int64_t>((n + kCkptThreads - 1) / kCkptThreads, 8ll * device_cus());
+    const int grid = (int)std::min<int64_t>((n + kCkptThreads - 1) / kCkptThreads, kCkptGrid * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);
     TraceScope tr("ckpt_pack", s);
     hipLaunchKernelGGL(k_ckpt_pack, dim3(grid), dim3(kCkptThreads), 0, s, src, rows, cols, nrows, q, scales);
@@ -1875,7 +1890,7 @@ int moe_ckpt_swiglu_bwd(const int8_t *q, const float *scales, const uint16_t *dA
         return MOE_EINVAL;
     const int lanes = I >= 1024 ? 64 : I >= 512 ? 32 : I >= 256 ? 16 : 8;
     const int64_t wgs = (rows * lanes + kCkptThreads - 1) / kCkptThreads;
-    const int grid = (int)std::min<int64_t>(wgs, 8ll * device_cus());
+    const int grid = (int)std::min<int64_t>(wgs, kCkptGrid * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);
     TraceScope tr("ckpt_swiglu_bwd", s);
     auto *fn = lanes == 64   ? k_ckpt_swiglu_bwd<64>

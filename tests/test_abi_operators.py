@@ -76,6 +76,8 @@ def test_norm_sizes():
     assert ops.block_norm_workspace_bytes(norm_desc()) == 16 * 2 * 7168 * 4
     assert ops.block_norm_workspace_bytes(norm_desc(rows=1 << 20)) == 256 * 2 * 7168 * 4
     assert ops.block_norm_workspace_bytes(norm_desc(rows=1 << 20, H=2048)) == 512 * 2 * 2048 * 4
+    assert ops.block_norm_workspace_bytes(norm_desc(rows=1 << 20, H=512)) == 2048 * 2 * 512 * 4
+    assert ops.block_norm_workspace_bytes(norm_desc(rows=5, H=512)) == 2 * 2 * 512 * 4
     assert ops.block_norm_workspace_bytes(norm_desc(rows=0)) == 0
     for bad in (norm_desc(rows=-1), norm_desc(H=0), norm_desc(H=7164), norm_desc(H=32776), norm_desc(gate=3), norm_desc(gate=-1),
                 norm_desc(eps=-1e-6), norm_desc(eps=float("nan"))):

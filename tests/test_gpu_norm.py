@@ -173,10 +173,11 @@ def test_norm_before_the_first_block(res, rows, H):
     check(c)
 
 
-@pytest.mark.parametrize("rows", [511, 512, 513, 2500])
+@pytest.mark.parametrize("rows", [511, 512, 513, 2500, 9001])
 def test_norm_many_rows(rows):
     # more rows than workgroups of the backward; every column sum in its order
     check(make(rows, 256, "token"))
+    check(make(rows, 1032, "none", seed=3))
 
 
 def test_norm_repeats_bitwise():
