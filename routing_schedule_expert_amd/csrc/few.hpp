@@ -453,7 +453,7 @@ __device__ __forceinline__ float few_sum(const f32x4 &acc) {
 
 __device__ __forceinline__ int wave_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// A unit of the gate/up launch: activation columns [i0, i0 + 16) of one expert
+// A unit of the gate/up launch: activation columns [i0, i0 + 4 M) of one expert
 // (W, with `inner` activation columns) for its `n` routes.  The routes' tokens
 // are route[..] / K, their activations go to row route[..] of act; route null:
 // the tokens themselves (shared expert), rows R + token.
@@ -467,9 +467,8 @@ __device__ __forceinline__ int few_token(const FewArgs &a, const int *route, int
 template <class T>
 __device__ __forceinline__ int few_act_row(const FewArgs &a, const T *route, int k) { return route ? (int)route[k] : a.R + k; }
 
-constexpr int kFewGateupBlocks = 4;  // two of gate rows, two of up rows
-
-// Operands of a unit's routes from `first` on.
+// Operands of a unit's routes from `first` on: M / 2 blocks of gate rows, M / 2 of
+// up rows.
 template <bool MX, int NT>
 __device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX> &l,
                                                 FewItem<2, NT> &it) {
@@ -484,9 +483,9 @@ __device__ __forceinline__ void few_gateup_item(const FewArgs &a, const FewUnit 
 
 // The waves' sums of a unit meet in LDS (red), 32 tokens at a time, and are
 // added in wave order; then the activation, rounded once.
-template <bool MX, int NT>
+template <bool MX, int M, int NT>
 __device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit &u, int first, const FewLane<MX> &l,
-                                                const f32x4 (&acc)[kFewGateupBlocks][NT], float *red) {
+                                                const f32x4 (&acc)[M][NT], float *red) {
     using L = FewLane<MX>;
     constexpr int per = 32 / L::kTokens;  // tiles that meet at a time
     const int t = threadIdx.x, wave = t >> 6;
@@ -497,11 +496,11 @@ __device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit 
         for (int q = q0; q < (q0 + per < NT ? q0 + per : NT); ++q) {
             float *dst = red + (wave * 32 + (q - q0) * L::kTokens + l.token) * kFewRedLd + few_sum_row();
 #pragma unroll
-            for (int m = 0; m < kFewGateupBlocks; ++m) dst[m * L::kRows] = few_sum(acc[m][q]);
+            for (int m = 0; m < M; ++m) dst[(m < M / 2 ? 0 : 16) + m % (M / 2) * L::kRows] = few_sum(acc[m][q]);
         }
         __syncthreads();
         const int tok = t >> 4, i = t & 15, k = first + q0 * L::kTokens + tok;
-        if (tok < (NT - q0) * L::kTokens && k < u.n) {
+        if (i < 4 * M && tok < (NT - q0) * L::kTokens && k < u.n) {
             float gate = 0.f, up = 0.f;
 #pragma unroll
             for (int v = 0; v < kFewWaves; ++v) {
@@ -516,16 +515,15 @@ __device__ __forceinline__ void few_gateup_join(const FewArgs &a, const FewUnit 
 
 // `count` units (unit(i) for i in turn), all with at most NT tiles of routes
 // from `first` on, the waves splitting H.
-template <bool MX, int NT, class Unit>
+template <bool MX, int M, int NT, class Unit>
 __device__ __forceinline__ void few_gateup_run(const FewArgs &a, int count, int first, Unit unit, float *red) {
     using L = FewLane<MX>;
-    constexpr int M = kFewGateupBlocks;
     const L l;
     const int wave = wave_uniform(threadIdx.x >> 6), steps = a.H / L::kStep;
     const int k0 = wave * steps / kFewWaves, n = (wave + 1) * steps / kFewWaves - k0;
     few_stream<MX, M, 2, NT, kFewGateupRegs, false>(
         l, FewRun::make(l, a.H, a.X), k0, n, count, [&](int i, FewItem<2, NT> &it) { few_gateup_item<MX, NT>(a, unit(i), first, l, it); },
-        [&](int i, const f32x4(&acc)[M][NT]) { few_gateup_join<MX, NT>(a, unit(i), first, l, acc, red); });
+        [&](int i, const f32x4(&acc)[M][NT]) { few_gateup_join<MX, M, NT>(a, unit(i), first, l, acc, red); });
 }
 
 // The routes [first, min(n, first + 64)) of a unit.
@@ -533,11 +531,11 @@ template <bool MX>
 __device__ __forceinline__ void few_gateup_pass(const FewArgs &a, const FewUnit &u, int first, float *red) {
     const int left = u.n - first;
     if (left <= 16)
-        few_gateup_run<MX, 2>(a, 1, first, [&](int) { return u; }, red);
+        few_gateup_run<MX, 4, 2>(a, 1, first, [&](int) { return u; }, red);
     else if (left <= 32)
-        few_gateup_run<MX, 4>(a, 1, first, [&](int) { return u; }, red);
+        few_gateup_run<MX, 4, 4>(a, 1, first, [&](int) { return u; }, red);
     else
-        few_gateup_run<MX, 8>(a, 1, first, [&](int) { return u; }, red);
+        few_gateup_run<MX, 4, 8>(a, 1, first, [&](int) { return u; }, red);
 }
 
 // Persistent over the units in order, every workgroup taking each gridDim.x-th
@@ -569,7 +567,7 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
     for (; u < shared; u += step) {
         const FewUnit s{{reinterpret_cast<const uint8_t *>(a.S13), nullptr, nullptr, a.H}, a.Is, u % sblocks * kFewRows, a.T, nullptr};
         if (a.T <= 8)
-            few_gateup_run<false, 1>(a, 1, 0, [&](int) { return s; }, red);
+            few_gateup_run<false, 4, 1>(a, 1, 0, [&](int) { return s; }, red);
         else
             few_gateup_pass<false>(a, s, u / sblocks * 64, red);
     }
@@ -585,10 +583,27 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
         for (int first = 0; first < r.n; first += 64) few_gateup_pass<MX>(a, r, first, red);
     }
     const int nmid = u < mid ? (mid - u + step - 1) / step : 0;
-    few_gateup_run<MX, 2>(a, nmid, 0, [&](int i) { return routed(u + i * step); }, red);
+    few_gateup_run<MX, 4, 2>(a, nmid, 0, [&](int i) { return routed(u + i * step); }, red);
     u += nmid * step;
-    const int nlow = u < all ? (all - u + step - 1) / step : 0;
-    few_gateup_run<MX, 1>(a, nlow, 0, [&](int i) { return routed(u + i * step); }, red);
+    if (all - mid + shared >= 2 * step) {
+        const int nlow = u < all ? (all - u + step - 1) / step : 0;
+        few_gateup_run<MX, 4, 1>(a, nlow, 0, [&](int i) { return routed(u + i * step); }, red);
+    } else {
+        // fewer than two a workgroup: half as wide, so that every workgroup has its share (a token with one
+        // local expert of the full-size share: the call takes 24.0 us, from 26.5; seven experts, 3.5 units a
+        // workgroup, lose: 66 to 68 us)
+        const int half = 2 * (all - mid), from = ((int)blockIdx.x + step - (2 * mid + shared) % step) % step;
+        const int nlow = from < half ? (half - from + step - 1) / step : 0;
+        few_gateup_run<MX, 2, 1>(
+            a, nlow, 0,
+            [&](int i) {
+                const int v = from + i * step;
+                FewUnit r = routed(mid + v / 2);
+                r.i0 += v % 2 * 8;
+                return r;
+            },
+            red);
+    }
 }
 
 // Parts of a reduction dimension of `inner` elements: at least 512 bytes of a

@@ -1665,7 +1665,7 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + (a.T + 63) / 64 * (Is / kFewRows);
     {
         TraceScope tr("few_gateup", s);
-        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(units, device_cus())), dim3(kFewThreads), lds_gu,
+        hipLaunchKernelGGL(k_few_gateup<MX>, dim3((int)std::min<int64_t>(2 * units, device_cus())), dim3(kFewThreads), lds_gu,
                            s, a);
     }
     if (launch_status() != MOE_OK) return MOE_EHIP;

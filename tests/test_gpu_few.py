@@ -109,6 +109,8 @@ CASES = [
     # P, Np, K, E, L, base, H, I, Is, mx
     (1, 1, 1, 1, 1, 0, 256, 128, 0, False),
     (1, 1, 2, 8, 8, 0, 256, 128, 0, True),
+    (1, 3, 2, 8, 8, 0, 256, 4096, 128, False),       # over two units a workgroup, the shared expert's before them
+    (1, 20, 2, 4, 4, 0, 256, 640, 256, True),        # some experts with 9 to 16 routes, some with up to 8
     (2, 3, 2, 8, 4, 3, 512, 384, 0, False),
     (2, 3, 2, 8, 4, 3, 512, 384, 128, True),
     (1, 17, 4, 16, 16, 0, 256, 128, 256, False),     # one column past a tile
