@@ -725,8 +725,10 @@ def moe_ckpt_pack(src, q, scales, nrows=None, stream=None):
 
 def ckpt_pack(src, nrows=None, stream=None):
     """Allocate and fill (codes, scales) of a bf16 tensor [rows][cols]."""
-    q = torch.empty(src.shape, dtype=torch.int8, device=src.device)
-    s = torch.empty((src.shape[0], src.shape[1] // CKPT_BLOCK), dtype=torch.float32, device=src.device)
+    # memory of the stream that writes it
+    with torch.cuda.stream(stream):
+        q = torch.empty(src.shape, dtype=torch.int8, device=src.device)
+        s = torch.empty((src.shape[0], src.shape[1] // CKPT_BLOCK), dtype=torch.float32, device=src.device)
     moe_ckpt_pack(src, q, s, nrows, stream)
     return q, s
 
@@ -749,4 +751,4 @@ def moe_layer_bwd_ckpt(d, dOut, w, X, phi, route_row, seg_off, q, scales, W13, W
             _buf("scales", scales, f32, cap * 2 * I // CKPT_BLOCK, X), _buf("W13", W13, bf, d.L * 2 * I * H, X),
             _buf("W2", W2, bf, d.L * H * I, X), _buf("dX", dX, bf, n * H, X), _buf("dW13", dW13, f32, d.L * 2 * I * H, X),
             _buf("dW2", dW2, f32, d.L * H * I, X), _buf("dw", dw, f32, n * d.K, X), _buf("ws", ws, torch.uint8, 0, X)]
-    return _run("moe_layer_bwd_ckpt", X, stream, ctypes.byref(d), *args, ws.numel())
+    return _run("moe_layer_bwd_ckpt", X, stream, ctypes.byref(d), *args, 0 if ws is None else ws.numel())

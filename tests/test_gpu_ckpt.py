@@ -267,3 +267,34 @@ def test_ckpt_binding_refuses_wrong_buffers():
         ops.moe_ckpt_pack(x[:, :64].contiguous(), q, s)
     with pytest.raises(ValueError):
         ops.moe_ckpt_pack(x, q, s, torch.tensor([3], device=dev()))
+
+
+def test_pack_allocates_on_the_stream_it_runs_on():
+    # memory that the current stream has freed but still writes does not go to a call on another stream
+    x = inputs.normal_bf16_device((64, 4096), 1.0, 21, dev())
+    want, ws = ops.ckpt_pack(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    big = inputs.normal_bf16_device((4096, 8192), 1.0, 22, dev()).float()
+    for _ in range(3):
+        for t in (torch.empty_like(want), torch.empty_like(ws)):
+            for _ in range(4):
+                big.add_(1.0)
+            t.fill_(3)
+            del t
+        q, sc = ops.ckpt_pack(x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(q, want) and torch.equal(sc, ws)
+
+
+def test_layer_bwd_ckpt_binding_needs_a_workspace():
+    d = ops.make_desc(1, 4, 1, 2, 2, H=256, I=128)
+    cap, n, bf, i32, f32 = ops.capacity_rows(d), 4, torch.bfloat16, torch.int32, torch.float32
+
+    def z(dtype, *shape):
+        return torch.zeros(shape, dtype=dtype, device=dev())
+
+    with pytest.raises(ops.MoeError):
+        ops.moe_layer_bwd_ckpt(d, z(bf, n, 256), z(f32, n), z(bf, n, 256), z(i32, cap, 2), z(i32, n), z(i32, 3),
+                               z(torch.int8, cap, 256), z(f32, cap, 2), z(bf, 2, 256, 256), z(bf, 2, 256, 128), z(bf, n, 256),
+                               z(f32, 2, 256, 256), z(f32, 2, 256, 128), z(f32, n), None)
