@@ -268,6 +268,8 @@ enum {
  * other output is bitwise the same.  Needs H <= 32768 (else
  * MOE_EUNSUPPORTED).  moe_layer_bwd needs Xd: a caller that wants the
  * backward either passes Xd here or fills it later with moe_dispatch.
+ * For up to 1024 slots (P*Np*K) and no backward, moe_layer_fwd_few below is the
+ * faster call.
  *   ws >= moe_workspace_bytes(d, MOE_OP_LAYER_FWD)
  * Uses d->num_batches == 1.
  */
@@ -560,7 +562,8 @@ int moe_layer_bwd_ring(const moe_desc *d, int32_t mb_tokens, int32_t ring_slots,
  * aligned.  pad_rows and sched_threads play no part.  A slot may name the same
  * expert as another slot of its token; both count.  X and w of slots that are
  * not local are not read into any sum, and a token's output does not depend on
- * what the other tokens hold.  Repeated calls give bitwise the same outputs.
+ * the X and w of other tokens (their routes can change the order of its fp32
+ * sums).  Repeated calls give bitwise the same outputs.
  *
  * moe_layer_fwd_few_mx — the same with MXFP8 routed weights (codes and scale
  * bytes as moe_quantize_mx writes them: W13q [L][2I][H], W13s [L][2I][H/32],
@@ -588,7 +591,7 @@ int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, c
  *     s  = sigmoid(z)                  (by n->gate: 1, one per row, one per element)
  *     r' = alpha * r + beta * s * p
  *     xn = r' / rms(r') * g_pre        (g_pre NULL: not computed)
- *     rms(v) = sqrt(mean(v^2) + eps)
+ *     rms(v) = sqrt(mean(v^2) + eps)     (mean(v^2) + eps has to lie in fp32's normal range)
  * r' enters the pre-norm before it is rounded; every output is rounded once.
  *   n      host descriptor: rows (>= 0), H (a multiple of 8, at most 32768),
  *          gate, res_fp32 (1: r, r_out and their gradients are float, 0: bf16),
@@ -664,8 +667,9 @@ int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
  *   wrow   float [rows], nullable     nrows as above
  *   dHU    bf16 [rows][2I] out        A bf16 [rows][I] out, nullable
  *   dw     float [rows] out, nullable (from A before its rounding)
- * Errors of both: MOE_EINVAL (sizes, NULL or misaligned pointers: 16 bytes, the
- * float and int32 arrays 4 bytes).  rows = 0 does nothing.
+ * Inputs and outputs of both must not overlap.  Errors of both: MOE_EINVAL
+ * (sizes, I >= 2^30, NULL or misaligned pointers: 16 bytes, the float and int32
+ * arrays 4 bytes).  rows = 0 does nothing.
  *
  * moe_layer_bwd_ckpt — moe_layer_bwd on a checkpoint: q and scales (moe_ckpt_pack
  * of the forward's HU with cols = 2I and nrows = seg_off + L; q [cap][2I]) take

@@ -80,8 +80,8 @@ struct FewArgs {
 // The experts stand by their number of routes: over 16, 9 to 16, up to 8, by id
 // within each kind.
 constexpr int kFewHead = 64;
-__host__ __device__ inline int few_max_experts(int L, int R) { return L < R ? L : R; }
-__host__ __device__ inline int few_plan_words(int L, int R) { return kFewHead + 2 * few_max_experts(L, R) + 1 + 2 * R; }
+__host__ __device__ constexpr int few_max_experts(int L, int R) { return L < R ? L : R; }
+__host__ __device__ constexpr int few_plan_words(int L, int R) { return kFewHead + 2 * few_max_experts(L, R) + 1 + 2 * R; }
 
 struct FewPlan {
     int *expert, *off, *route, *place;
@@ -98,11 +98,11 @@ struct FewPlan {
 // expert, 8 words for the head, and the list.
 constexpr int kFewRedLd = 36;  // 32 sums of a column and 4 words that spread the columns over the banks
 constexpr int kFewRedWords = kFewWaves * 32 * kFewRedLd;
-__host__ __device__ inline int few_gateup_words(int L, int R) {
+__host__ __device__ constexpr int few_gateup_words(int L, int R) {
     return kFewRedWords + L + 8 + few_plan_words(L, R) - kFewHead;
 }
 // The list in the down launch's LDS: numbers of routes and places in 16 bits.
-__host__ __device__ inline int few_list_words(int L, int R) { return 2 * few_max_experts(L, R) + 1 + R; }
+__host__ __device__ constexpr int few_list_words(int L, int R) { return 2 * few_max_experts(L, R) + 1 + R; }
 
 // Builds the list in LDS: count the routes of each expert (a route's rank is
 // the order in which the LDS atomics answer: it only says which MFMA column

@@ -1,7 +1,7 @@
 // C-ABI entry points and kernels of the MoE layer share (gfx950).
 // The operations, their arguments and error behaviour are documented in
-// include/moe.h; the device code lives in schedule.hpp, rowops.hpp, gemm.hpp
-// and layer.hpp.
+// include/moe.h; the device code lives in schedule.hpp, rowops.hpp, gemm.hpp,
+// wide.hpp, layer.hpp, mx.hpp, mxbwd.hpp, few.hpp, norm.hpp and ckpt.hpp.
 #include <hip/hip_runtime.h>
 
 #include <string.h>
@@ -1659,7 +1659,10 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R);
     size_t lds_down = list + sums + std::min<size_t>(32 << 10, sums * (waves - 1));
     if (lds_down > kMaxLds / 2) lds_down = std::max(list + sums, kMaxLds / 2);
-    if (lds_gu > kMaxLds || lds_down > kMaxLds) return MOE_EUNSUPPORTED;
+    // the largest calls: 4096 experts, 1024 routes, and every slot a token of its own with the shared expert's row
+    static_assert(4 * few_gateup_words(4096, kFewMaxRoutes) <= (int)kMaxLds &&
+                      4 * (few_list_words(4096, kFewMaxRoutes) + 2 * kFewMaxRoutes * 16) <= (int)kMaxLds,
+                  "every call that few_check lets through fits the LDS");
     a.words = (int)((lds_down - list) / 16) * 4;
     lds_down = list + 4 * (size_t)a.words;
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + (a.T + 63) / 64 * (Is / kFewRows);
@@ -1883,7 +1886,7 @@ int moe_ckpt_pack(const uint16_t *src, int64_t rows, int32_t cols, const int32_t
 
 int moe_ckpt_swiglu_bwd(const int8_t *q, const float *scales, const uint16_t *dA, const float *wrow, int64_t rows,
                         int32_t I, const int32_t *nrows, uint16_t *dHU, uint16_t *A, float *dw, void *stream) {
-    if (rows < 0 || I < 1 || I % kCkptBlock || I > (1 << 30) || rows > (1ll << 40)) return MOE_EINVAL;
+    if (rows < 0 || I < 1 || I % kCkptBlock || I >= (1 << 30) || rows > (1ll << 40)) return MOE_EINVAL;
     if (rows == 0) return MOE_OK;
     if (!q || !scales || !dA || !dHU || !aligned16(q) || !aligned4(scales) || !aligned16(dA) || !aligned4(wrow) ||
         !aligned4(nrows) || !aligned16(dHU) || !aligned16(A) || !aligned4(dw))

@@ -140,7 +140,7 @@ def test_ckpt_refusals():
         assert pack(a[0], 4, 128, None, a[1], a[2], None) == ops.MOE_EINVAL
     assert pack(P[0], 4, 128, _fake(0x10002), P[1], P[2], None) == ops.MOE_EINVAL
     assert bwd(None, None, None, None, 0, 128, None, None, None, None, None) == ops.MOE_OK
-    for rows, I in ((-1, 128), (4, 0), (4, 64)):
+    for rows, I in ((-1, 128), (4, 0), (4, 64), (4, 1 << 30)):
         assert bwd(*P[:4], rows, I, None, *P[4:7], None) == ops.MOE_EINVAL
     for i in range(8):
         a = [P[0], P[1], P[2], P[3], P[4], P[5], P[6], P[7]]  # q, scales, dA, wrow, nrows, dHU, A, dw
