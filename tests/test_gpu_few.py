@@ -181,6 +181,25 @@ def test_few_mx_every_code_and_scale():
     check(c, call(c))
 
 
+def test_few_mx_nan_codes_and_scales():
+    # a NaN code or scale byte anywhere in an expert's weights reaches that expert's tokens and no others
+    ids = [[0, 1], [2, 3], [1, 1], [4, 5], [5, 0], [3, 2]]
+    c = make(1, 6, 2, 6, 6, 0, 512, 256, mx=True, ids=ids)
+    clean = call(c)[0].clone()
+    (q13, s13), (q2, s2) = c["W13"], c["W2"]
+    for t, spot, v in ((q13, (1, 300, 77), 0x7F), (q2, (3, 9, 200), 0xFF), (s13, (4, 3, 5), 255), (s2, (4, 100, 1), 255)):
+        old = int(t[spot])
+        t[spot] = v
+        out = call(c)[0]
+        hit = [i for i, e in enumerate(ids) if spot[0] in e]
+        keep = [i for i in range(6) if i not in hit]
+        assert torch.equal(out[keep], clean[keep])
+        cols = slice(None) if t is q13 or t is s13 else spot[1]  # a row of W2 is one output element
+        assert not bool(out[hit][:, cols].isfinite().any())
+        t[spot] = old
+    assert torch.equal(call(c)[0], clean)
+
+
 def test_few_repeats_bitwise_and_on_another_stream():
     c = make(2, 13, 3, 12, 6, 3, 512, 256, Is=128)
     first = call(c).clone()
