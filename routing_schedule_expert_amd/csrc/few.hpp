@@ -25,8 +25,9 @@
 // The activations' rounding to bf16 is the layer forward's own (and one of two
 // roundings: the experts' sums stay fp32 to the output).  Keeping them as a high
 // and a low bf16, which halves the output's error variance, doubles the down
-// launch's token loads: 36.6 us against 36.2 for 8 tokens of the full-size share,
-// but 264 against 241 for 128 and 78 against 61 for 32 with MXFP8 weights.
+// launch's token loads: 41.5 us against 39 for 8 tokens of the full-size share, 264
+// against 241 for 128, 61 against 47 for 37 tokens of 64 experts, and 118 against 61
+// for 32 tokens with MXFP8 weights (30 against 16 for 4).
 //
 // Measured (launches alone; a read-only kernel gets 7.1 TB/s; each launch spends
 // about 5 us before its stream flows and after it ends):
