@@ -229,7 +229,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_norm_fwd(NormArgs a) {
 template <bool F32, int CH>
 __global__ __launch_bounds__(kNormMaxThreads) void k_norm_bwd(NormBwdArgs a) {
     extern __shared__ __attribute__((aligned(16))) float norm_smem[];
-    norm_bwd_body<F32, CH>(a, norm_smem);
+    if constexpr (CH == 1)
+        norm_bwd_body<F32>(a, norm_smem);
+    else
+        norm_bwd_wide_body<F32, CH>(a, norm_smem);
 }
 
 template <int COLS>
@@ -1755,7 +1758,8 @@ int norm_check(const moe_norm_desc *n) {
 }
 
 // Chunks of 8 elements per thread, the threads of a row's workgroup, and its LDS
-// (the sums' slots, and the gains with one chunk per thread).
+// (the sums' slots, and the gains with one chunk per thread; with more, the
+// backward's sums of dg_post).
 int norm_chunks(const moe_norm_desc *n) { return n->H <= kNormLdsH ? 1 : n->H <= 2 * kNormLdsH ? 2 : 4; }
 int norm_threads(const moe_norm_desc *n) {
     const int per = 8 * 64 * norm_chunks(n);
@@ -1772,7 +1776,10 @@ int64_t norm_groups(const moe_norm_desc *n) {
     return std::min<int64_t>(n->rows, waves <= 8 ? 512 : 256);
 }
 int64_t norm_ws_bytes(const moe_norm_desc *n) { return align256(norm_groups(n) * 2 * n->H * 4); }
-size_t norm_lds_bytes(const moe_norm_desc *n) { return 256 + (norm_chunks(n) == 1 ? 8 * (size_t)n->H : 0); }
+size_t norm_lds_bytes(const moe_norm_desc *n, bool bwd) {
+    const int ch = norm_chunks(n);
+    return 384 + (ch == 1 ? 8 * (size_t)n->H : bwd ? 32 * (size_t)ch * norm_threads(n) : 0);
+}
 
 auto *norm_fwd_kernel(const moe_norm_desc *n) {
     const int ch = norm_chunks(n);
@@ -1819,7 +1826,7 @@ int moe_block_norm_fwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     hipStream_t s = static_cast<hipStream_t>(stream);
     TraceScope tr("block_norm_fwd", s);
     auto *fn = norm_fwd_kernel(n);
-    hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), norm_lds_bytes(n), s, a);
+    hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), norm_lds_bytes(n, false), s, a);
     return launch_status();
 }
 
@@ -1848,7 +1855,7 @@ int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     if (some) {
         TraceScope tr("block_norm_bwd", s);
         auto *fn = norm_bwd_kernel(n);
-        hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), norm_lds_bytes(n), s, b);
+        hipLaunchKernelGGL(fn, dim3(grid), dim3(threads), norm_lds_bytes(n, true), s, b);
         if (launch_status() != MOE_OK) return MOE_EHIP;
     }
     if (!sums) return MOE_OK;

@@ -21,7 +21,7 @@
 //   - The next row's loads are issued before this row's reductions.  Loads return
 //     in order, so nothing else may be loaded from memory in the loop: g_post and
 //     g_pre lie in LDS.  (Both only while the registers last: up to H = 8192, the
-//     forward's loads ahead up to 16384.)
+//     forward's loads ahead up to 16384; the backward reads a longer row twice.)
 //   - Rows are raw buffers: absent tensors are empty buffers and the last chunk's
 //     spare lanes read zeros, so the loop has no branch around a memory access and
 //     the compiler waits for exactly the loads it needs.
@@ -120,16 +120,21 @@ struct NormGains {
         const f32x4 v[4] = {post ? a[0] : one, post ? a[1] : one, pre ? b[0] : one, pre ? b[1] : one};
         o[0] = v[0], o[1] = v[1], p[0] = v[2], p[1] = v[3];
     }
+    // no branch around the loads from memory: what is absent comes from an empty buffer
     template <bool LDS>
     __device__ __forceinline__ void load(int which, int chunk, float (&g)[8]) const {
-        const float *p = which ? pre : post;
-        const f32x4 *s = reinterpret_cast<const f32x4 *>(LDS ? lds + which * H : p) + 2 * chunk;
-        if ((!LDS && !p) || chunk * 8 >= H) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = 1.0f;
-            return;
+        f32x4 a, b;
+        if constexpr (LDS) {
+            const f32x4 *s = reinterpret_cast<const f32x4 *>(lds + which * H) + 2 * chunk;
+            a = b = f32x4{1.f, 1.f, 1.f, 1.f};
+            if (chunk * 8 < H) a = s[0], b = s[1];
+        } else {
+            const float *p = which ? pre : post;
+            const __amdgpu_buffer_rsrc_t s = raw_buffer(p, p ? (uint32_t)H * 4 : 0);
+            a = __builtin_bit_cast(f32x4, buffer_load16(s, chunk * 32));
+            b = __builtin_bit_cast(f32x4, buffer_load16(s, chunk * 32 + 16));
+            if (!p) a = b = f32x4{1.f, 1.f, 1.f, 1.f};
         }
-        const f32x4 a = s[0], b = s[1];
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[e] = a[e], g[4 + e] = b[e];
     }
@@ -268,121 +273,239 @@ __device__ __forceinline__ void norm_fwd_body(const NormArgs &a, float *lds) {
     }
 }
 
-template <bool F32, int CH>
+// Up to H = 8192: one chunk per thread, the row and the next one's loads in registers,
+// gains in LDS.
+template <bool F32>
 __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) {
-    constexpr bool in_lds = CH == 1, ahead = CH == 1;  // gains in LDS; the next row's loads ahead
+    constexpr int RS = F32 ? 4 : 2;
+    const NormArgs &a = b.f;
+    const int t = threadIdx.x, H = a.H;
+    const bool post = a.g_post, pre = a.g_pre, elem = a.gate == MOE_GATE_ELEM, token = a.gate == MOE_GATE_TOKEN;
+    const float inv_h = 1.0f / (float)H, alpha = a.y ? a.alpha : 1.0f, beta = a.y ? a.beta : 0.0f;
+    const void *ze = elem ? a.z : nullptr;
+    RowSum<2> sum(lds);
+    const NormGains gains{a.g_post, a.g_pre, lds + 64, H};
+    Raw8<false> y, z, dx;
+    Raw8<F32> r, up;
+    float st_y, st_r, zt;
+    auto fetch = [&](int64_t row, bool in) {
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H, in), by = row_buffer<2>(a.y, row, H, in),
+                                     bz = row_buffer<2>(ze, row, H, in), bu = row_buffer<RS>(b.dr_out, row, H, in),
+                                     bd = row_buffer<2>(b.dxn, row, H, in);
+        r.load(br, t);
+        y.load(by, t);
+        z.load(bz, t);
+        up.load(bu, t);
+        dx.load(bd, t);
+        st_y = row_word(a.stats, 2 * row, in);
+        st_r = row_word(a.stats, 2 * row + 1, in);
+        zt = row_word(token ? a.z : nullptr, row, in);
+    };
+    float acc_post[8], acc_pre[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc_post[e] = acc_pre[e] = 0.f;
+    int64_t row = blockIdx.x;
+    if (row >= a.rows) return;
+    fetch(row, true);
+    norm_clear(lds, 64);
+    gains.fill();
+    __syncthreads();
+    for (; row < a.rows; row += gridDim.x) {
+        const float ystd = post ? st_y : 1.0f, rstd = st_r;
+        const float gt = token ? sigmoid(zt) : 1.0f;
+        // yh, the gate, D (first what arrives for r'), t and xh of the row
+        float yh[8], gv[8], D[8], tv[8], xh[8], s[2] = {0.f, 0.f};
+        float go[8], gi[8];
+        gains.load<true>(0, t, go);
+        gains.load<true>(1, t, gi);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            yh[e] = y[e] * ystd;
+            gv[e] = elem ? sigmoid(z[e]) : gt;
+            D[e] = up[e];
+            xh[e] = fmaf(beta * gv[e], yh[e] * go[e], alpha * r[e]) * rstd;
+            const float d = dx[e];
+            tv[e] = d * gi[e];
+            acc_pre[e] = fmaf(d, xh[e], acc_pre[e]);
+            s[0] = fmaf(tv[e], xh[e], s[0]);
+        }
+        fetch(row + gridDim.x, row + gridDim.x < a.rows);
+        if (pre) {
+            sum(s);
+            const float c1 = s[0] * inv_h;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) D[e] = fmaf(rstd, fmaf(-xh[e], c1, tv[e]), D[e]);
+        }
+        s[0] = s[1] = 0.f;
+        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(b.dr, row, H), by = row_buffer<2>(b.dy, row, H),
+                                     bz = row_buffer<2>(elem ? b.dz : nullptr, row, H);
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = alpha * D[e];
+        store8<F32>(br, t, o);
+        gains.load<true>(0, t, go);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = beta * D[e], p = yh[e] * go[e];
+            o[e] = d * p * gv[e] * (1.0f - gv[e]);
+            s[1] = fmaf(d, p, s[1]);
+            const float dp = d * gv[e];
+            acc_post[e] = fmaf(dp, yh[e], acc_post[e]);
+            D[e] = dp * go[e];  // q
+            s[0] = fmaf(D[e], yh[e], s[0]);
+        }
+        store8<false>(bz, t, o);
+        if (post || token) sum(s);
+        const float c2 = post ? s[0] * inv_h : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = ystd * fmaf(-yh[e], c2, D[e]);
+        store8<false>(by, t, o);
+        if (token && t == 0) static_cast<float *>(b.dz)[row] = s[1] * gt * (1.0f - gt);
+    }
+    if (post || pre) {
+        const __amdgpu_buffer_rsrc_t bo = row_buffer<4>(post ? b.part : nullptr, 2 * (int64_t)blockIdx.x, H),
+                                     bi = row_buffer<4>(pre ? b.part : nullptr, 2 * (int64_t)blockIdx.x + 1, H);
+        store8<true>(bo, t, acc_post);
+        store8<true>(bi, t, acc_pre);
+    }
+}
+
+// A chunk of a row as the backward reads it, and what it makes of one element.
+template <bool F32>
+struct NormBwdChunk {
+    Raw8<false> y, z, dx;
+    Raw8<F32> r, up;
+};
+struct NormBwdElem {
+    float yh, gate, u, xh, t;  // u = beta s p, the block's part of r'
+};
+
+// Past H = 8192 a row does not fit the registers beside the column sums (holding it
+// spilled: 10,000 rows of 12,288 took 810 us against 618, 4,000 of 32,768 2,490 against
+// 841): the row is read for its sums and read again, from the caches, for the outputs,
+// with one reduction between: with u = beta s p, the three sums
+//   S1 = sum t xh,  S2 = sum u (dr' + rstd(r') t),  S3 = sum u xh
+// give both means, mean(t xh) = S1 / H and, because q yh = D u, mean(q yh) =
+// (S2 - rstd(r') S1 S3 / H) / H.  (The same single reduction in the body above costs
+// the registers that hold the next row: 4,095 rows of 2,056 in fp32 56 us, from 44.)
+template <bool F32, int CH>
+__device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *lds) {
     constexpr int RS = F32 ? 4 : 2;
     const NormArgs &a = b.f;
     const int t = threadIdx.x, nt = blockDim.x, H = a.H;
     const bool post = a.g_post, pre = a.g_pre, elem = a.gate == MOE_GATE_ELEM, token = a.gate == MOE_GATE_TOKEN;
     const float inv_h = 1.0f / (float)H, alpha = a.y ? a.alpha : 1.0f, beta = a.y ? a.beta : 0.0f;
     const void *ze = elem ? a.z : nullptr;
-    RowSum<2> sum(lds);
-    const NormGains gains{a.g_post, a.g_pre, in_lds ? lds + 64 : nullptr, H};
-    Raw8<false> y[CH], z[CH], dx[CH];
-    Raw8<F32> r[CH], up[CH];
-    float st_y, st_r, zt;
-    auto fetch = [&](int64_t row, bool in) {
-        const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(a.r, row, H, in), by = row_buffer<2>(a.y, row, H, in),
-                                     bz = row_buffer<2>(ze, row, H, in), bu = row_buffer<RS>(b.dr_out, row, H, in),
-                                     bd = row_buffer<2>(b.dxn, row, H, in);
+    RowSum<3> sum(lds);
+    // gains and rows are read from memory as they are used
+    const NormGains gains{a.g_post, a.g_pre, nullptr, H};
+    using Chunk = NormBwdChunk<F32>;
+    auto fetch = [&](Chunk &k, int64_t row, int c) {
+        k.r.load(row_buffer<RS>(a.r, row, H), c);
+        k.y.load(row_buffer<2>(a.y, row, H), c);
+        k.z.load(row_buffer<2>(ze, row, H), c);
+        k.up.load(row_buffer<RS>(b.dr_out, row, H), c);
+        k.dx.load(row_buffer<2>(b.dxn, row, H), c);
+    };
+    struct Row {
+        float st_y, st_r, zt;
+    };
+    auto fetch_row = [&](Row &k, int64_t row, bool in) {
+        k.st_y = row_word(a.stats, 2 * row, in);
+        k.st_r = row_word(a.stats, 2 * row + 1, in);
+        k.zt = row_word(token ? a.z : nullptr, row, in);
+    };
+    // the sums of dg_post in LDS, [half][chunk], a thread's own; those of dg_pre in registers
+    float acc_pre[CH][8];
+    f32x4 *post_lds = reinterpret_cast<f32x4 *>(lds + 96);
+    const int half = CH * nt;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc_pre[i][e] = 0.f;
+        post_lds[i * nt + t] = post_lds[half + i * nt + t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    int64_t row = blockIdx.x;
+    if (row >= a.rows) return;
+    Chunk cur;
+    Row w, wnext;
+    fetch_row(w, row, true);
+    norm_clear(lds, 96);
+    __syncthreads();
+    for (; row < a.rows; row += gridDim.x) {
+        const bool more = row + gridDim.x < a.rows;
+        fetch_row(wnext, row + gridDim.x, more);
+        const float ystd = post ? w.st_y : 1.0f, rstd = w.st_r, gt = token ? sigmoid(w.zt) : 1.0f;
+        auto element = [&](const Chunk &k, int e, const float (&go)[8], const float (&gi)[8]) {
+            NormBwdElem x;
+            x.yh = k.y[e] * ystd;
+            x.gate = elem ? sigmoid(k.z[e]) : gt;
+            x.u = beta * x.gate * (x.yh * go[e]);
+            x.xh = pre ? fmaf(alpha, k.r[e], x.u) * rstd : 0.f;
+            x.t = k.dx[e] * gi[e];
+            return x;
+        };
+        float s[3] = {0.f, 0.f, 0.f};
+        // the scheduling barriers keep one chunk's loads and values in registers at a time
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
-            r[i].load(br, c);
-            y[i].load(by, c);
-            z[i].load(bz, c);
-            up[i].load(bu, c);
-            dx[i].load(bd, c);
-        }
-        st_y = row_word(a.stats, 2 * row, in);
-        st_r = row_word(a.stats, 2 * row + 1, in);
-        zt = row_word(token ? a.z : nullptr, row, in);
-    };
-    float acc_post[CH][8], acc_pre[CH][8];
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc_post[i][e] = acc_pre[i][e] = 0.f;
-    int64_t row = blockIdx.x;
-    if (row >= a.rows) return;
-    if (ahead) fetch(row, true);
-    norm_clear(lds, 64);
-    gains.fill();
-    __syncthreads();
-    for (; row < a.rows; row += gridDim.x) {
-        if (!ahead) fetch(row, true);
-        const float ystd = post ? st_y : 1.0f, rstd = st_r;
-        const float gt = token ? sigmoid(zt) : 1.0f;
-        // yh, the gate, D (first what arrives for r'), t and xh of the row
-        float yh[CH][8], gv[CH][8], D[CH][8], tv[CH][8], xh[CH][8], s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
             float go[8], gi[8];
-            gains.load<in_lds>(0, i * nt + t, go);
-            gains.load<in_lds>(1, i * nt + t, gi);
+            fetch(cur, row, c);
+            gains.load<false>(0, c, go);
+            gains.load<false>(1, c, gi);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                yh[i][e] = y[i][e] * ystd;
-                gv[i][e] = elem ? sigmoid(z[i][e]) : gt;
-                D[i][e] = up[i][e];
-                xh[i][e] = fmaf(beta * gv[i][e], yh[i][e] * go[e], alpha * r[i][e]) * rstd;
-                const float d = dx[i][e];
-                tv[i][e] = d * gi[e];
-                acc_pre[i][e] = fmaf(d, xh[i][e], acc_pre[i][e]);
-                s[0] = fmaf(tv[i][e], xh[i][e], s[0]);
+                const NormBwdElem x = element(cur, e, go, gi);
+                s[0] = fmaf(x.t, x.xh, s[0]);
+                s[1] = fmaf(x.u, fmaf(rstd, x.t, cur.up[e]), s[1]);
+                s[2] = fmaf(x.u, x.xh, s[2]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (ahead) fetch(row + gridDim.x, row + gridDim.x < a.rows);
-        if (pre) {
-            sum(s);
-            const float c1 = s[0] * inv_h;
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) D[i][e] = fmaf(rstd, fmaf(-xh[i][e], c1, tv[i][e]), D[i][e]);
-        }
-        s[0] = s[1] = 0.f;
+        if (pre || post || token) sum(s);
+        const float c1 = s[0] * inv_h, du = fmaf(-rstd * c1, s[2], s[1]), c2 = post ? du * inv_h : 0.f;
         const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(b.dr, row, H), by = row_buffer<2>(b.dy, row, H),
                                      bz = row_buffer<2>(elem ? b.dz : nullptr, row, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
-            float o[8], go[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = alpha * D[i][e];
-            store8<F32>(br, c, o);
-            gains.load<in_lds>(0, c, go);
+            float go[8], gi[8], dr[8], dz[8], dy[8], dp_yh[8];
+            fetch(cur, row, c);
+            gains.load<false>(0, c, go);
+            gains.load<false>(1, c, gi);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = beta * D[i][e], p = yh[i][e] * go[e];
-                o[e] = d * p * gv[i][e] * (1.0f - gv[i][e]);
-                s[1] = fmaf(d, p, s[1]);
-                const float dp = d * gv[i][e];
-                acc_post[i][e] = fmaf(dp, yh[i][e], acc_post[i][e]);
-                D[i][e] = dp * go[e];  // q
-                s[0] = fmaf(D[i][e], yh[i][e], s[0]);
+                const NormBwdElem x = element(cur, e, go, gi);
+                const float D = fmaf(rstd, fmaf(-x.xh, c1, x.t), cur.up[e]), dp = beta * D * x.gate;
+                dr[e] = alpha * D;
+                dz[e] = D * x.u * (1.0f - x.gate);
+                dy[e] = ystd * fmaf(-x.yh, c2, dp * go[e]);
+                dp_yh[e] = dp * x.yh;
+                acc_pre[i][e] = fmaf(cur.dx[e], x.xh, acc_pre[i][e]);
             }
-            store8<false>(bz, c, o);
-        }
-        if (post || token) sum(s);
-        const float c2 = post ? s[0] * inv_h : 0.f;
+            f32x4 lo = post_lds[c], hi = post_lds[half + c];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            float o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = ystd * fmaf(-yh[i][e], c2, D[i][e]);
-            store8<false>(by, i * nt + t, o);
+            for (int e = 0; e < 4; ++e) lo[e] += dp_yh[e], hi[e] += dp_yh[4 + e];
+            post_lds[c] = lo, post_lds[half + c] = hi;
+            store8<F32>(br, c, dr);
+            store8<false>(bz, c, dz);
+            store8<false>(by, c, dy);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (token && t == 0) static_cast<float *>(b.dz)[row] = s[1] * gt * (1.0f - gt);
+        if (token && t == 0) static_cast<float *>(b.dz)[row] = du * (1.0f - gt);
+        w = wnext;
     }
     if (post || pre) {
         const __amdgpu_buffer_rsrc_t bo = row_buffer<4>(post ? b.part : nullptr, 2 * (int64_t)blockIdx.x, H),
                                      bi = row_buffer<4>(pre ? b.part : nullptr, 2 * (int64_t)blockIdx.x + 1, H);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            store8<true>(bo, i * nt + t, acc_post[i]);
-            store8<true>(bi, i * nt + t, acc_pre[i]);
+            const int c = i * nt + t;
+            const f32x4 lo = post_lds[c], hi = post_lds[half + c];
+            const float acc_post[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            store8<true>(bo, c, acc_post);
+            store8<true>(bi, c, acc_pre[i]);
         }
     }
 }

@@ -281,3 +281,24 @@ def test_norm_binding_refuses_wrong_buffers():
         ops.moe_block_norm_fwd(c["n"], c["y"], c["r"], c["z"], c["g_post"], c["g_pre"], c["r_out"], c["xn"][:3].contiguous(), c["stats"])
     with pytest.raises(ops.MoeError):
         ops.moe_block_norm_fwd(c["n"], c["y"], c["r"], None, c["g_post"], c["g_pre"], c["r_out"], c["xn"], c["stats"])
+
+
+@pytest.mark.parametrize("H", [1024, 9000, 20000])
+def test_norm_gradient_without_a_pre_norm_ignores_r(H):
+    # dr and dy do not depend on the residual where nothing norms it, whatever it holds
+    g = torch.Generator(device=dev()).manual_seed(H)
+    n = ops.make_norm_desc(3, H, gate=ops.MOE_GATE_TOKEN, alpha=0.5)
+    y, r, up = (torch.randn((3, H), generator=g, device=dev()).to(torch.bfloat16) for _ in range(3))
+    z, gp = torch.randn(3, generator=g, device=dev()), torch.rand(H, generator=g, device=dev())
+    out, stats = torch.empty_like(r), torch.empty((3, 2), device=dev())
+
+    def run():
+        b = ops.alloc_norm_bwd(n, dev(), pre=False)
+        ops.moe_block_norm_fwd(n, y, r, z, gp, None, out, None, stats)
+        ops.block_norm_bwd(n, y, r, z, gp, None, stats, up, None, b)
+        return [b.dy, b.dr, b.dz, b.dg_post]
+
+    want = run()
+    r[1, 5], r[2, H - 1] = float("inf"), float("nan")
+    got = run()
+    assert all(torch.equal(a, c) and bool(a.isfinite().all()) for a, c in zip(got, want))
