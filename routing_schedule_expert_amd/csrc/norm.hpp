@@ -73,13 +73,20 @@ __device__ __forceinline__ float row_word(const void *p, int64_t i, bool in) {
     return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(raw_buffer(static_cast<const float *>(p) + (in ? i : 0), in ? 4u : 0u), 0, 0, 0));
 }
 
-// Eight elements (a chunk) as they lie in memory.
+// Eight elements (a chunk) as they lie in memory.  KEEP: they are read again.
+template <bool KEEP>
+__device__ __forceinline__ u32x4 load_chunk(__amdgpu_buffer_rsrc_t b, int off) {
+    return KEEP ? buffer_load16(b, off) : buffer_load16_nt(b, off);
+}
 template <bool F32>
 struct Raw8;
 template <>
 struct Raw8<false> {
     u32x4 v;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int chunk) { v = buffer_load16_nt(b, chunk * 16); }
+    template <bool KEEP = false>
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int chunk) {
+        v = load_chunk<KEEP>(b, chunk * 16);
+    }
     __device__ __forceinline__ float operator[](int i) const {
         return __uint_as_float((i & 1) ? (v[i >> 1] & 0xffff0000u) : (v[i >> 1] << 16));
     }
@@ -87,9 +94,10 @@ struct Raw8<false> {
 template <>
 struct Raw8<true> {
     u32x4 v[2];
+    template <bool KEEP = false>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int chunk) {
-        v[0] = buffer_load16_nt(b, chunk * 32);
-        v[1] = buffer_load16_nt(b, chunk * 32 + 16);
+        v[0] = load_chunk<KEEP>(b, chunk * 32);
+        v[1] = load_chunk<KEEP>(b, chunk * 32 + 16);
     }
     __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(v[i >> 2][i & 3]); }
 };
@@ -375,15 +383,26 @@ template <bool F32>
 struct NormBwdChunk {
     Raw8<false> y, z, dx;
     Raw8<F32> r, up;
+    template <bool KEEP>
+    __device__ __forceinline__ void load(const NormBwdArgs &b, int64_t row, int c) {
+        constexpr int RS = F32 ? 4 : 2;
+        const NormArgs &a = b.f;
+        r.template load<KEEP>(row_buffer<RS>(a.r, row, a.H), c);
+        y.template load<KEEP>(row_buffer<2>(a.y, row, a.H), c);
+        z.template load<KEEP>(row_buffer<2>(a.gate == MOE_GATE_ELEM ? a.z : nullptr, row, a.H), c);
+        up.template load<KEEP>(row_buffer<RS>(b.dr_out, row, a.H), c);
+        dx.template load<KEEP>(row_buffer<2>(b.dxn, row, a.H), c);
+    }
 };
 struct NormBwdElem {
     float yh, gate, u, xh, t;  // u = beta s p, the block's part of r'
 };
 
 // Past H = 8192 a row does not fit the registers beside the column sums (holding it
-// spilled: 10,000 rows of 12,288 took 810 us against 618, 4,000 of 32,768 2,490 against
-// 841): the row is read for its sums and read again, from the caches, for the outputs,
-// with one reduction between: with u = beta s p, the three sums
+// spilled: 10,000 rows of 12,288 took 810 us against 490, 4,000 of 32,768 2,490 against
+// 757): the row is read for its sums and read again, from the caches, for the outputs
+// (617 and 832 us where the first reading is nontemporal too), with one reduction
+// between: with u = beta s p, the three sums
 //   S1 = sum t xh,  S2 = sum u (dr' + rstd(r') t),  S3 = sum u xh
 // give both means, mean(t xh) = S1 / H and, because q yh = D u, mean(q yh) =
 // (S2 - rstd(r') S1 S3 / H) / H.  (The same single reduction in the body above costs
@@ -395,18 +414,10 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
     const int t = threadIdx.x, nt = blockDim.x, H = a.H;
     const bool post = a.g_post, pre = a.g_pre, elem = a.gate == MOE_GATE_ELEM, token = a.gate == MOE_GATE_TOKEN;
     const float inv_h = 1.0f / (float)H, alpha = a.y ? a.alpha : 1.0f, beta = a.y ? a.beta : 0.0f;
-    const void *ze = elem ? a.z : nullptr;
     RowSum<3> sum(lds);
     // gains and rows are read from memory as they are used
     const NormGains gains{a.g_post, a.g_pre, nullptr, H};
     using Chunk = NormBwdChunk<F32>;
-    auto fetch = [&](Chunk &k, int64_t row, int c) {
-        k.r.load(row_buffer<RS>(a.r, row, H), c);
-        k.y.load(row_buffer<2>(a.y, row, H), c);
-        k.z.load(row_buffer<2>(ze, row, H), c);
-        k.up.load(row_buffer<RS>(b.dr_out, row, H), c);
-        k.dx.load(row_buffer<2>(b.dxn, row, H), c);
-    };
     struct Row {
         float st_y, st_r, zt;
     };
@@ -451,7 +462,7 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
             float go[8], gi[8];
-            fetch(cur, row, c);
+            cur.template load<true>(b, row, c);
             gains.load<false>(0, c, go);
             gains.load<false>(1, c, gi);
 #pragma unroll
@@ -471,7 +482,7 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + t;
             float go[8], gi[8], dr[8], dz[8], dy[8], dp_yh[8];
-            fetch(cur, row, c);
+            cur.template load<false>(b, row, c);
             gains.load<false>(0, c, go);
             gains.load<false>(1, c, gi);
 #pragma unroll
