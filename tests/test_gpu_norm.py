@@ -302,3 +302,21 @@ def test_norm_gradient_without_a_pre_norm_ignores_r(H):
     r[1, 5], r[2, H - 1] = float("inf"), float("nan")
     got = run()
     assert all(torch.equal(a, c) and bool(a.isfinite().all()) for a, c in zip(got, want))
+
+
+@pytest.mark.parametrize("gate,res", [("elem", "bf16"), ("token", "fp32"), ("none", "bf16")])
+@pytest.mark.parametrize("rows,H", [(257, 8200), (600, 12296), (5, 16392), (520, 24584)])
+def test_norm_long_rows(rows, H, gate, res):
+    # rows that the backward reads twice, several a workgroup
+    c = make(rows, H, gate, res, seed=4)
+    check(c)
+    b = bwd(c)
+    first = [None if t is None else t.clone() for t in (b.dy, b.dr, b.dz, b.dg_post, b.dg_pre)]
+    b = bwd(c)
+    assert all(a is None or torch.equal(a, t) for a, t in zip(first, (b.dy, b.dr, b.dz, b.dg_post, b.dg_pre)))
+    # in place: dy over y, dr over what arrives for r', dz over z; then dy over dxn, dr over r
+    y, up, z, dxn, r = (None if c[k] is None else c[k].clone() for k in ("y", "dr_out", "z", "dxn", "r"))
+    ops.moe_block_norm_bwd(c["n"], y, c["r"], z, c["g_post"], c["g_pre"], c["stats"], up, c["dxn"], y, up, z, b.dg_post, b.dg_pre, b.ws)
+    assert all(a is None or torch.equal(a, t) for a, t in zip(first, (y, up, z, b.dg_post, b.dg_pre)))
+    ops.moe_block_norm_bwd(c["n"], c["y"], r, c["z"], c["g_post"], c["g_pre"], c["stats"], c["dr_out"], dxn, dxn, r, b.dz, b.dg_post, b.dg_pre, b.ws)
+    assert torch.equal(dxn, first[0]) and torch.equal(r, first[1])
