@@ -143,29 +143,25 @@ def _dev(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _buf(name: str, t, dtype, n: int, ref=None):
-    """Device pointer of a tensor that the call will touch n elements of: on
-    ref's device (a GPU), contiguous, of dtype, at least that large; None stays
-    NULL."""
+def _buf(name: str, t, dtype, n: int, dev: int):
+    """Device pointer of a tensor that the call will touch n elements of: on GPU
+    `dev`, contiguous, of dtype, at least that large; None stays NULL."""
     if t is None:
         return None
-    if (t.dtype != dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda or
-            (ref is not None and t.get_device() != ref.get_device())):
+    if t.dtype != dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         _dev(t)
-        where = "" if ref is None else f" on {ref.device}"
-        raise ValueError(f"{name}: needs {n} elements of {dtype}{where}, got {t.numel()} of {t.dtype} on {t.device}")
+        raise ValueError(f"{name}: needs {n} elements of {dtype} on cuda:{dev}, got {t.numel()} of {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _run(where: str, ref: torch.Tensor, stream, *args) -> int:
-    """Calls entry point `where` with ref's device current, on `stream` or that
+def _run(where: str, dev: int, stream, *args) -> int:
+    """Calls entry point `where` with GPU `dev` current, on `stream` or that
     device's current stream."""
-    fn, dev = getattr(load(), where), ref.get_device()
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if dev < 0:
+        raise TypeError("device buffers must be CUDA (HIP) torch tensors")
+    fn = getattr(_lib or load(), where)
+    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -591,24 +587,24 @@ def few_workspace_bytes(d: moe_desc, Is: int = 0) -> int:
 
 
 def _few_args(d, Is, routes, w, X, S13, S2, out, ws):
-    n, H, i32, f32, bf = d.P * d.Np, d.H, torch.int32, torch.float32, torch.bfloat16
-    return ([_buf("routes", routes, i32, n * d.K, X), _buf("w", w, f32, n * d.K, X), _buf("X", X, bf, n * H)],
-            [_buf("S13", S13, bf, 2 * Is * H, X), _buf("S2", S2, bf, Is * H, X), _buf("out", out, bf, n * H, X),
-             _buf("ws", ws, torch.uint8, 0, X), 0 if ws is None else ws.numel()])
+    n, H, i32, f32, bf, dev = d.P * d.Np, d.H, torch.int32, torch.float32, torch.bfloat16, X.get_device()
+    return ([_buf("routes", routes, i32, n * d.K, dev), _buf("w", w, f32, n * d.K, dev), _buf("X", X, bf, n * H, dev)],
+            [_buf("S13", S13, bf, 2 * Is * H, dev), _buf("S2", S2, bf, Is * H, dev), _buf("out", out, bf, n * H, dev),
+             _buf("ws", ws, torch.uint8, 0, dev), 0 if ws is None else ws.numel()])
 
 
 def moe_layer_fwd_few(d, Is, routes, w, X, W13, W2, S13, S2, out, ws, stream=None):
     head, tail = _few_args(d, Is, routes, w, X, S13, S2, out, ws)
-    n, bf = d.L * d.I * d.H, torch.bfloat16
-    return _run("moe_layer_fwd_few", X, stream, ctypes.byref(d), Is, *head, _buf("W13", W13, bf, 2 * n, X),
-                _buf("W2", W2, bf, n, X), *tail)
+    n, bf, dev = d.L * d.I * d.H, torch.bfloat16, X.get_device()
+    return _run("moe_layer_fwd_few", dev, stream, ctypes.byref(d), Is, *head, _buf("W13", W13, bf, 2 * n, dev),
+                _buf("W2", W2, bf, n, dev), *tail)
 
 
 def moe_layer_fwd_few_mx(d, Is, routes, w, X, W13q, W13s, W2q, W2s, S13, S2, out, ws, stream=None):
     head, tail = _few_args(d, Is, routes, w, X, S13, S2, out, ws)
-    n, u8 = d.L * d.I * d.H, torch.uint8
-    return _run("moe_layer_fwd_few_mx", X, stream, ctypes.byref(d), Is, *head, _buf("W13q", W13q, u8, 2 * n, X),
-                _buf("W13s", W13s, u8, 2 * n // 32, X), _buf("W2q", W2q, u8, n, X), _buf("W2s", W2s, u8, n // 32, X), *tail)
+    n, u8, dev = d.L * d.I * d.H, torch.uint8, X.get_device()
+    return _run("moe_layer_fwd_few_mx", dev, stream, ctypes.byref(d), Is, *head, _buf("W13q", W13q, u8, 2 * n, dev),
+                _buf("W13s", W13s, u8, 2 * n // 32, dev), _buf("W2q", W2q, u8, n, dev), _buf("W2s", W2s, u8, n // 32, dev), *tail)
 
 
 @dataclass
@@ -652,30 +648,30 @@ def block_norm_workspace_bytes(n: moe_norm_desc) -> int:
 
 
 def _norm_inputs(n, y, r, z, g_post, g_pre):
-    e, bf, f32 = n.rows * n.H, torch.bfloat16, torch.float32
+    e, bf, f32, dev = n.rows * n.H, torch.bfloat16, torch.float32, r.get_device()
     elem = n.gate == MOE_GATE_ELEM
-    return [_buf("y", y, bf, e, r), _buf("r", r, f32 if n.res_fp32 else bf, e),
-            _buf("z", z, bf if elem else f32, e if elem else n.rows, r), _buf("g_post", g_post, f32, n.H, r),
-            _buf("g_pre", g_pre, f32, n.H, r)]
+    return [_buf("y", y, bf, e, dev), _buf("r", r, f32 if n.res_fp32 else bf, e, dev),
+            _buf("z", z, bf if elem else f32, e if elem else n.rows, dev), _buf("g_post", g_post, f32, n.H, dev),
+            _buf("g_pre", g_pre, f32, n.H, dev)]
 
 
 def moe_block_norm_fwd(n, y, r, z, g_post, g_pre, r_out, xn, stats, stream=None):
-    e = n.rows * n.H
+    e, dev = n.rows * n.H, r.get_device()
     args = _norm_inputs(n, y, r, z, g_post, g_pre)
-    args += [_buf("r_out", r_out, r.dtype, e, r), _buf("xn", xn, torch.bfloat16, e, r),
-             _buf("stats", stats, torch.float32, 2 * n.rows, r)]
-    return _run("moe_block_norm_fwd", r, stream, ctypes.byref(n), *args)
+    args += [_buf("r_out", r_out, r.dtype, e, dev), _buf("xn", xn, torch.bfloat16, e, dev),
+             _buf("stats", stats, torch.float32, 2 * n.rows, dev)]
+    return _run("moe_block_norm_fwd", dev, stream, ctypes.byref(n), *args)
 
 
 def moe_block_norm_bwd(n, y, r, z, g_post, g_pre, stats, dr_out, dxn, dy, dr, dz, dg_post, dg_pre, ws, stream=None):
-    e, bf, f32 = n.rows * n.H, torch.bfloat16, torch.float32
+    e, bf, f32, dev = n.rows * n.H, torch.bfloat16, torch.float32, r.get_device()
     elem = n.gate == MOE_GATE_ELEM
     args = _norm_inputs(n, y, r, z, g_post, g_pre)
-    args += [_buf("stats", stats, f32, 2 * n.rows, r), _buf("dr_out", dr_out, r.dtype, e, r), _buf("dxn", dxn, bf, e, r),
-             _buf("dy", dy, bf, e, r), _buf("dr", dr, r.dtype, e, r),
-             _buf("dz", dz, bf if elem else f32, e if elem else n.rows, r), _buf("dg_post", dg_post, f32, n.H, r),
-             _buf("dg_pre", dg_pre, f32, n.H, r), _buf("ws", ws, torch.uint8, 0, r)]
-    return _run("moe_block_norm_bwd", r, stream, ctypes.byref(n), *args, 0 if ws is None else ws.numel())
+    args += [_buf("stats", stats, f32, 2 * n.rows, dev), _buf("dr_out", dr_out, r.dtype, e, dev), _buf("dxn", dxn, bf, e, dev),
+             _buf("dy", dy, bf, e, dev), _buf("dr", dr, r.dtype, e, dev),
+             _buf("dz", dz, bf if elem else f32, e if elem else n.rows, dev), _buf("dg_post", dg_post, f32, n.H, dev),
+             _buf("dg_pre", dg_pre, f32, n.H, dev), _buf("ws", ws, torch.uint8, 0, dev)]
+    return _run("moe_block_norm_bwd", dev, stream, ctypes.byref(n), *args, 0 if ws is None else ws.numel())
 
 
 @dataclass
@@ -717,10 +713,10 @@ def moe_ckpt_pack(src, q, scales, nrows=None, stream=None):
     """Pack a bf16 tensor [rows][cols] into int8 codes (same shape) and float
     scales [rows][cols/128]; nrows: a device int32 (one element, e.g.
     seg_off[L:]) that limits the rows packed."""
-    rows, cols = src.shape
-    args = [_buf("src", src, torch.bfloat16, 0), rows, cols, _buf("nrows", nrows, torch.int32, 1, src),
-            _buf("q", q, torch.int8, rows * cols, src), _buf("scales", scales, torch.float32, rows * (cols // CKPT_BLOCK), src)]
-    return _run("moe_ckpt_pack", src, stream, *args)
+    (rows, cols), dev = src.shape, src.get_device()
+    args = [_buf("src", src, torch.bfloat16, 0, dev), rows, cols, _buf("nrows", nrows, torch.int32, 1, dev),
+            _buf("q", q, torch.int8, rows * cols, dev), _buf("scales", scales, torch.float32, rows * (cols // CKPT_BLOCK), dev)]
+    return _run("moe_ckpt_pack", dev, stream, *args)
 
 
 def ckpt_pack(src, nrows=None, stream=None):
@@ -734,21 +730,21 @@ def ckpt_pack(src, nrows=None, stream=None):
 
 
 def moe_ckpt_swiglu_bwd(q, scales, dA, wrow, dHU, A, dw, nrows=None, stream=None):
-    rows, I = dA.shape
+    (rows, I), dev = dA.shape, dA.get_device()
     bf, f32 = torch.bfloat16, torch.float32
-    args = [_buf("q", q, torch.int8, 2 * rows * I, dA), _buf("scales", scales, f32, 2 * rows * I // CKPT_BLOCK, dA),
-            _buf("dA", dA, bf, 0), _buf("wrow", wrow, f32, rows, dA), rows, I, _buf("nrows", nrows, torch.int32, 1, dA),
-            _buf("dHU", dHU, bf, 2 * rows * I, dA), _buf("A", A, bf, rows * I, dA), _buf("dw", dw, f32, rows, dA)]
-    return _run("moe_ckpt_swiglu_bwd", dA, stream, *args)
+    args = [_buf("q", q, torch.int8, 2 * rows * I, dev), _buf("scales", scales, f32, 2 * rows * I // CKPT_BLOCK, dev),
+            _buf("dA", dA, bf, 0, dev), _buf("wrow", wrow, f32, rows, dev), rows, I, _buf("nrows", nrows, torch.int32, 1, dev),
+            _buf("dHU", dHU, bf, 2 * rows * I, dev), _buf("A", A, bf, rows * I, dev), _buf("dw", dw, f32, rows, dev)]
+    return _run("moe_ckpt_swiglu_bwd", dev, stream, *args)
 
 
 def moe_layer_bwd_ckpt(d, dOut, w, X, phi, route_row, seg_off, q, scales, W13, W2, dX, dW13, dW2, dw, ws, stream=None):
     cap, n, H, I = capacity_rows(d), d.P * d.Np, d.H, d.I
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    args = [_buf("dOut", dOut, bf, n * H, X), _buf("w", w, f32, n * d.K, X), _buf("X", X, bf, n * H),
-            _buf("phi", phi, i32, 2 * cap, X), _buf("route_row", route_row, i32, n * d.K, X),
-            _buf("seg_off", seg_off, i32, d.L + 1, X), _buf("q", q, torch.int8, cap * 2 * I, X),
-            _buf("scales", scales, f32, cap * 2 * I // CKPT_BLOCK, X), _buf("W13", W13, bf, d.L * 2 * I * H, X),
-            _buf("W2", W2, bf, d.L * H * I, X), _buf("dX", dX, bf, n * H, X), _buf("dW13", dW13, f32, d.L * 2 * I * H, X),
-            _buf("dW2", dW2, f32, d.L * H * I, X), _buf("dw", dw, f32, n * d.K, X), _buf("ws", ws, torch.uint8, 0, X)]
-    return _run("moe_layer_bwd_ckpt", X, stream, ctypes.byref(d), *args, 0 if ws is None else ws.numel())
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, X.get_device()
+    args = [_buf("dOut", dOut, bf, n * H, dev), _buf("w", w, f32, n * d.K, dev), _buf("X", X, bf, n * H, dev),
+            _buf("phi", phi, i32, 2 * cap, dev), _buf("route_row", route_row, i32, n * d.K, dev),
+            _buf("seg_off", seg_off, i32, d.L + 1, dev), _buf("q", q, torch.int8, cap * 2 * I, dev),
+            _buf("scales", scales, f32, cap * 2 * I // CKPT_BLOCK, dev), _buf("W13", W13, bf, d.L * 2 * I * H, dev),
+            _buf("W2", W2, bf, d.L * H * I, dev), _buf("dX", dX, bf, n * H, dev), _buf("dW13", dW13, f32, d.L * 2 * I * H, dev),
+            _buf("dW2", dW2, f32, d.L * H * I, dev), _buf("dw", dw, f32, n * d.K, dev), _buf("ws", ws, torch.uint8, 0, dev)]
+    return _run("moe_layer_bwd_ckpt", dev, stream, ctypes.byref(d), *args, 0 if ws is None else ws.numel())
