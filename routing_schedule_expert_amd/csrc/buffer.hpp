@@ -10,7 +10,8 @@ namespace moe {
 
 // [base, base + bytes); base and bytes wave-uniform (word 3 as for every raw
 // buffer on gfx9 parts).  A wave-uniform offset has to stay within `bytes`: the
-// range check compares the lane's offset with what is left after it.
+// range check compares each 4-byte word's lane offset with what is left after it,
+// so the words of a load that lie before the end are read and the others are zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t raw_buffer(const void *base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
 }
