@@ -365,8 +365,9 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
         store8<false>(bz, t, o);
         if (post || token) sum(s);
         const float c2 = post ? s[0] * inv_h : 0.f;
+        // without a post-norm dy is q itself, whatever y holds (an infinity times c2 = 0 would be NaN)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = ystd * fmaf(-yh[e], c2, D[e]);
+        for (int e = 0; e < 8; ++e) o[e] = post ? ystd * fmaf(-yh[e], c2, D[e]) : D[e];
         store8<false>(by, t, o);
         if (token && t == 0) static_cast<float *>(b.dz)[row] = s[1] * gt * (1.0f - gt);
     }
@@ -475,7 +476,7 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
             __builtin_amdgcn_sched_barrier(0);
         }
         if (pre || post || token) sum(s);
-        const float c1 = s[0] * inv_h, du = fmaf(-rstd * c1, s[2], s[1]), c2 = post ? du * inv_h : 0.f;
+        const float c1 = s[0] * inv_h, du = pre ? fmaf(-rstd * c1, s[2], s[1]) : s[1], c2 = post ? du * inv_h : 0.f;
         const __amdgpu_buffer_rsrc_t br = row_buffer<RS>(b.dr, row, H), by = row_buffer<2>(b.dy, row, H),
                                      bz = row_buffer<2>(elem ? b.dz : nullptr, row, H);
 #pragma unroll
@@ -491,7 +492,7 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
                 const float D = fmaf(rstd, fmaf(-x.xh, c1, x.t), cur.up[e]), dp = beta * D * x.gate;
                 dr[e] = alpha * D;
                 dz[e] = D * x.u * (1.0f - x.gate);
-                dy[e] = ystd * fmaf(-x.yh, c2, dp * go[e]);
+                dy[e] = post ? ystd * fmaf(-x.yh, c2, dp * go[e]) : dp;  // as above: q itself, whatever y holds
                 dp_yh[e] = dp * x.yh;
                 acc_pre[i][e] = fmaf(cur.dx[e], x.xh, acc_pre[i][e]);
             }

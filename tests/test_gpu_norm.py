@@ -320,3 +320,23 @@ def test_norm_long_rows(rows, H, gate, res):
     assert all(a is None or torch.equal(a, t) for a, t in zip(first, (y, up, z, b.dg_post, b.dg_pre)))
     ops.moe_block_norm_bwd(c["n"], c["y"], r, c["z"], c["g_post"], c["g_pre"], c["stats"], c["dr_out"], dxn, dxn, r, b.dz, b.dg_post, b.dg_pre, b.ws)
     assert torch.equal(dxn, first[0]) and torch.equal(r, first[1])
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("H", [1024, 9000, 20000])
+def test_norm_gradient_without_norms_ignores_y(H, gate):
+    # dr and dy do not depend on the block's output where nothing norms it, whatever it holds; the gate's gradient alone does
+    c = make(4, H, gate, post=False, pre=False, seed=H)
+    c["dr_out"][1, 5] = 1
+    fwd(c)
+    want = bwd(c)
+    c["y"][1, 5], c["y"][2, H - 1] = float("inf"), float("nan")
+    fwd(c)
+    got = bwd(c)
+    assert torch.equal(got.dr, want.dr) and torch.equal(got.dy, want.dy) and bool(got.dy.isfinite().all())
+    if gate == "token":
+        assert torch.equal(got.dz[[0, 3]], want.dz[[0, 3]]) and bool(got.dz[1].isinf()) and bool(got.dz[2].isnan())
+    if gate == "elem":
+        assert bool(got.dz[1, 5].isinf()) and bool(got.dz[2, H - 1].isnan())
+        got.dz[1, 5], got.dz[2, H - 1] = want.dz[1, 5], want.dz[2, H - 1]
+        assert torch.equal(got.dz, want.dz)
