@@ -149,6 +149,17 @@ struct NormGains {
 };
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// s = sigmoid(z) and 1 - s, which the gate's gradient needs, in one register: the smaller
+// of the two, its sign bit set where that is 1 - s.  The difference 1 - s itself would lose
+// its bits as the gate opens (at z = 11 all but 8, from z = 17 on s is 1); exp(-z) s does not.
+struct Gate {
+    float k;
+    __device__ __forceinline__ Gate() {}
+    __device__ __forceinline__ Gate(float e, float s) : k(e < 1.0f ? -(e * s) : s) {}  // e = exp(-z)
+    __device__ __forceinline__ bool rest_held() const { return (int)__float_as_uint(k) < 0; }
+    __device__ __forceinline__ float open() const { return rest_held() ? 1.0f + k : k; }
+    __device__ __forceinline__ float rest() const { return rest_held() ? -k : 1.0f - k; }
+};
 
 // The sum over a wave, on every lane: within rows of 16 lanes by rotations, then
 // across the four rows.
@@ -281,8 +292,17 @@ __device__ __forceinline__ void norm_fwd_body(const NormArgs &a, float *lds) {
     }
 }
 
+// A value that the compiler must hold as it is, not as others that it can be computed from.
+template <class T>
+__device__ __forceinline__ void keep(T &v) {
+    asm volatile("" : "+v"(v));
+}
+
 // Up to H = 8192: one chunk per thread, the row and the next one's loads in registers,
-// gains in LDS.
+// gains in LDS.  With an fp32 residual the registers are just enough: the gate is held in
+// eight (Gate; with exp(-z) and s beside each other 15 are spilled) and y as it lies in
+// memory, in four, not as yh: 20,000 rows of 4,096 take 353 us, 390 with yh held, which
+// spills 4; with bf16, where nothing is, holding y costs 4,095 rows of 2,048 31.7 us for 30.2.
 template <bool F32>
 __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) {
     constexpr int RS = F32 ? 4 : 2;
@@ -320,23 +340,28 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
     __syncthreads();
     for (; row < a.rows; row += gridDim.x) {
         const float ystd = post ? st_y : 1.0f, rstd = st_r;
-        const float gt = token ? sigmoid(zt) : 1.0f;
+        const float et = token ? __expf(-zt) : 0.0f, gt = __builtin_amdgcn_rcpf(1.0f + et);
         // yh, the gate, D (first what arrives for r'), t and xh of the row
-        float yh[8], gv[8], D[8], tv[8], xh[8], s[2] = {0.f, 0.f};
+        float yh[8], D[8], tv[8], xh[8], s[2] = {0.f, 0.f};
+        Gate gate[8];
         float go[8], gi[8];
         gains.load<true>(0, t, go);
         gains.load<true>(1, t, gi);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             yh[e] = y[e] * ystd;
-            gv[e] = elem ? sigmoid(z[e]) : gt;
+            const float ez = elem ? __expf(-z[e]) : et, gv = elem ? __builtin_amdgcn_rcpf(1.0f + ez) : gt;
+            gate[e] = Gate(ez, gv);
+            keep(gate[e].k);
             D[e] = up[e];
-            xh[e] = fmaf(beta * gv[e], yh[e] * go[e], alpha * r[e]) * rstd;
+            xh[e] = fmaf(beta * gv, yh[e] * go[e], alpha * r[e]) * rstd;
             const float d = dx[e];
             tv[e] = d * gi[e];
             acc_pre[e] = fmaf(d, xh[e], acc_pre[e]);
             s[0] = fmaf(tv[e], xh[e], s[0]);
         }
+        Raw8<false> yk = y;
+        if constexpr (F32) keep(yk.v);
         fetch(row + gridDim.x, row + gridDim.x < a.rows);
         if (pre) {
             sum(s);
@@ -354,10 +379,11 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
         gains.load<true>(0, t, go);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float d = beta * D[e], p = yh[e] * go[e];
-            o[e] = d * p * gv[e] * (1.0f - gv[e]);
+            if constexpr (F32) yh[e] = yk[e] * ystd;
+            const float d = beta * D[e], p = yh[e] * go[e], gv = gate[e].open();
+            o[e] = d * p * gv * gate[e].rest();
             s[1] = fmaf(d, p, s[1]);
-            const float dp = d * gv[e];
+            const float dp = d * gv;
             acc_post[e] = fmaf(dp, yh[e], acc_post[e]);
             D[e] = dp * go[e];  // q
             s[0] = fmaf(D[e], yh[e], s[0]);
@@ -369,7 +395,7 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = post ? ystd * fmaf(-yh[e], c2, D[e]) : D[e];
         store8<false>(by, t, o);
-        if (token && t == 0) static_cast<float *>(b.dz)[row] = s[1] * gt * (1.0f - gt);
+        if (token && t == 0) static_cast<float *>(b.dz)[row] = s[1] * gt * Gate(et, gt).rest();
     }
     if (post || pre) {
         const __amdgpu_buffer_rsrc_t bo = row_buffer<4>(post ? b.part : nullptr, 2 * (int64_t)blockIdx.x, H),
@@ -396,7 +422,7 @@ struct NormBwdChunk {
     }
 };
 struct NormBwdElem {
-    float yh, gate, u, xh, t;  // u = beta s p, the block's part of r'
+    float yh, e, gate, u, xh, t;  // e = exp(-z), gate = s; u = beta s p, the block's part of r'
 };
 
 // Past H = 8192 a row does not fit the registers beside the column sums (holding it
@@ -447,11 +473,13 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
     for (; row < a.rows; row += gridDim.x) {
         const bool more = row + gridDim.x < a.rows;
         fetch_row(wnext, row + gridDim.x, more);
-        const float ystd = post ? w.st_y : 1.0f, rstd = w.st_r, gt = token ? sigmoid(w.zt) : 1.0f;
+        const float ystd = post ? w.st_y : 1.0f, rstd = w.st_r, et = token ? __expf(-w.zt) : 0.0f,
+                    gt = __builtin_amdgcn_rcpf(1.0f + et);
         auto element = [&](const Chunk &k, int e, const float (&go)[8], const float (&gi)[8]) {
             NormBwdElem x;
             x.yh = k.y[e] * ystd;
-            x.gate = elem ? sigmoid(k.z[e]) : gt;
+            x.e = elem ? __expf(-k.z[e]) : et;
+            x.gate = elem ? __builtin_amdgcn_rcpf(1.0f + x.e) : gt;
             x.u = beta * x.gate * (x.yh * go[e]);
             x.xh = pre ? fmaf(alpha, k.r[e], x.u) * rstd : 0.f;
             x.t = k.dx[e] * gi[e];
@@ -491,7 +519,9 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
                 const NormBwdElem x = element(cur, e, go, gi);
                 const float D = fmaf(rstd, fmaf(-x.xh, c1, x.t), cur.up[e]), dp = beta * D * x.gate;
                 dr[e] = alpha * D;
-                dz[e] = D * x.u * (1.0f - x.gate);
+                // 1 - s as e s, e finite: where e is infinite, u is 0.  (Gate's form, with a selection an
+                // element, costs 8,000 rows of 16,384 532 us for 516.)
+                dz[e] = D * x.u * (fminf(x.e, __FLT_MAX__) * x.gate);
                 dy[e] = post ? ystd * fmaf(-x.yh, c2, dp * go[e]) : dp;  // as above: q itself, whatever y holds
                 dp_yh[e] = dp * x.yh;
                 acc_pre[i][e] = fmaf(cur.dx[e], x.xh, acc_pre[i][e]);
@@ -505,7 +535,7 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
             store8<false>(by, c, dy);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (token && t == 0) static_cast<float *>(b.dz)[row] = du * (1.0f - gt);
+        if (token && t == 0) static_cast<float *>(b.dz)[row] = du * Gate(et, gt).rest();
         w = wnext;
     }
     if (post || pre) {

@@ -340,3 +340,44 @@ def test_norm_gradient_without_norms_ignores_y(H, gate):
         assert bool(got.dz[1, 5].isinf()) and bool(got.dz[2, H - 1].isnan())
         got.dz[1, 5], got.dz[2, H - 1] = want.dz[1, 5], want.dz[2, H - 1]
         assert torch.equal(got.dz, want.dz)
+
+
+def column_steps(n):
+    """Additions in a row of the backward's column sums: a workgroup's rows, the partial rows that one thread of
+    the second launch takes, and its tree over the threads of a column (64 columns a workgroup, 16 up to H = 1024)."""
+    groups = ops.block_norm_workspace_bytes(n) // (8 * n.H)
+    cols = 16 if n.H <= 1024 else 64
+    return -(-n.rows // groups) + -(-groups * cols // 1024) + (1024 // cols).bit_length() - 1
+
+
+@pytest.mark.parametrize("gate,res", [("elem", "bf16"), ("elem", "fp32"), ("token", "bf16"), ("token", "fp32")])
+@pytest.mark.parametrize("rows,H", [(61, 776), (1030, 1032), (24, 8192), (19, 9000), (7, 20000)])
+def test_norm_gradient_of_open_and_closed_gates(rows, H, gate, res):
+    """Gates up to 10^-13 from open or closed.  s (1 - s) is what the gate's gradient scales with, so its error is
+    counted relative to that: exponentials of |z| <= 30 are off by 32 steps of 2^-24 each, in s and in 1 - s,
+    64 * 2^-24 = 2^-18 beside the other stages.  dz is compared with the formula itself (64 bits lose 1 - s too)."""
+    c = make(rows, H, gate, res, seed=H)
+    z = torch.linspace(-30, 30, c["z"].numel(), device=dev())[torch.randperm(c["z"].numel(), device=dev())]
+    c["z"] = z.reshape(c["z"].shape).to(c["z"].dtype)
+    n = c["n"]
+    ins = {k: dbl(c[k]) for k in ("y", "r", "z", "g_post", "g_pre")}
+    for k in ("y", "r", "g_post", "g_pre"):
+        ins[k].requires_grad_(True)
+    new, xn = formula(c, **ins)
+    ((new * dbl(c["dr_out"])).sum() + (xn * dbl(c["dxn"])).sum()).backward()
+    fwd(c)
+    b, m = bwd(c), mags(c)
+    more, sums = 2.0 ** -18, column_steps(n) * 2.0 ** -24
+    near("xn", c["xn"], xn.detach(), m["xn"], more)
+    near("dy", b.dy, ins["y"].grad, m["dy"], more)
+    near("dr", b.dr, ins["r"].grad, m["dr"], more)
+    near("dg_post", b.dg_post, ins["g_post"].grad, m["dg_post"], more + sums)
+    near("dg_pre", b.dg_pre, ins["g_pre"].grad, m["dg_pre"], more + sums)
+    z = ins["z"] if gate == "elem" else ins["z"].unsqueeze(1)
+    y = dbl(c["y"])
+    p = y * torch.rsqrt(y.square().mean(1, keepdim=True) + n.eps) * dbl(c["g_post"])
+    slope = n.beta * p * torch.sigmoid(z) * torch.sigmoid(-z)
+    want, mag = slope * ins["r"].grad / n.alpha, slope.abs() * m["dr"] / n.alpha
+    if gate == "token":
+        want, mag = want.sum(1), mag.sum(1)
+    near("dz", b.dz, want, mag, more)
