@@ -105,6 +105,32 @@ __host__ __device__ constexpr int few_gateup_words(int L, int R) {
 // The list in the down launch's LDS: numbers of routes and places in 16 bits.
 __host__ __device__ constexpr int few_list_words(int L, int R) { return 2 * few_max_experts(L, R) + 1 + R; }
 
+// LDS words of the down launch for `rows` places of C columns and their parts' sums,
+// one of each place for each wave, up to 32 KiB of parts, within `half` words beside the
+// list where the places alone fit that (a call's routes are rarely all local: the parts
+// then have the rows' unused space).
+__host__ __device__ constexpr int few_sum_words(int rows, int C, int waves, int half) {
+    const int sums = rows * C, parts = sums * waves < 8192 ? sums * waves : 8192;
+    return (sums + parts <= half ? sums + parts : sums > half ? sums : half) / 4 * 4;
+}
+// The parts, of S that are wanted, for n places whose parts' sums have `room` places: every
+// part of a round needs a tile of 8 places, or all of them.
+__host__ __device__ constexpr int few_fit_parts(int S, int n, int room) {
+    while (S > 1 && room < (n < 8 ? n : 8) * S) S /= 2;
+    return S;
+}
+constexpr bool few_small_calls_keep_their_parts() {
+    for (int B = 1; B <= 2; ++B)
+        for (int shared = 0; shared <= 1; ++shared)
+            for (int K = 1; K <= 64; ++K)  // one token, any number of its slots local
+                for (int n = 1; n <= K; ++n) {
+                    const int C = 8 * B, S = few_down_waves(B), room = few_sum_words(K + shared, C, S, 16384) / C - n - shared;
+                    if (few_fit_parts(S, n, room) != S || few_fit_parts(S, 1, room) != S) return false;
+                    if (room / S < n) return false;  // in one round
+                }
+    return true;
+}
+
 // Builds the list in LDS: count the routes of each expert (a route's rank is
 // the order in which the LDS atomics answer: it only says which MFMA column
 // computes the route, and columns are independent), take the experts of each
@@ -607,12 +633,17 @@ __device__ __forceinline__ void few_gateup_body(const FewArgs &a, int *lds) {
     }
 }
 
-// Parts of a reduction dimension of `inner` elements: at least 512 bytes of a
-// row each, a power of two up to the waves.
+// Parts of a reduction dimension of `inner` elements, for n places: a power of two
+// up to the waves, each part with at least 512 bytes of a row, or 2 KiB where the
+// places are one tile or less: there the parts' join costs more than a shorter
+// stream saves (down launch, one token, 4 experts and the shared one of H = 4096, I =
+// 1024: 12.2 us with one part, 15.8 with four; 2 experts of H = 7168, I = 2048, MXFP8:
+// 11.8 and 13.2, bf16 15.9 with one, 15.5 with two or four; one expert's 16 routes of H =
+// 7168, I = 2048: 13.6 with one, 13.1 with four, its 64: 31.3 and 20.5).
 template <bool MX>
-__device__ __forceinline__ int few_parts(int inner, int waves) {
+__device__ __forceinline__ int few_parts(int inner, int n, int waves) {
     int S = waves;
-    while (S > 1 && inner < (MX ? 512 : 256) * S) S /= 2;
+    while (S > 1 && inner * (MX ? 1 : 2) < (n <= 8 ? 2048 : 512) * S) S /= 2;
     return S;
 }
 
@@ -705,8 +736,7 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
         __syncthreads();
     };
     if (a.Is) {  // every token's column: all waves share it
-        int S = few_parts<false>(a.Is, kWaves);
-        while (S > 1 && room < 8 * S) S /= 2;
+        const int S = few_fit_parts(few_parts<false>(a.Is, a.T, kWaves), a.T, room);
         const int cap = S > 1 ? room / S : a.T;
         const FewMatrix W{reinterpret_cast<const uint8_t *>(a.S2), nullptr, nullptr, a.Is};
         for (int base = 0; base < a.T; base += cap) {
@@ -721,10 +751,10 @@ __device__ __forceinline__ void few_down_body(const FewArgs &a, int *lds) {
             if (S > 1) join(n + base, n + end, S, cap);
         }
     }
-    const int most = few_parts<MX>(a.I, kWaves);
+    const int most = few_parts<MX>(a.I, n, kWaves);
     int S = 1;
     while (S < most && (na * S < 4 * kWaves || 15 * ((na * S + kWaves - 1) / kWaves) * kWaves > 16 * na * S)) S *= 2;
-    while (S > 1 && room < 8 * S) S /= 2;
+    S = few_fit_parts(S, n, room);
     const int part = wave % S, group = wave / S, groups = kWaves / S, cap = S > 1 ? room / S : n;
     const int wide = wave_uniform(a.plan[3]), mid = wave_uniform(a.plan[4]);
     for (int base = 0, from = 0; base < n; base += cap) {

@@ -1653,21 +1653,18 @@ int few_launch(const moe_desc *d, int32_t Is, FewArgs a, void *ws, hipStream_t s
     a.plan = static_cast<int32_t *>(ws);
     a.act = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + few_plan_bytes(d));
     const int rows = few_rows(d, Is);
-    // down launch: 16 output columns a workgroup, 8 where that leaves CUs without
-    // one.  LDS: the sums of every row and 32 KiB for their parts, but no more than
-    // half a CU's where the rows fit that (the calls' routes are rarely all local:
-    // the parts then have the rows' unused space)
+    // down launch: 16 output columns a workgroup, 8 where that leaves CUs without one;
+    // no more than half a CU's LDS where the rows fit that
     const int C = a.H / 16 < device_cus() ? 8 : 16, waves = few_down_waves(C / 8);
-    const size_t list = 4 * (size_t)few_list_words(a.L, a.R), sums = 4 * (size_t)rows * C;
+    const int list = few_list_words(a.L, a.R);
     const size_t lds_gu = 4 * (size_t)few_gateup_words(a.L, a.R);
-    size_t lds_down = list + sums + std::min<size_t>(32 << 10, sums * (waves - 1));
-    if (lds_down > kMaxLds / 2) lds_down = std::max(list + sums, kMaxLds / 2);
     // the largest calls: 4096 experts, 1024 routes, and every slot a token of its own with the shared expert's row
     static_assert(4 * few_gateup_words(4096, kFewMaxRoutes) <= (int)kMaxLds &&
                       4 * (few_list_words(4096, kFewMaxRoutes) + 2 * kFewMaxRoutes * 16) <= (int)kMaxLds,
                   "every call that few_check lets through fits the LDS");
-    a.words = (int)((lds_down - list) / 16) * 4;
-    lds_down = list + 4 * (size_t)a.words;
+    static_assert(few_small_calls_keep_their_parts(), "the sums of one token's parts fit beside its places");
+    a.words = few_sum_words(rows, C, waves, (int)kMaxLds / 8 - list);
+    const size_t lds_down = 4 * (size_t)(list + a.words);
     const int64_t units = (int64_t)few_max_experts(a.L, a.R) * (a.I / kFewRows) + (a.T + 63) / 64 * (Is / kFewRows);
     {
         TraceScope tr("few_gateup", s);

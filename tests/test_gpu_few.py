@@ -259,3 +259,13 @@ def test_few_binding_refuses_wrong_buffers():
         ops.moe_layer_fwd_few(d, 0, c["routes"], c["w"], c["X"], c["W13"][:3].contiguous(), c["W2"], None, None, b.out, b.ws)
     with pytest.raises(ops.MoeError):
         ops.moe_layer_fwd_few(d, 0, c["routes"], c["w"], c["X"], c["W13"], c["W2"], None, None, b.out, b.ws[:64])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("H", [2048, 7168])
+@pytest.mark.parametrize("K,local,Is", [(1, 1, 0), (2, 1, 0), (2, 2, 0), (4, 3, 0), (1, 1, 2048), (4, 4, 2048), (6, 1, 0), (8, 8, 2048)])
+def test_few_one_token_in_parts(K, local, Is, H, mx):
+    # the smallest calls: few experts, so the waves of a down workgroup take parts of their rows
+    ids = [[3 - 2 * j if j < local and j < 2 else 2 + j % 2 if j < local else 9 for j in range(K)]]
+    c = make(1, 1, K, 10, 3, 1, H, 2048, Is, mx, ids=ids, seed=K + local)
+    check(c, call(c))
