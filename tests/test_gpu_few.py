@@ -269,3 +269,42 @@ def test_few_one_token_in_parts(K, local, Is, H, mx):
     ids = [[3 - 2 * j if j < local and j < 2 else 2 + j % 2 if j < local else 9 for j in range(K)]]
     c = make(1, 1, K, 10, 3, 1, H, 2048, Is, mx, ids=ids, seed=K + local)
     check(c, call(c))
+
+
+def spread(counts, T, K):
+    """Routes of T tokens with K slots, counts[e] of them to expert e and the others nowhere, in no order."""
+    flat = np.full(T * K, -1, np.int32)
+    flat[:sum(counts)] = np.repeat(np.arange(len(counts)), counts)
+    return np.random.Generator(np.random.PCG64(sum(counts))).permutation(flat).reshape(T, K)
+
+
+# T, K, the experts' routes, H, I, Is.  The four waves of a down workgroup of 16 output columns (H >= 4096 on 256 CUs),
+# or eight at 8 columns, are parts of an expert's rows times groups of experts; the parts' sums meet in rounds, as many
+# places at a time as there is LDS for.  Experts with up to 8, 16, 32, 64 routes and more, alone and together:
+DOWN = [
+    (7, 2, [7, 4], 4096, 1024, 0),               # four parts of bf16, two of MXFP8
+    (12, 2, [12, 9], 4096, 2048, 512),           # four parts of both, two of the shared expert
+    (24, 2, [24, 20], 4096, 1024, 0),
+    (50, 2, [50, 41], 7168, 2048, 2048),
+    (70, 2, [70, 69], 4096, 1024, 512),
+    (64, 2, [40, 30, 15, 11, 6, 1], 4096, 1024, 0),
+    (20, 8, [24, 20, 20, 20, 20, 17, 9, 3], 4096, 1024, 0),   # two parts
+    (12, 16, [12, 12, 12, 20, 1, 8, 9, 7, 16, 17, 2, 3, 33, 4, 5, 6], 4096, 512, 512),  # whole rows
+    (100, 2, [100, 90], 4096, 1024, 512),        # two rounds, the second expert in both
+    (128, 8, [500, 300, 200, 13, 4], 4096, 1024, 0),          # 49 places a round
+    (300, 1, [140, 100, 30, 12, 6], 4096, 1024, 1024),        # three rounds, the shared expert's tokens too
+    (300, 1, [140, 100, 30, 12, 6], 512, 4096, 2048),         # eight waves, eight parts, three rounds
+    (128, 8, [500, 300, 200, 13, 4], 256, 2048, 2048),
+    (33, 3, [33, 9, 17, 1], 512, 4096, 128),
+    (1024, 1, [600, 424], 4096, 1024, 2048),     # no room for parts
+    (1024, 1, [600, 400], 256, 2048, 2048),      # 20 rounds
+]
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,K,counts,H,I,Is", DOWN)
+def test_few_down_tiles_parts_and_rounds(T, K, counts, H, I, Is, mx):
+    c = make(1, T, K, len(counts), len(counts), 0, H, I, Is, mx, ids=spread(counts, T, K), seed=T)
+    out = call(c).clone()
+    check(c, out)
+    assert torch.equal(call(c), out)
