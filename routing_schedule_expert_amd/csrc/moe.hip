@@ -1895,7 +1895,11 @@ int moe_ckpt_swiglu_bwd(const int8_t *q, const float *scales, const uint16_t *dA
     if (!q || !scales || !dA || !dHU || !aligned16(q) || !aligned4(scales) || !aligned16(dA) || !aligned4(wrow) ||
         !aligned4(nrows) || !aligned16(dHU) || !aligned16(A) || !aligned4(dw))
         return MOE_EINVAL;
-    const int lanes = I >= 1024 ? 64 : I >= 512 ? 32 : I >= 256 ? 16 : 8;
+    // as many lanes as take a row in one step, even where some then have no column (some
+    // 300 MB, us with 8 / 16 / 32 / 64 lanes: I = 128 50 / 54 / 88 / 163, 256 53 / 50 / 55 / 87,
+    // 384 56 / 54 / 50 / 64, 512 55 / 53 / 49 / 54, 640 58 / 56 / 54 / 50, 1152 62 / 60 / 56 / 55,
+    // 4096 70 / 67 / 58 / 55; 2,000 rows: 768 12.4 / 8.0 / 6.7 / 5.9)
+    const int lanes = I > 512 ? 64 : I > 256 ? 32 : I > 128 ? 16 : 8;
     const int64_t wgs = (rows * lanes + kCkptThreads - 1) / kCkptThreads;
     const int grid = (int)std::min<int64_t>(wgs, kCkptGrid * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);
