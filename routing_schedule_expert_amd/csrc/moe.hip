@@ -1857,7 +1857,10 @@ int moe_block_norm_bwd(const moe_norm_desc *n, const uint16_t *y, const void *r,
     }
     if (!sums) return MOE_OK;
     TraceScope tr("block_norm_dg", s);
-    if (n->H <= 1024)  // few columns: fewer of them and more partial rows to a workgroup
+    // few columns: 16 of them and more partial rows to a workgroup instead of 64 (us with 16 / 64: H = 512
+    // 7.0 / 11.3 of 2,048 partial rows, 1,032 5.7 / 7.5 and 1,536 6.4 / 7.1 of 1,024, 2,048 5.0 / 5.0 and 4,096
+    // 7.5 / 5.1 of 512)
+    if (n->H < 2048)
         hipLaunchKernelGGL(k_norm_dg<16>, dim3((n->H + 15) / 16, 2), dim3(1024), 0, s, b.part, grid, n->H, dg_post, dg_pre);
     else
         hipLaunchKernelGGL(k_norm_dg<64>, dim3((n->H + 63) / 64, 2), dim3(1024), 0, s, b.part, grid, n->H, dg_post, dg_pre);

@@ -344,9 +344,9 @@ def test_norm_gradient_without_norms_ignores_y(H, gate):
 
 def column_steps(n):
     """Additions in a row of the backward's column sums: a workgroup's rows, the partial rows that one thread of
-    the second launch takes, and its tree over the threads of a column (64 columns a workgroup, 16 up to H = 1024)."""
+    the second launch takes, and its tree over the threads of a column (16 columns a workgroup below H = 2048, or 64)."""
     groups = ops.block_norm_workspace_bytes(n) // (8 * n.H)
-    cols = 16 if n.H <= 1024 else 64
+    cols = 16 if n.H < 2048 else 64
     return -(-n.rows // groups) + -(-groups * cols // 1024) + (1024 // cols).bit_length() - 1
 
 
