@@ -159,6 +159,8 @@ def _run(where: str, dev: int, stream, *args) -> int:
     device's current stream."""
     if dev < 0:
         raise TypeError("device buffers must be CUDA (HIP) torch tensors")
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"{where}: the stream is on cuda:{stream.device_index}, the buffers on cuda:{dev}")
     fn = getattr(_lib or load(), where)
     stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev:

@@ -1,6 +1,7 @@
 """Host-side checks of the few-token layer, the block norms and the 8-bit
 checkpoints (no GPU needed): sizes, and refusals before anything is launched."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 
@@ -166,3 +167,14 @@ def test_layer_bwd_ckpt_refusals():
     assert lib.moe_layer_bwd_ckpt(ctypes.byref(two), *args, ws, None) == ops.MOE_EINVAL
     odd = ops.make_desc(8, 7168, 8, 384, 48, H=7000, I=2048)
     assert lib.moe_layer_bwd_ckpt(ctypes.byref(odd), *args, ws, None) == ops.MOE_EUNSUPPORTED
+
+
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    # a kernel on one GPU's stream with another's buffers: refused before anything is called
+    called = []
+    monkeypatch.setattr(ops, "_lib", SimpleNamespace(moe_ckpt_pack=lambda *a: called.append(a)))
+    with pytest.raises(ValueError, match="cuda:1"):
+        ops._run("moe_ckpt_pack", 0, SimpleNamespace(device_index=1, cuda_stream=0))
+    with pytest.raises(ValueError, match="cuda:0"):
+        ops._run("moe_ckpt_pack", 3, SimpleNamespace(device_index=0, cuda_stream=0))
+    assert not called
