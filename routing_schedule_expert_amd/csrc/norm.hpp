@@ -340,7 +340,7 @@ __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs &b, float *lds) 
     __syncthreads();
     for (; row < a.rows; row += gridDim.x) {
         const float ystd = post ? st_y : 1.0f, rstd = st_r;
-        const float et = token ? __expf(-zt) : 0.0f, gt = __builtin_amdgcn_rcpf(1.0f + et);
+        const float et = token ? __expf(-zt) : 0.0f, gt = token ? __builtin_amdgcn_rcpf(1.0f + et) : 1.0f;
         // yh, the gate, D (first what arrives for r'), t and xh of the row
         float yh[8], D[8], tv[8], xh[8], s[2] = {0.f, 0.f};
         Gate gate[8];
@@ -474,7 +474,7 @@ __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *
         const bool more = row + gridDim.x < a.rows;
         fetch_row(wnext, row + gridDim.x, more);
         const float ystd = post ? w.st_y : 1.0f, rstd = w.st_r, et = token ? __expf(-w.zt) : 0.0f,
-                    gt = __builtin_amdgcn_rcpf(1.0f + et);
+                    gt = __builtin_amdgcn_rcpf(1.0f + et);  // 1 without a gate
         auto element = [&](const Chunk &k, int e, const float (&go)[8], const float (&gi)[8]) {
             NormBwdElem x;
             x.yh = k.y[e] * ystd;
