@@ -548,9 +548,9 @@ int moe_layer_bwd_ring(const moe_desc *d, int32_t mb_tokens, int32_t ring_slots,
  * the combine; this call does not, so the two differ by that rounding).
  * Only the weights of experts that a slot names are read, once for every 64 slots
  * that name the expert: up to about 64 each the call beats moe_layer_fwd (8 experts of
- * H = 7168, I = 2048: 135 against 316 us at 16 slots each, 247 against 314 at 64), past
- * that it loses (427 against 319 at 96) except with few experts or small ones (one
- * expert: 183 against 241 us at 256 slots).
+ * H = 7168, I = 2048: 135 against 316 us at 16 slots each, 245 against 313 at 64), past
+ * that it loses (426 against 317 at 96) except with few experts or small ones (one
+ * expert: 184 against 241 us at 256 slots).
  *   routes int32 [P][Np][K]   w float [P][Np][K]   X bf16 [P][Np][H]
  *   W13 bf16 [L][2I][H]       W2 bf16 [L][H][I]
  *   Is, S13, S2  the shared expert ([BPT] section 2.C; S[t] = S2 (silu(gate) *
@@ -563,7 +563,10 @@ int moe_layer_bwd_ring(const moe_desc *d, int32_t mb_tokens, int32_t ring_slots,
  *        (MOE_WS_INVALID_IDS of the other calls)
  * Needs P*Np*K <= 1024 (else MOE_EUNSUPPORTED: moe_layer_fwd takes those),
  * H % 256 == 0 and I % 128 == 0, d->num_batches == 1; every pointer 16-byte
- * aligned.  pad_rows and sched_threads play no part.  A slot may name the same
+ * aligned.  X, the activations (slots and, with a shared expert, tokens, times
+ * the larger of I and Is) and 16 rows of any weight stay below 2 GiB each (else
+ * MOE_EUNSUPPORTED).  pad_rows and sched_threads play no part, but are checked
+ * as for the other calls.  A slot may name the same
  * expert as another slot of its token; both count.  X and w of slots that are
  * not local are not read into any sum, and a token's output does not depend on
  * the X and w of other tokens (their routes can change the order of its fp32
@@ -623,7 +626,9 @@ int moe_layer_fwd_few_mx(const moe_desc *d, int32_t Is, const int32_t *routes, c
  *   dxn    bf16 [rows][H]   gradient of xn, NULL exactly where g_pre is
  *   dy     bf16 [rows][H] out, NULL exactly where y is; may be y or dxn itself
  *   dr     [rows][H] out    may be r or dr_out itself
- *   dz     as z, out, NULL exactly where z is; may be z itself
+ *   dz     as z, out, NULL exactly where z is; may be z itself.  beta p s (1 - s) times
+ *          the gradient of r' (summed over a token's row), with 1 - s to fp32's relative
+ *          accuracy however open the gate is
  *   dg_post, dg_pre  float [H] out, NULL exactly where g_post / g_pre are; zeros
  *                           for rows = 0
  *   ws >= moe_block_norm_workspace_bytes(n) (unused without g_post and g_pre:

@@ -29,14 +29,15 @@
 // against 241 for 128, 61 against 47 for 37 tokens of 64 experts, and 118 against 61
 // for 32 tokens with MXFP8 weights (30 against 16 for 4).
 //
-// Measured (launches alone; a read-only kernel gets 7.1 TB/s; each launch spends
-// about 5 us before its stream flows and after it ends):
+// Measured (launches alone, rates of the weights of the experts that are hit; a
+// read-only kernel gets 7.1 TB/s; each launch spends about 5 us before its stream
+// flows and after it ends):
 //   full-size share (H = 7168, I = 2048, 48 local experts, top-8 of 384)
-//     8 tokens, 8 experts hit    gate/up 70 us (6.7 TB/s)   down 39 us (6.0 TB/s)
-//     128 tokens + shared expert gate/up 427 us (6.5 TB/s)  down 240 us (5.7 TB/s)
-//     32 tokens, MXFP8           gate/up 108 us (6.4 TB/s)  down 62 us (5.6 TB/s)
-//   H = 2048, I = 1024, 64 experts, 37 tokens + shared expert
-//                                gate/up 90 us (5.9 TB/s)   down 47 us (5.7 TB/s)
+//     8 tokens, 7 experts         gate/up 64 us (6.4 TB/s)   down 35 us (5.8 TB/s)
+//     128 tokens, 46 and shared   gate/up 427 us (6.5 TB/s)  down 245 us (5.6 TB/s)
+//     32 tokens, MXFP8, 17        gate/up 86 us (6.0 TB/s)   down 53 us (4.9 TB/s)
+//   H = 2048, I = 1024, 37 tokens, 64 experts and the shared one
+//                                 gate/up 93 us (5.8 TB/s)   down 48 us (5.7 TB/s)
 #pragma once
 
 #include "buffer.hpp"

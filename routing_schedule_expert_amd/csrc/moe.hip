@@ -1764,9 +1764,9 @@ int norm_threads(const moe_norm_desc *n) {
 }
 // Workgroups of the backward, each leaving one row of partial sums.  At few waves
 // (H <= 1536) many, each with four rows at least, or the CUs run dry between rows
-// (30,000 rows of 640: 76 us with 2048, 140 with 512); above, those that a
-// 256-CU part holds at once, at most 512 (4,095 rows of 2,056, fp32: 44 us against 54
-// with 768 and 56 with 256).
+// (30,000 rows of 640: 71 us with 2048, 86 with 1024, 142 with 512); above, those that a
+// 256-CU part holds at once, at most 512 (4,095 rows of 2,056, fp32, with the
+// sums' launch: 46 us against 50 with 768 and 54 with 256).
 int64_t norm_groups(const moe_norm_desc *n) {
     const int waves = norm_threads(n) / 64;
     if (waves <= 3) return std::min<int64_t>((n->rows + 3) / 4, waves <= 2 ? 2048 : 1024);

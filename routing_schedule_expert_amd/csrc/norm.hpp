@@ -26,8 +26,9 @@
 //     spare lanes read zeros, so the loop has no branch around a memory access and
 //     the compiler waits for exactly the loads it needs.
 // Measured: 57,344 rows of 7,168 with a gate per element, forward 0.79 ms (5.2
-// TB/s; 1.15 ms with the gains read from L2 in the loop); 16,384 rows, backward 0.37
-// ms and 5 us for the column sums (5.1 TB/s); a copy of 4 GiB gets 4.9 to 5.4 TB/s.
+// TB/s; 1.15 ms with the gains read from L2 in the loop); 16,384 rows, backward 0.36
+// to 0.38 ms and 5 us for the column sums (5.0 to 5.1 TB/s); a copy of 4 GiB gets 4.9 to
+// 5.4 TB/s.
 #pragma once
 
 #include "buffer.hpp"
@@ -433,7 +434,7 @@ struct NormBwdElem {
 //   S1 = sum t xh,  S2 = sum u (dr' + rstd(r') t),  S3 = sum u xh
 // give both means, mean(t xh) = S1 / H and, because q yh = D u, mean(q yh) =
 // (S2 - rstd(r') S1 S3 / H) / H.  (The same single reduction in the body above costs
-// the registers that hold the next row: 4,095 rows of 2,056 in fp32 56 us, from 44.)
+// the registers that hold the next row: 4,095 rows of 2,056 in fp32 took 56 us for 44.)
 template <bool F32, int CH>
 __device__ __forceinline__ void norm_bwd_wide_body(const NormBwdArgs &b, float *lds) {
     constexpr int RS = F32 ? 4 : 2;
