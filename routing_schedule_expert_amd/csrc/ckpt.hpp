@@ -9,8 +9,8 @@
 // block maximum keeps a Gaussian block to 0.6% rms, against 2.6% for an 8-bit
 // float's relative step; the scale adds 3% to the bytes.
 //
-// Measured: 61,440 rows of I = 2048, pack 139 us (5.5 TB/s), SwiGLU backward 244 us
-// (5.2 TB/s); a copy of 4 GiB gets 4.9 to 5.4 TB/s.  Both are bound by HBM.
+// Measured: 61,440 rows of I = 2048, pack 139 us (5.5 TB/s), SwiGLU backward 244 to
+// 252 us (5.0 to 5.2 TB/s); a copy of 4 GiB gets 4.9 to 5.4 TB/s.  Both are bound by HBM.
 //
 // Of the three buffers the bf16 backward keeps per dispatched row (Xd, HU, A:
 // H + 3 I elements of 2 bytes) only HU's codes remain (2 I bytes and their

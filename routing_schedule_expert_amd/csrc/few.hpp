@@ -115,9 +115,13 @@ __host__ __device__ constexpr int few_sum_words(int rows, int C, int waves, int 
     return (sums + parts <= half ? sums + parts : sums > half ? sums : half) / 4 * 4;
 }
 // The parts, of S that are wanted, for n places whose parts' sums have `room` places: every
-// part of a round needs a tile of 8 places, or all of them.
+// part of a round needs 16 places, or all of them.  A round reads the weights of its experts
+// again: 1,000 routes of two experts of H = 7168, I = 2048 with a shared one took 985 us of 512
+// tokens and 1,284 of 1,024 (MXFP8 1,108 and 1,410) in rounds of 12 places, and 846 and 1,213
+// (854 and 1,220) with half the parts or one; with more places parts win (900 routes of 1,024
+// tokens: 727 us with four parts and rounds of 31, 855 with two, 1,210 with one).
 __host__ __device__ constexpr int few_fit_parts(int S, int n, int room) {
-    while (S > 1 && room < (n < 8 ? n : 8) * S) S /= 2;
+    while (S > 1 && room < (n < 16 ? n : 16) * S) S /= 2;
     return S;
 }
 constexpr bool few_small_calls_keep_their_parts() {
