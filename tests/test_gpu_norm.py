@@ -381,3 +381,24 @@ def test_norm_gradient_of_open_and_closed_gates(rows, H, gate, res):
     if gate == "token":
         want, mag = want.sum(1), mag.sum(1)
     near("dz", b.dz, want, mag, more)
+
+
+@pytest.mark.parametrize("gate", ["token", "elem"])
+@pytest.mark.parametrize("H", [1032, 9000])
+def test_norm_gates_shut_and_open_for_good(H, gate):
+    # gates of minus and plus infinity are those of -200 and 200: nothing passes, or all of it, and no gradient reaches them
+    c = make(6, H, gate, seed=H)
+    out = []
+    for far in (200.0, float("inf")):
+        c["z"][0], c["z"][1] = -far, far
+        if gate == "elem":
+            c["z"][3, 7], c["z"][3, H - 1] = far, -far
+        fwd(c)
+        b = bwd(c)
+        out.append([t.clone() for t in (c["r_out"], c["xn"], b.dr, b.dy, b.dz, b.dg_post, b.dg_pre)])
+    for a, t in zip(*out):
+        assert torch.equal(a, t) and bool(t.isfinite().all())
+    dz = out[1][4]
+    assert not dz[:2].any() and not out[1][3][0].any() and bool(dz[2:].any())
+    if gate == "elem":
+        assert not dz[3, 7] and not dz[3, H - 1]
