@@ -564,9 +564,9 @@ int moe_layer_bwd_ring(const moe_desc *d, int32_t mb_tokens, int32_t ring_slots,
  * Needs P*Np*K <= 1024 (else MOE_EUNSUPPORTED: moe_layer_fwd takes those),
  * H % 256 == 0 and I % 128 == 0, d->num_batches == 1; every pointer 16-byte
  * aligned.  X, the activations (slots and, with a shared expert, tokens, times
- * the larger of I and Is) and 16 rows of any weight stay below 2 GiB each (else
- * MOE_EUNSUPPORTED).  pad_rows and sched_threads play no part, but are checked
- * as for the other calls.  A slot may name the same
+ * the larger of I and Is) and 16 rows of any weight stay below 2 GiB each, 768 I
+ * and 768 Is below 2^30 (else MOE_EUNSUPPORTED).  pad_rows and sched_threads play
+ * no part, but are checked as for the other calls.  A slot may name the same
  * expert as another slot of its token; both count.  X and w of slots that are
  * not local are not read into any sum, and a token's output does not depend on
  * the X and w of other tokens (their routes can change the order of its fp32
