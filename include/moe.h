@@ -701,6 +701,146 @@ int moe_layer_bwd_ckpt(const moe_desc *d, const uint16_t *dOut, const float *w, 
                        size_t ws_bytes, void *stream);
 
 /*
+ * Element types of the calls below.
+ */
+enum {
+    MOE_TYPE_BF16 = 0,
+    MOE_TYPE_FP16 = 1,
+    MOE_TYPE_FP32 = 2,
+};
+
+/*
+ * moe_gated_ffn_fwd — the gated feed-forward block of dense layers and of the shared
+ * expert, for any number of rows: with W13 = [Wg; Wu],
+ *     h = X Wg^T,  u = X Wu^T,  a = act(h) u  (rounded once to 16 bits),  out = a W2^T
+ * (moe_layer_fwd_shared runs the shared expert beside the routed ones, for 256-row tiles.)
+ *   n    host descriptor: rows (>= 0), H and I (multiples of 8, at most 65536), act
+ *        (MOE_ACT_*; GELU is x Phi(x), GELU_TANH its tanh form), type (of every 16-bit
+ *        buffer: MOE_TYPE_BF16 or MOE_TYPE_FP16), ldx (elements from one row of X and
+ *        dX to the next; 0: H) and ldo (the same of out and dOut), multiples of 8, at
+ *        least H, at most 2^20
+ *   X    [rows][H]    W13 [2I][H]    W2 [H][I]
+ *   HU   [rows][2I] out, nullable    h and u rounded, which the backward needs
+ *   A    [rows][I] out               a
+ *   out  [rows][H] out
+ *   ws >= moe_gated_ffn_workspace_bytes(n, 0)
+ *
+ * moe_gated_ffn_bwd — its gradient:
+ *     dA = dOut W2,  dh = dA u act'(h),  du = dA act(h)   (rounded once to 16 bits)
+ *     dX = [dh du] W13,  dW13 = [dh du]^T X,  dW2 = dOut^T a
+ *   dOut [rows][H]    X, HU, W13, W2 as the forward had or left them
+ *   A    [rows][I], nullable: a is computed again from HU (and rounded as above)
+ *   dX   [rows][H] out, nullable
+ *   dW13 [2I][H], dW2 [H][I] out, each nullable, of dw_type: MOE_TYPE_FP32 or n->type.
+ *        accumulate = 1 (fp32 only) adds to what they hold.  Zeros for rows = 0
+ *   ws >= moe_gated_ffn_workspace_bytes(n, 1)
+ * Outputs must not overlap inputs or each other.  Pointers 16-byte aligned; what lies
+ * between rows (ldx, ldo > H) is neither read nor written.  A row's out, HU, A and dX
+ * depend on that row alone.  Every sum is fp32, in an order that depends on the sizes
+ * only: repeated calls give bitwise the same.
+ * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for H, I or a stride that is not a
+ * multiple of 8 or past its limit, I * H >= 2^30 or rows >= 2^30.  With rows = 0 the row buffers
+ * may be NULL.  moe_gated_ffn_workspace_bytes returns -1 for an n that the calls refuse.
+ */
+enum {
+    MOE_ACT_SILU = 0,
+    MOE_ACT_GELU = 1,
+    MOE_ACT_GELU_TANH = 2,
+    MOE_ACT_RELU = 3,
+};
+typedef struct moe_ffn_desc {
+    int64_t rows, ldx, ldo;
+    int32_t H, I, act, type;
+} moe_ffn_desc;
+int64_t moe_gated_ffn_workspace_bytes(const moe_ffn_desc *n, int32_t bwd);
+int moe_gated_ffn_fwd(const moe_ffn_desc *n, const uint16_t *X, const uint16_t *W13, const uint16_t *W2, uint16_t *HU,
+                      uint16_t *A, uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+int moe_gated_ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_t *X, const uint16_t *HU,
+                      const uint16_t *A, const uint16_t *W13, const uint16_t *W2, uint16_t *dX, void *dW13, void *dW2,
+                      int32_t dw_type, int32_t accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_layer_norm_fwd — layer norm of every row, in fp32:
+ *     m = mean(x),  s = 1 / sqrt(mean((x - m)^2) + eps),  y = (x - m) s g + b
+ *   n      host descriptor: rows (>= 0), H (1 to 32768), x_type, y_type (any MOE_TYPE_*:
+ *          the same for both, or FP32 x with a 16-bit y), ldx, ldy (elements from one
+ *          row to the next of x, dx, dres and of y, dy; 0: H; at least H, at most 2^40),
+ *          eps (>= 0)
+ *   x      [rows][H]    g, b  float [H], nullable (1 and 0)
+ *   y      [rows][H] out, may be x itself where type and stride are the same
+ *   stats  float [rows][2] out, nullable: m and s, what the backward needs besides
+ *
+ * moe_layer_norm_bwd — its gradient:
+ *     t = dy g,  xh = (x - m) s,  dx = s (t - mean(t) - xh mean(t xh)) + dres
+ *     dg = sum over rows of dy xh,  db = sum over rows of dy
+ *   dres   [rows][H], nullable: what else arrives for x, of its type and stride
+ *   dx     [rows][H] out, may be x or dres itself, or dy of the same type and stride
+ *   dg, db float [H] out, both or neither NULL (g NULL or not); zeros for rows = 0
+ *   ws >= moe_layer_norm_workspace_bytes(n), 16-byte aligned (unused without dg: may be NULL)
+ * Rows may start anywhere: pointers, strides and H need only their elements' alignment
+ * (g, b, dg, db, stats: 4 bytes, stats 8).  Rows whose starts and lengths are multiples of
+ * 8 elements on 16-byte aligned pointers run fastest.  Other overlaps are not allowed; what
+ * lies between rows is neither read nor written.  A row's outputs depend on that row alone, and
+ * the column sums have a fixed order: repeated calls give bitwise the same.
+ * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for other types, H > 32768 or strides past 2^40.
+ */
+typedef struct moe_ln_desc {
+    int64_t rows, ldx, ldy;
+    int32_t H, x_type, y_type;
+    float eps;
+} moe_ln_desc;
+int64_t moe_layer_norm_workspace_bytes(const moe_ln_desc *n);
+int moe_layer_norm_fwd(const moe_ln_desc *n, const void *x, const float *g, const float *b, void *y, float *stats,
+                       void *stream);
+int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, const float *stats, const void *dy,
+                       const void *dres, void *dx, float *dg, float *db, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_grad_clip — the norm of many gradients together, and the gradients scaled to it:
+ *     norm = sqrt(sum of (scale g)^2) over all of them     (MOE_NORM_L2)
+ *          = the largest |scale g|                         (MOE_NORM_MAX)
+ *     coef = min(1, max_norm / (norm + eps)),   out = (scale coef) g, rounded once
+ *   t, n    host array of n (>= 0) tensors: g, out (g itself, or a buffer that overlaps no
+ *           gradient), numel (>= 0), type (MOE_TYPE_*; of both).  Element alignment is
+ *           enough; out of the alignment of g (modulo 16) runs fastest.  Read during the
+ *           call only, and not kept
+ *   scale   applied before the norm (1 / ranks, 1 / loss scale)
+ *   max_norm >= 0, eps >= 0
+ *   result  device: sum (of the squares of scale g, or their maximum, in 64 bits: what
+ *           ranks that hold shards add up), norm and coef; 8-byte aligned
+ *   ws >= moe_grad_workspace_bytes(n), 8-byte aligned
+ * Squares are summed in 64 bits, in an order that depends on the sizes only.  A NaN
+ * gradient makes norm and coef NaN, and all of out; an infinite one makes coef 0, and
+ * out 0 but NaN where the gradient is infinite.  The caller who wants such a step
+ * skipped reads result.  A norm past fp32's range is infinite there; sum, coef and out still hold.  Gradients that stay as they are (scale coef = 1, out = g) are not written.
+ *
+ * moe_grad_norm — result alone (out is not read).
+ * moe_grad_scale — out = (scale *coef) g with a coef (device float) of the caller's, for
+ * instance of a sum over ranks.
+ * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for 2^44 elements or more in all.
+ */
+enum {
+    MOE_NORM_L2 = 0,
+    MOE_NORM_MAX = 1,
+};
+typedef struct moe_grad {
+    const void *g;
+    void *out;
+    int64_t numel;
+    int32_t type, reserved; /* reserved: 0 */
+} moe_grad;
+typedef struct moe_grad_result {
+    double sum;
+    float norm, coef;
+} moe_grad_result;
+int64_t moe_grad_workspace_bytes(int32_t n);
+int moe_grad_norm(const moe_grad *t, int32_t n, int32_t kind, float scale, float max_norm, float eps,
+                  moe_grad_result *result, void *ws, size_t ws_bytes, void *stream);
+int moe_grad_clip(const moe_grad *t, int32_t n, int32_t kind, float scale, float max_norm, float eps,
+                  moe_grad_result *result, void *ws, size_t ws_bytes, void *stream);
+int moe_grad_scale(const moe_grad *t, int32_t n, const float *coef, float scale, void *stream);
+
+/*
  * Launch trace (optional, host side).  moe_trace_enable(n) records, for the
  * next n kernel launches made by this library on any stream, a start and stop
  * event on the launch's own stream; moe_trace_read copies the finished

@@ -4,9 +4,10 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SRC = os.path.join(HERE, "csrc", "moe.hip")
+SRCS = [os.path.join(HERE, "csrc", name) for name in ("moe.hip", "block.hip")]
 OUT = os.path.join(HERE, "libmoe.so")
 
 HIPCC_FLAGS = [
@@ -14,24 +15,34 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # packed fp32 instructions stay out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 
 
 def build(verbose: bool = False) -> str:
+    """Compiles the sources side by side and links them."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = OUT + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-o", tmp, SRC]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    err = "\n".join(l for l in res.stderr.splitlines() if "packed-fp32-ops" not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+    with tempfile.TemporaryDirectory() as tmpdir:
+        objs = [os.path.join(tmpdir, os.path.basename(s) + ".o") for s in SRCS]
+        procs = [subprocess.Popen([hipcc, *HIPCC_FLAGS, "-c", "-o", o, s], stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+                 for s, o in zip(SRCS, objs)]
+        for p in procs:
+            _finish(p, verbose)
+        tmp = OUT + ".tmp"
+        _finish(subprocess.Popen([hipcc, "--offload-arch=gfx950", "-shared", "-o", tmp, *objs], stdout=subprocess.PIPE,
+                                 stderr=subprocess.PIPE, text=True), verbose)
     os.replace(tmp, OUT)
     return OUT
+
+
+def _finish(p: subprocess.Popen, verbose: bool) -> None:
+    _, text = p.communicate()
+    err = "\n".join(l for l in text.splitlines() if "packed-fp32-ops" not in l)
+    if p.returncode != 0:
+        raise RuntimeError(f"hipcc failed ({p.returncode}):\n{err}")
+    if verbose and err.strip():
+        print(err, file=sys.stderr)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,613 @@
+// C-ABI entry points and kernels of a dense block's operators (gfx950): the gated
+// feed-forward block, layer norm, and the clipping of gradients.  Their arguments and
+// errors are documented in include/moe.h; the device code lives in dense.hpp, ffn.hpp,
+// lnorm.hpp and grads.hpp.
+#include <hip/hip_runtime.h>
+
+#include "common.hpp"
+#include "dense.hpp"
+#include "ffn.hpp"
+#include "grads.hpp"
+#include "host.hpp"
+#include "lnorm.hpp"
+
+using namespace moe;
+
+// ---------------------------------------------------------------------------
+// Kernels.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+extern __shared__ char block_lds[];
+__device__ __forceinline__ uint32_t block_lds_address() { return (uint32_t)(uintptr_t)(lds_char *)block_lds; }
+
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int NS, class Out>
+__global__ __launch_bounds__(kDenseThreads, 1) void k_dense(DenseArgs g, Out out) {
+    dense_body<T, MI, NI, AT, BT, GLU, NS>(g, out, block_lds_address(), blockIdx.x, gridDim.x);
+}
+
+// Both weight gradients in one launch.
+template <class T, int MI, int NI, int NS>
+__global__ __launch_bounds__(kDenseThreads, 1) void k_wgrads(DenseArgs g1, MatOut<T> o1, int blocks1, DenseArgs g2, MatOut<T> o2) {
+    const int b = blockIdx.x;
+    if (b < blocks1)
+        dense_body<T, MI, NI, true, true, false, NS>(g1, o1, block_lds_address(), b, blocks1);
+    else
+        dense_body<T, MI, NI, true, true, false, NS>(g2, o2, block_lds_address(), b - blocks1, gridDim.x - blocks1);
+}
+
+template <bool GLU, class Out>
+__global__ __launch_bounds__(256) void k_dense_join(DenseArgs g, Out out) {
+    dense_join_body<GLU>(g, out);
+}
+
+template <class TI, class TO, int CH, bool WAVE, bool ODD>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_fwd(LnArgs a, int lanes) {
+    ln_fwd_body<TI, TO, CH, WAVE, ODD>(a, lanes, reinterpret_cast<float *>(block_lds));
+}
+
+template <class TI, class TO, int CH, bool WAVE, bool ODD, bool SUMS>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_bwd(LnBwdArgs a, int lanes) {
+    ln_bwd_body<TI, TO, CH, WAVE, ODD, SUMS>(a, lanes, reinterpret_cast<float *>(block_lds));
+}
+
+template <class TI, class TO, bool ODD>
+__global__ __launch_bounds__(256) void k_ln_columns(LnBwdArgs a) {
+    __shared__ float lds[1024];
+    ln_columns_body<TI, TO, ODD>(a, lds);
+}
+
+template <int COLS>
+__global__ __launch_bounds__(1024) void k_ln_dg(const float *part, int parts, int H, float *dg, float *db) {
+    __shared__ float lds[1024];
+    norm_dg_body<COLS>(part, parts, H, dg, db, lds);
+}
+
+// The launch's tensors are read where the arguments lie: indexed at run time, a copy
+// would go through scratch memory.
+template <class L>
+__device__ __forceinline__ const __attribute__((address_space(4))) L &first_argument() {
+    return *(const __attribute__((address_space(4))) L *)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+__global__ __launch_bounds__(kGradThreads) void k_grad_sums(GradLaunch<kSumTensors, false>, GradScalars k) {
+    __shared__ double lds[kGradThreads / 64];
+    grad_sums_body(first_argument<GradLaunch<kSumTensors, false>>(), k, lds);
+}
+
+__global__ __launch_bounds__(kGradThreads) void k_grad_scale(GradLaunch<kScaleTensors, true>, GradScalars k) {
+    __shared__ double lds[kGradThreads / 64];
+    grad_scale_body(first_argument<GradLaunch<kScaleTensors, true>>(), k, lds);
+}
+
+__global__ __launch_bounds__(kGradThreads) void k_grad_result(GradScalars k) {
+    __shared__ double lds[kGradThreads / 64];
+    const moe_grad_result r = grad_result(k, lds);
+    if (threadIdx.x == 0) *k.result = r;
+}
+
+__global__ void k_zero_f32(float *p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) p[i] = 0.f;
+}
+
+int launch_zero(float *p, int64_t words, hipStream_t s) {
+    TraceScope tr("zero", s);
+    hipLaunchKernelGGL(k_zero_f32, dim3((int)std::min<int64_t>((words + 255) / 256, 2048)), dim3(256), 0, s, p, words);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Gated feed-forward block.
+// ---------------------------------------------------------------------------
+
+// A product's tile and its cut along K.
+enum DenseTile { kTileL = 0, kTileS = 1, kTileX = 2 };
+struct DensePlan {
+    DenseTile tile;
+    int mt, nt, splits, steps;
+    int blocks() const { return mt * nt * splits; }
+};
+
+int up_to(int64_t n, int d) { return (int)((n + d - 1) / d); }
+
+DensePlan dense_plan(int M, int N, int K, bool glu) {
+    static const int bm[] = {256, 128, 64}, bn[] = {256, 128, 128};
+    DensePlan p{};
+    const int steps = std::max(1, up_to(K, kDenseK));
+    for (int t = kTileL; t <= kTileX; ++t) {
+        p.tile = (DenseTile)t;
+        p.mt = up_to(M, bm[t]);
+        p.nt = up_to(N, glu ? bn[t] / 2 : bn[t]);
+        if ((int64_t)p.mt * p.nt >= 192) break;
+    }
+    p.splits = 1;
+    const int tiles = p.mt * p.nt;
+    if (tiles < 128) p.splits = std::max(1, std::min(std::min(steps / 4, 256 / tiles), 16));
+    p.steps = up_to(steps, p.splits);
+    p.splits = up_to(steps, p.steps);
+    return p;
+}
+int64_t dense_part_bytes(const DensePlan &p, int64_t M, int64_t N, bool glu) {
+    return p.splits > 1 ? align256(p.splits * M * N * (glu ? 2 : 1) * 4) : 0;
+}
+
+DenseArgs dense_args(const DensePlan &p, const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int M, int N, int K,
+                     void *part) {
+    return DenseArgs{A, B, lda, ldb, M, N, K, p.mt, p.nt, p.splits, p.steps, static_cast<float *>(part)};
+}
+
+constexpr int kStagesL = 2, kStagesS = 4, kStagesX = 4;
+size_t dense_lds(DenseTile t) {
+    return t == kTileL   ? kStagesL * dense_stage_bytes(4, 4)
+           : t == kTileS ? kStagesS * dense_stage_bytes(2, 2)
+                         : kStagesX * dense_stage_bytes(1, 2);
+}
+
+template <class T, bool AT, bool BT, bool GLU, class Out>
+int launch_dense(const DensePlan &p, const DenseArgs &g, const Out &out, hipStream_t s, const char *name) {
+    {
+        TraceScope tr(name, s);
+        auto *fn = p.tile == kTileL   ? k_dense<T, 4, 4, AT, BT, GLU, kStagesL, Out>
+                   : p.tile == kTileS ? k_dense<T, 2, 2, AT, BT, GLU, kStagesS, Out>
+                                      : k_dense<T, 1, 2, AT, BT, GLU, kStagesX, Out>;
+        hipLaunchKernelGGL(fn, dim3(p.blocks()), dim3(kDenseThreads), dense_lds(p.tile), s, g, out);
+    }
+    int rc = launch_status();
+    if (rc != MOE_OK || p.splits == 1) return rc;
+    TraceScope tr("dense_join", s);
+    auto *join = k_dense_join<GLU, Out>;
+    const int64_t n = (int64_t)g.M * (g.N / 8);
+    hipLaunchKernelGGL(join, dim3((int)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, s, g, out);
+    return launch_status();
+}
+
+int64_t ffn_ldx(const moe_ffn_desc *n) { return n->ldx ? n->ldx : n->H; }
+int64_t ffn_ldo(const moe_ffn_desc *n) { return n->ldo ? n->ldo : n->H; }
+
+int ffn_check(const moe_ffn_desc *n) {
+    if (!n || n->rows < 0 || n->H < 1 || n->I < 1 || n->act < MOE_ACT_SILU || n->act > MOE_ACT_RELU ||
+        (n->type != MOE_TYPE_BF16 && n->type != MOE_TYPE_FP16) || n->ldx < 0 || n->ldo < 0 || ffn_ldx(n) < n->H || ffn_ldo(n) < n->H)
+        return MOE_EINVAL;
+    // a tile's rows, and 64 rows of an MN-contiguous operand, are raw buffers below 2 GiB
+    constexpr int64_t kLd = 1 << 20;
+    if (n->H % 8 || n->I % 8 || n->H > 65536 || n->I > 65536 || n->ldx % 8 || n->ldo % 8 || ffn_ldx(n) > kLd || ffn_ldo(n) > kLd ||
+        (int64_t)n->H * n->I >= (1ll << 30) || n->rows >= (1ll << 30))
+        return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+struct FfnPlans {
+    DensePlan up, down;          // forward
+    DensePlan act, dx, dw1, dw2;  // backward
+};
+FfnPlans ffn_plans(const moe_ffn_desc *n) {
+    const int R = (int)n->rows, H = n->H, I = n->I;
+    FfnPlans p;
+    p.up = dense_plan(R, I, H, true);
+    p.down = dense_plan(R, H, I, false);
+    p.act = dense_plan(R, I, H, false);
+    p.dx = dense_plan(R, H, 2 * I, false);
+    p.dw1 = dense_plan(2 * I, H, R, false);
+    p.dw2 = dense_plan(H, I, R, false);
+    // the two weight gradients share a launch and its tile
+    if (p.dw1.tile != p.dw2.tile) {
+        DensePlan &o = p.dw1.tile < p.dw2.tile ? p.dw2 : p.dw1;
+        const bool first = &o == &p.dw1;
+        const DenseTile t = first ? p.dw2.tile : p.dw1.tile;
+        static const int bm[] = {256, 128, 64}, bn[] = {256, 128, 128};
+        o.tile = t;
+        o.mt = up_to(first ? 2 * I : H, bm[t]);
+        o.nt = up_to(first ? H : I, bn[t]);
+    }
+    return p;
+}
+
+// dHU, a (where it was not kept), then the parts of one product at a time (both weight
+// gradients': one after the other)
+int64_t ffn_bwd_base(const moe_ffn_desc *n) { return align256(n->rows * 4 * n->I) + align256(n->rows * 2 * n->I); }
+int64_t ffn_ws_bytes(const moe_ffn_desc *n, bool bwd) {
+    if (n->rows == 0) return 0;
+    const FfnPlans p = ffn_plans(n);
+    const int64_t R = n->rows, H = n->H, I = n->I;
+    if (!bwd) return std::max(dense_part_bytes(p.up, R, I, true), dense_part_bytes(p.down, R, H, false));
+    const int64_t dw = dense_part_bytes(p.dw1, 2 * I, H, false) + dense_part_bytes(p.dw2, H, I, false);
+    return ffn_bwd_base(n) + std::max(dw, std::max(dense_part_bytes(p.act, R, I, false), dense_part_bytes(p.dx, R, H, false)));
+}
+
+template <class T>
+int ffn_fwd(const moe_ffn_desc *n, const uint16_t *X, const uint16_t *W13, const uint16_t *W2, uint16_t *HU, uint16_t *A,
+            uint16_t *out, void *ws, hipStream_t s) {
+    const FfnPlans p = ffn_plans(n);
+    const int R = (int)n->rows, H = n->H, I = n->I;
+    const DenseArgs up = dense_args(p.up, X, ffn_ldx(n), W13, H, R, I, H, ws);
+    int rc = launch_dense<T, false, false, true>(p.up, up, GluOut<T>{HU, A, I, n->act}, s, "ffn_up");
+    if (rc != MOE_OK) return rc;
+    const DenseArgs down = dense_args(p.down, A, I, W2, I, R, H, I, ws);
+    return launch_dense<T, false, false, false>(p.down, down, MatOut<T>{out, ffn_ldo(n), 0, 0}, s, "ffn_down");
+}
+
+template <class T>
+int launch_wgrads(const FfnPlans &p, const DenseArgs &g1, const MatOut<T> &o1, const DenseArgs &g2, const MatOut<T> &o2, hipStream_t s) {
+    const int b1 = o1.p ? p.dw1.blocks() : 0, b2 = o2.p ? p.dw2.blocks() : 0;
+    const DenseTile t = p.dw1.tile;
+    {
+        TraceScope tr("ffn_wgrads", s);
+        auto *fn = t == kTileL   ? k_wgrads<T, 4, 4, kStagesL>
+                   : t == kTileS ? k_wgrads<T, 2, 2, kStagesS>
+                                 : k_wgrads<T, 1, 2, kStagesX>;
+        hipLaunchKernelGGL(fn, dim3(b1 + b2), dim3(kDenseThreads), dense_lds(t), s, g1, o1, b1, g2, o2);
+    }
+    auto join = [&](const DensePlan &q, const DenseArgs &g, const MatOut<T> &o) {
+        if (!o.p || q.splits == 1) return launch_status();
+        TraceScope tr("dense_join", s);
+        auto *fn = k_dense_join<false, MatOut<T>>;
+        const int64_t m = (int64_t)g.M * (g.N / 8);
+        hipLaunchKernelGGL(fn, dim3((int)std::min<int64_t>((m + 255) / 256, 2048)), dim3(256), 0, s, g, o);
+        return launch_status();
+    };
+    const int rc = join(p.dw1, g1, o1);
+    return rc != MOE_OK ? rc : join(p.dw2, g2, o2);
+}
+
+template <class T>
+int ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_t *X, const uint16_t *HU, const uint16_t *A, const uint16_t *W13,
+            const uint16_t *W2, uint16_t *dX, void *dW13, void *dW2, int f32, int add, void *ws, hipStream_t s) {
+    const FfnPlans p = ffn_plans(n);
+    const int R = (int)n->rows, H = n->H, I = n->I;
+    const int64_t ldx = ffn_ldx(n), ldo = ffn_ldo(n);
+    char *w = static_cast<char *>(ws);
+    uint16_t *dHU = reinterpret_cast<uint16_t *>(w), *a = reinterpret_cast<uint16_t *>(w + align256(n->rows * 4 * n->I));
+    char *part = w + ffn_bwd_base(n);
+    const DenseArgs act = dense_args(p.act, dOut, ldo, W2, I, R, I, H, part);
+    int rc = launch_dense<T, false, true, false>(p.act, act, GluBwdOut<T>{HU, dHU, A || !dW2 ? nullptr : a, I, n->act}, s, "ffn_bwd_act");
+    if (rc != MOE_OK) return rc;
+    if (dX) {
+        const DenseArgs dx = dense_args(p.dx, dHU, 2 * I, W13, H, R, H, 2 * I, part);
+        rc = launch_dense<T, false, true, false>(p.dx, dx, MatOut<T>{dX, ldx, 0, 0}, s, "ffn_bwd_dx");
+        if (rc != MOE_OK) return rc;
+    }
+    if (!dW13 && !dW2) return MOE_OK;
+    const DenseArgs dw1 = dense_args(p.dw1, dHU, 2 * I, X, ldx, 2 * I, H, R, part);
+    const DenseArgs dw2 = dense_args(p.dw2, dOut, ldo, A ? A : a, I, H, I, R, part + dense_part_bytes(p.dw1, 2 * I, H, false));
+    return launch_wgrads<T>(p, dw1, MatOut<T>{dW13, H, f32, add}, dw2, MatOut<T>{dW2, I, f32, add}, s);
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm.
+// ---------------------------------------------------------------------------
+
+int64_t ln_ldx(const moe_ln_desc *n) { return n->ldx ? n->ldx : n->H; }
+int64_t ln_ldy(const moe_ln_desc *n) { return n->ldy ? n->ldy : n->H; }
+constexpr int kLnWaveH = 2048, kLnMaxH = 32768, kLnSumH = 8192;
+
+int ln_check(const moe_ln_desc *n) {
+    if (!n || n->rows < 0 || n->H < 1 || n->ldx < 0 || n->ldy < 0 || ln_ldx(n) < n->H || ln_ldy(n) < n->H || !(n->eps >= 0.0f) ||
+        n->x_type < MOE_TYPE_BF16 || n->x_type > MOE_TYPE_FP32 || n->y_type < MOE_TYPE_BF16 || n->y_type > MOE_TYPE_FP32)
+        return MOE_EINVAL;
+    if (n->H > kLnMaxH || n->rows > (1ll << 40) || ln_ldx(n) > (1ll << 40) || ln_ldy(n) > (1ll << 40) ||
+        (n->x_type != n->y_type && n->x_type != MOE_TYPE_FP32))
+        return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+// How a row is shared out.
+struct LnPlan {
+    bool wave;
+    int chunks, lanes, threads, teams;  // 8-column chunks per thread, threads per row and per workgroup, rows per workgroup
+};
+LnPlan ln_plan(const moe_ln_desc *n) {
+    LnPlan p;
+    const int c = (n->H + 7) / 8;
+    p.wave = n->H <= kLnWaveH;
+    if (p.wave) {
+        p.chunks = n->H <= 512 ? 1 : n->H <= 1024 ? 2 : 4;
+        p.lanes = 8;
+        while (p.lanes * p.chunks < c) p.lanes *= 2;
+        p.threads = 256;
+        p.teams = p.threads / p.lanes;
+    } else {
+        p.chunks = n->H <= 8192 ? 1 : n->H <= 16384 ? 2 : 4;
+        p.lanes = p.threads = (c + 64 * p.chunks - 1) / (64 * p.chunks) * 64;
+        p.teams = 1;
+    }
+    return p;
+}
+
+// Workgroups of the backward: each leaves one row of column sums.
+int ln_groups(const moe_ln_desc *n) {
+    const LnPlan p = ln_plan(n);
+    if (p.wave) return (int)std::max<int64_t>(1, std::min<int64_t>((n->rows + 4 * p.teams - 1) / (4 * p.teams), 1024));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n->rows, p.threads <= 512 ? 512 : 256));
+}
+// rows of sums of the long rows' second reading
+int ln_column_groups(const moe_ln_desc *n) { return (int)std::max<int64_t>(1, std::min<int64_t>((n->rows + 15) / 16, 64)); }
+int ln_parts(const moe_ln_desc *n) { return n->H <= kLnSumH ? ln_groups(n) : ln_column_groups(n); }
+int64_t ln_ws_bytes(const moe_ln_desc *n) { return n->rows ? align256((int64_t)ln_parts(n) * 2 * n->H * 4) : 0; }
+
+// Whether every row of p starts on 16 bytes and ends on a whole chunk.
+bool ln_even(const moe_ln_desc *n, const void *p, int64_t ld) { return !p || (n->H % 8 == 0 && ld % 8 == 0 && aligned16(p)); }
+bool ln_aligned(const void *p, int type) { return ((uintptr_t)p & (type == MOE_TYPE_FP32 ? 3u : 1u)) == 0; }
+
+template <class TI, class TO, bool ODD>
+auto *ln_fwd_kernel(const LnPlan &p) {
+    if (p.wave)
+        return p.chunks == 1   ? k_ln_fwd<TI, TO, 1, true, ODD>
+               : p.chunks == 2 ? k_ln_fwd<TI, TO, 2, true, ODD>
+                               : k_ln_fwd<TI, TO, 4, true, ODD>;
+    return p.chunks == 1   ? k_ln_fwd<TI, TO, 1, false, ODD>
+           : p.chunks == 2 ? k_ln_fwd<TI, TO, 2, false, ODD>
+                           : k_ln_fwd<TI, TO, 4, false, ODD>;
+}
+template <class TI, class TO, bool ODD>
+auto *ln_bwd_kernel(const LnPlan &p) {
+    if (p.wave)
+        return p.chunks == 1   ? k_ln_bwd<TI, TO, 1, true, ODD, true>
+               : p.chunks == 2 ? k_ln_bwd<TI, TO, 2, true, ODD, true>
+                               : k_ln_bwd<TI, TO, 4, true, ODD, true>;
+    return p.chunks == 1   ? k_ln_bwd<TI, TO, 1, false, ODD, true>
+           : p.chunks == 2 ? k_ln_bwd<TI, TO, 2, false, ODD, false>
+                           : k_ln_bwd<TI, TO, 4, false, ODD, false>;
+}
+
+// f of the types and whether the rows are odd
+template <class F>
+int ln_typed(const moe_ln_desc *n, bool odd, F &&f) {
+    auto with = [&](auto ti, auto to) { return odd ? f(ti, to, std::true_type{}) : f(ti, to, std::false_type{}); };
+    if (n->x_type == MOE_TYPE_BF16) return with(Bf16{}, Bf16{});
+    if (n->x_type == MOE_TYPE_FP16) return with(Fp16{}, Fp16{});
+    if (n->y_type == MOE_TYPE_BF16) return with(F32{}, Bf16{});
+    if (n->y_type == MOE_TYPE_FP16) return with(F32{}, Fp16{});
+    return with(F32{}, F32{});
+}
+
+// ---------------------------------------------------------------------------
+// Gradients.
+// ---------------------------------------------------------------------------
+
+int64_t grad_pieces_of(int64_t n) { return (n + kGradPiece - 1) / kGradPiece; }
+
+int grad_check(const moe_grad *t, int32_t n, bool out) {
+    if (n < 0 || (n > 0 && !t)) return MOE_EINVAL;
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) {
+        const moe_grad &k = t[i];
+        if (k.numel < 0 || k.type < MOE_TYPE_BF16 || k.type > MOE_TYPE_FP32 || k.reserved) return MOE_EINVAL;
+        if (k.numel >= (1ll << 44)) return MOE_EUNSUPPORTED;
+        if (k.numel == 0) continue;
+        if (!k.g || !ln_aligned(k.g, k.type) || (out && (!k.out || !ln_aligned(k.out, k.type)))) return MOE_EINVAL;
+        all += k.numel;
+        if (all >= (1ll << 44)) return MOE_EUNSUPPORTED;
+    }
+    return MOE_OK;
+}
+bool grad_scalars_ok(int32_t kind, float scale, float max_norm, float eps) {
+    return (kind == MOE_NORM_L2 || kind == MOE_NORM_MAX) && scale == scale && max_norm >= 0.f && eps >= 0.f;
+}
+
+// Tensors [*at, ...) that a launch takes, as many as fit; false when none is left.
+template <int N, bool OUT>
+bool grad_fill(GradLaunch<N, OUT> &l, const moe_grad *t, int32_t n, int32_t *at) {
+    l.count = 0;
+    int64_t pieces = 0;
+    while (*at < n && l.count < N) {
+        const moe_grad &k = t[*at];
+        if (k.numel) {
+            const int64_t p = grad_pieces_of(k.numel);
+            l.t[l.count] = GradTensor{k.g, k.numel << 2 | k.type};
+            if constexpr (OUT) l.out[l.count] = k.out;
+            l.piece[l.count++] = (int32_t)pieces;
+            pieces += p;
+        }
+        ++*at;
+    }
+    l.piece[l.count] = (int32_t)pieces;
+    return l.count > 0;
+}
+
+int grad_launches(int32_t n) { return (n + kSumTensors - 1) / kSumTensors; }
+int64_t grad_ws_bytes(int32_t n) { return 8 * (int64_t)(kGradParts + grad_launches(n)); }
+
+int launch_grad_sums(const moe_grad *t, int32_t n, GradScalars &k, hipStream_t s) {
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) all += grad_pieces_of(t[i].numel);
+    double *parts = k.parts;
+    GradLaunch<kSumTensors, false> l;
+    for (int32_t at = 0; grad_fill(l, t, n, &at);) {
+        // its share of the slots, one at least
+        const int64_t pieces = l.piece[l.count], share = std::max<int64_t>(1, pieces * kGradParts / std::max(all, pieces));
+        const int grid = (int)std::min(pieces, share);
+        GradScalars a = k;
+        a.parts = parts;
+        {
+            TraceScope tr("grad_sums", s);
+            hipLaunchKernelGGL(k_grad_sums, dim3(grid), dim3(kGradThreads), 0, s, l, a);
+        }
+        if (launch_status() != MOE_OK) return MOE_EHIP;
+        parts += grid;
+    }
+    k.nparts = (int32_t)(parts - k.parts);
+    return MOE_OK;
+}
+
+int launch_grad_result(const GradScalars &k, hipStream_t s) {
+    TraceScope tr("grad_result", s);
+    hipLaunchKernelGGL(k_grad_result, dim3(1), dim3(kGradThreads), 0, s, k);
+    return launch_status();
+}
+
+int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s, bool *any) {
+    GradLaunch<kScaleTensors, true> l;
+    *any = false;
+    // from the last tensors to the first, as within a launch: the cache holds what was read last
+    for (int32_t end = n; end > 0;) {
+        int32_t begin = end, taken = 0;
+        while (begin > 0 && taken < kScaleTensors) taken += t[--begin].numel > 0;
+        int32_t at = begin;
+        if (grad_fill(l, t, end, &at)) {
+            const int grid = (int)std::min<int64_t>(l.piece[l.count], 8 * device_cus());
+            TraceScope tr("grad_scale", s);
+            hipLaunchKernelGGL(k_grad_scale, dim3(grid), dim3(kGradThreads), 0, s, l, k);
+            if (launch_status() != MOE_OK) return MOE_EHIP;
+            *any = true;
+        }
+        end = begin;
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_gated_ffn_workspace_bytes(const moe_ffn_desc *n, int32_t bwd) {
+    return ffn_check(n) == MOE_OK && (bwd == 0 || bwd == 1) ? ffn_ws_bytes(n, bwd) : -1;
+}
+
+int moe_gated_ffn_fwd(const moe_ffn_desc *n, const uint16_t *X, const uint16_t *W13, const uint16_t *W2, uint16_t *HU, uint16_t *A,
+                      uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = ffn_check(n);
+    if (rc != MOE_OK) return rc;
+    if (n->rows == 0) return MOE_OK;
+    if (!X || !W13 || !W2 || !A || !out || !all_aligned({X, W13, W2, HU, A, out, ws})) return MOE_EINVAL;
+    const int64_t need = ffn_ws_bytes(n, false);
+    if (need && !ws) return MOE_EINVAL;
+    if ((int64_t)ws_bytes < need) return MOE_ENOSPC;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return n->type == MOE_TYPE_BF16 ? ffn_fwd<Bf16>(n, X, W13, W2, HU, A, out, ws, s) : ffn_fwd<Fp16>(n, X, W13, W2, HU, A, out, ws, s);
+}
+
+int moe_gated_ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_t *X, const uint16_t *HU, const uint16_t *A,
+                      const uint16_t *W13, const uint16_t *W2, uint16_t *dX, void *dW13, void *dW2, int32_t dw_type, int32_t accumulate,
+                      void *ws, size_t ws_bytes, void *stream) {
+    const int rc = ffn_check(n);
+    if (rc != MOE_OK) return rc;
+    if ((dw_type != MOE_TYPE_FP32 && dw_type != n->type) || (accumulate != 0 && accumulate != 1)) return MOE_EINVAL;
+    if (accumulate && dw_type != MOE_TYPE_FP32) return MOE_EUNSUPPORTED;
+    if (!all_aligned({dW13, dW2})) return MOE_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n->rows == 0) {
+        if (accumulate) return MOE_OK;
+        const int64_t words = (int64_t)n->H * n->I / (dw_type == MOE_TYPE_FP32 ? 1 : 2);
+        int r = dW13 ? launch_zero(static_cast<float *>(dW13), 2 * words, s) : MOE_OK;
+        if (r == MOE_OK && dW2) r = launch_zero(static_cast<float *>(dW2), words, s);
+        return r;
+    }
+    if (!dOut || !X || !HU || !W13 || !W2 || !ws || !all_aligned({dOut, X, HU, A, W13, W2, dX, ws})) return MOE_EINVAL;
+    if (!dX && !dW13 && !dW2) return MOE_EINVAL;
+    if ((int64_t)ws_bytes < ffn_ws_bytes(n, true)) return MOE_ENOSPC;
+    const int f32 = dw_type == MOE_TYPE_FP32;
+    return n->type == MOE_TYPE_BF16 ? ffn_bwd<Bf16>(n, dOut, X, HU, A, W13, W2, dX, dW13, dW2, f32, accumulate, ws, s)
+                                    : ffn_bwd<Fp16>(n, dOut, X, HU, A, W13, W2, dX, dW13, dW2, f32, accumulate, ws, s);
+}
+
+int64_t moe_layer_norm_workspace_bytes(const moe_ln_desc *n) { return ln_check(n) == MOE_OK ? ln_ws_bytes(n) : -1; }
+
+int moe_layer_norm_fwd(const moe_ln_desc *n, const void *x, const float *g, const float *b, void *y, float *stats, void *stream) {
+    const int rc = ln_check(n);
+    if (rc != MOE_OK) return rc;
+    if (n->rows == 0) return MOE_OK;
+    if (!x || !y || !ln_aligned(x, n->x_type) || !ln_aligned(y, n->y_type) || !aligned4(g) || !aligned4(b) || ((uintptr_t)stats & 7u))
+        return MOE_EINVAL;
+    const LnPlan p = ln_plan(n);
+    const LnArgs a{x, g, b, y, stats, n->rows, ln_ldx(n), ln_ldy(n), n->H, n->eps};
+    const bool odd = !ln_even(n, x, a.ldx) || !ln_even(n, y, a.ldy);
+    const int64_t per_cu = p.wave ? 8 : std::max(1, 1024 / p.threads);
+    const int grid = (int)std::min<int64_t>((n->rows + p.teams - 1) / p.teams, per_cu * device_cus());
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return ln_typed(n, odd, [&](auto ti, auto to, auto is_odd) {
+        TraceScope tr("layer_norm_fwd", s);
+        auto *fn = ln_fwd_kernel<decltype(ti), decltype(to), decltype(is_odd)::value>(p);
+        hipLaunchKernelGGL(fn, dim3(grid), dim3(p.threads), p.wave ? 0 : 384, s, a, p.lanes);
+        return launch_status();
+    });
+}
+
+int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, const float *stats, const void *dy, const void *dres,
+                       void *dx, float *dg, float *db, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = ln_check(n);
+    if (rc != MOE_OK) return rc;
+    if (!dg != !db || !aligned4(dg) || !aligned4(db)) return MOE_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n->rows > 0) {
+        if (!x || !stats || !dy || !dx || !ln_aligned(x, n->x_type) || !ln_aligned(dy, n->y_type) || !ln_aligned(dres, n->x_type) ||
+            !ln_aligned(dx, n->x_type) || !aligned4(g) || ((uintptr_t)stats & 7u) || !aligned16(ws))
+            return MOE_EINVAL;
+        if (dg && !ws) return MOE_EINVAL;
+        if (dg && (int64_t)ws_bytes < ln_ws_bytes(n)) return MOE_ENOSPC;
+        const LnPlan p = ln_plan(n);
+        const bool long_rows = n->H > kLnSumH;
+        LnBwdArgs a{LnArgs{x, g, nullptr, nullptr, const_cast<float *>(stats), n->rows, ln_ldx(n), ln_ldy(n), n->H, n->eps}, dy, dres, dx,
+                    dg ? static_cast<float *>(ws) : nullptr};
+        const bool odd = !ln_even(n, x, a.f.ldx) || !ln_even(n, dy, a.f.ldy) || !ln_even(n, dres, a.f.ldx) || !ln_even(n, dx, a.f.ldx);
+        const int grid = ln_groups(n);
+        const size_t lds = 256 + (p.wave ? 64 * (size_t)p.chunks * p.lanes : 0);
+        int r = ln_typed(n, odd, [&](auto ti, auto to, auto is_odd) {
+            using TI = decltype(ti);
+            using TO = decltype(to);
+            constexpr bool ODD = decltype(is_odd)::value;
+            if (long_rows && dg) {  // before dx, which may take the place of an input
+                TraceScope tr("layer_norm_columns", s);
+                auto *fn = k_ln_columns<TI, TO, ODD>;
+                hipLaunchKernelGGL(fn, dim3((n->H + 511) / 512, ln_column_groups(n)), dim3(256), 0, s, a);
+                if (launch_status() != MOE_OK) return (int)MOE_EHIP;
+            }
+            TraceScope tr("layer_norm_bwd", s);
+            auto *fn = ln_bwd_kernel<TI, TO, ODD>(p);
+            hipLaunchKernelGGL(fn, dim3(grid), dim3(p.threads), lds, s, a, p.lanes);
+            return launch_status();
+        });
+        if (r != MOE_OK) return r;
+    }
+    if (!dg) return MOE_OK;
+    TraceScope tr("layer_norm_dg", s);
+    const int parts = n->rows ? ln_parts(n) : 0;
+    auto *fn = n->H < 2048 ? k_ln_dg<16> : k_ln_dg<64>;
+    const int cols = n->H < 2048 ? 16 : 64;
+    hipLaunchKernelGGL(fn, dim3((n->H + cols - 1) / cols, 2), dim3(1024), 0, s, static_cast<const float *>(ws), parts, n->H, dg, db);
+    return launch_status();
+}
+
+int64_t moe_grad_workspace_bytes(int32_t n) { return n >= 0 ? grad_ws_bytes(n) : -1; }
+
+static int grad_norm_check(const moe_grad *t, int32_t n, int32_t kind, float scale, float max_norm, float eps, const void *result,
+                           const void *ws, size_t ws_bytes, bool out) {
+    const int rc = grad_check(t, n, out);
+    if (rc != MOE_OK) return rc;
+    if (!grad_scalars_ok(kind, scale, max_norm, eps) || !result || ((uintptr_t)result & 7u) || !ws || ((uintptr_t)ws & 7u)) return MOE_EINVAL;
+    return (int64_t)ws_bytes < grad_ws_bytes(n) ? MOE_ENOSPC : MOE_OK;
+}
+
+int moe_grad_norm(const moe_grad *t, int32_t n, int32_t kind, float scale, float max_norm, float eps, moe_grad_result *result, void *ws,
+                  size_t ws_bytes, void *stream) {
+    int rc = grad_norm_check(t, n, kind, scale, max_norm, eps, result, ws, ws_bytes, false);
+    if (rc != MOE_OK) return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    GradScalars k{static_cast<double *>(ws), result, nullptr, 0, kind, scale, max_norm, eps};
+    rc = launch_grad_sums(t, n, k, s);
+    return rc != MOE_OK ? rc : launch_grad_result(k, s);
+}
+
+int moe_grad_clip(const moe_grad *t, int32_t n, int32_t kind, float scale, float max_norm, float eps, moe_grad_result *result, void *ws,
+                  size_t ws_bytes, void *stream) {
+    int rc = grad_norm_check(t, n, kind, scale, max_norm, eps, result, ws, ws_bytes, true);
+    if (rc != MOE_OK) return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    GradScalars k{static_cast<double *>(ws), result, nullptr, 0, kind, scale, max_norm, eps};
+    rc = launch_grad_sums(t, n, k, s);
+    if (rc != MOE_OK) return rc;
+    bool any;
+    rc = launch_grad_scale(t, n, k, s, &any);
+    return rc != MOE_OK || any ? rc : launch_grad_result(k, s);
+}
+
+int moe_grad_scale(const moe_grad *t, int32_t n, const float *coef, float scale, void *stream) {
+    const int rc = grad_check(t, n, true);
+    if (rc != MOE_OK) return rc;
+    if (!coef || !aligned4(coef) || scale != scale) return MOE_EINVAL;
+    GradScalars k{nullptr, nullptr, coef, 0, MOE_NORM_L2, scale, 0.f, 0.f};
+    bool any;
+    return launch_grad_scale(t, n, k, static_cast<hipStream_t>(stream), &any);
+}
+
+}  // extern "C"

@@ -1,0 +1,361 @@
+// Dense 16-bit matrix products (bf16 or fp16 operands, fp32 accumulators) of any
+// number of rows and columns: the products of the gated feed-forward block and of
+// its gradient.
+//
+//   D[m][n] = sum_k A(m, k) B(n, k)
+//
+// Each operand lies either K-contiguous ([mn][k]) or MN-contiguous ([k][mn]), so no
+// transposed copy is made for the gradient.  A workgroup of 4 waves (2 x 2) makes a
+// tile of 64 MI x 64 NI outputs, each wave 32 MI x 32 NI of it in blocks of
+// v_mfma_f32_32x32x16.  K steps of 64 go from memory to LDS by buffer loads with the
+// lds bit, into a ring of NS stages.
+//
+// Edges cost the loop nothing.  Rows past the last one lie past the end of the raw
+// buffer, which reads as zeros there; columns (of an MN-contiguous operand) and the
+// k of the last step past K get an address past it.
+//
+// One wave per SIMD does not hide its own waits, so the loop does: the fragments of a
+// 16-deep sub-step are read from LDS while the one before is multiplied, across the
+// step's barrier too.  A step's barrier stands before its last sub-step, whose
+// fragments are in registers by then: its MFMAs run while the next stage's first
+// fragments are read and the stage just read is filled anew, which then has a whole
+// step's time to land.
+//
+// The loads are written as asm without outputs: known to the compiler as loads into
+// LDS, each transposing LDS read would wait for all of them.  They are waited for by
+// count (vector memory operations complete in order) before the barrier that
+// publishes their stage; the compiler's own waits only become longer by them.
+#pragma once
+
+#include "buffer.hpp"
+#include "common.hpp"
+
+namespace moe {
+
+struct Bf16 {
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+#else
+        return c;
+#endif
+    }
+    static __device__ __forceinline__ uint16_t down(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+    static __device__ __forceinline__ float up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+};
+struct Fp16 {
+    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+#else
+        return c;
+#endif
+    }
+    static __device__ __forceinline__ uint16_t down(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+    static __device__ __forceinline__ float up(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+};
+
+struct F32 {};  // fp32 elements, where a call takes them too
+
+template <class T>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (uint32_t)T::down(v[2 * i]) | (uint32_t)T::down(v[2 * i + 1]) << 16;
+    return o;
+}
+template <class T>
+__device__ __forceinline__ void unpack8(const u32x4 &p, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = T::up((uint16_t)p[i]), v[2 * i + 1] = T::up((uint16_t)(p[i] >> 16));
+}
+
+constexpr int kDenseThreads = 256;
+constexpr int kDenseK = 64;          // k per step
+constexpr uint32_t kPastEnd = 0x80000000u;  // a lane offset past every buffer's end
+
+// 16 bytes per lane from a raw buffer to 1 KiB of LDS at byte address `lds`.  The whole
+// offset is the lane's: the range check subtracts a wave-uniform one from the size,
+// which must not go below zero.
+__device__ __forceinline__ void dense_dma(u32x4 rsrc, uint32_t lds, uint32_t lane_off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(lane_off), "s"(rsrc));
+#else
+    (void)rsrc, (void)lds, (void)lane_off;
+#endif
+}
+__device__ __forceinline__ u32x4 dense_rsrc(const void *base, uint32_t bytes) {
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+// A K-contiguous operand's rows [0, valid) of a tile of R rows, row i at base + i ld.
+// LDS: [R][64], rows of 128 bytes, two of them to a window of 256 bytes whose 16
+// chunks of 16 bytes are permuted by XOR with the window's number: the 16 lanes of a
+// ds_read_b128's phase, 16 rows at one k, then hit 16 different chunks of the window.
+template <int R>
+struct LoadK {
+    static constexpr int BL = R / 8 / 4;  // 1 KiB blocks (8 rows) per wave and step
+    static constexpr int P = BL < 4 ? BL : 4;
+    const char *base;
+    uint32_t bytes, block, first;  // bytes: of the valid rows; block: of 8 rows; first: this wave's first block's offset
+    uint32_t off[P], kc[P];
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int valid, int wave, int lane, int row_blocks_before = 0) {
+        base = reinterpret_cast<const char *>(p);
+        block = (uint32_t)(16 * ld);
+        first = (uint32_t)(wave * BL - row_blocks_before) * block;
+        bytes = (uint32_t)(2 * ld) * (uint32_t)valid;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int span = ((wave * BL + i) & 3) * 4 + (lane >> 4), slot = (lane & 15) ^ (span & 15);
+            kc[i] = (uint32_t)(slot & 7) * 8;
+            off[i] = (uint32_t)((lane >> 4) * 2 + (slot >> 3)) * (uint32_t)(2 * ld) + kc[i] * 2;
+        }
+    }
+    // the last step: k from `left` on read zeros
+    __device__ __forceinline__ void cut(int left) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if ((int)kc[i] >= left) off[i] = kPastEnd;
+    }
+    __device__ __forceinline__ u32x4 stage(int64_t step, bool in) const { return dense_rsrc(base, in ? bytes : 0u); }
+    __device__ __forceinline__ uint32_t step_off(int64_t step) const { return (uint32_t)(step * (kDenseK * 2)) + first; }
+    __device__ __forceinline__ void load(const u32x4 &rsrc, uint32_t so, uint32_t lds, int wave, int i) const {
+        dense_dma(rsrc, lds + (wave * BL + i) * 1024, off[i % P] + (so + i * block));
+    }
+};
+
+// An MN-contiguous operand's columns [0, valid) of a tile of R columns, k row r at
+// base + r ld.  LDS: [64][R], chunks of 16 bytes permuted so that the four k rows
+// that 16 lanes of a transposing read take lie in four different quarters of a
+// 256-byte window.
+template <int R>
+struct LoadMn {
+    static constexpr int BL = R / 8 / 4, CPR = R / 8, RPB = 64 / CPR;  // blocks per wave; chunks per k row; k rows per block
+    static constexpr int P = RPB < 4 ? 4 / RPB : 1;
+    static_assert(BL % P == 0, "a wave's blocks start on a multiple of four k rows");
+    const char *base;
+    int64_t row;  // bytes
+    int K;
+    uint32_t off[P];
+    static __device__ __forceinline__ int swz(int r) { return R == 64 ? 4 * ((r >> 1) & 1) : 4 * (r & 3); }
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int valid, int K_, int lane) {
+        base = reinterpret_cast<const char *>(p);
+        row = 2 * ld;
+        K = K_;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int r = i * RPB + lane / CPR, c = (lane % CPR) ^ swz(r);
+            off[i] = c * 8 < valid ? (uint32_t)(lane / CPR) * (uint32_t)row + c * 16 : kPastEnd;
+        }
+    }
+    __device__ __forceinline__ void cut(int) {}
+    __device__ __forceinline__ u32x4 stage(int64_t step, bool in) const {
+        const int64_t left = K - step * kDenseK;
+        return dense_rsrc(base + step * kDenseK * row, in ? (uint32_t)(left < kDenseK ? left : kDenseK) * (uint32_t)row : 0u);
+    }
+    __device__ __forceinline__ uint32_t step_off(int64_t) const { return 0; }
+    __device__ __forceinline__ void load(const u32x4 &rsrc, uint32_t, uint32_t lds, int wave, int i) const {
+        dense_dma(rsrc, lds + (wave * BL + i) * 1024, off[i % P] + (uint32_t)((wave * BL + i) * RPB) * (uint32_t)row);
+    }
+};
+
+// Fragments: lane l of a block of 32 rows holds row l % 32, k 8 (l / 32) ... + 7 of the
+// sub-step's 16.
+template <class T, bool TR, int R>
+struct Frags {
+    typedef typename T::v8 v8;
+    uint32_t at;  // K-contiguous: chunk of sub-step 0 in block 0; MN-contiguous: k row and columns of block 0
+    __device__ __forceinline__ void init(int lane) {
+        if constexpr (!TR) {
+            const int row = lane & 31, span = row >> 1, slot = ((row & 1) * 8 | (lane >> 5)) ^ (span & 15);
+            at = span * 256 + slot * 16;
+        } else {
+            const int g = (lane >> 4) & 1, q = lane & 15, j = q >> 2, cq = q & 3;
+            at = (8 * (lane >> 5) + j) * (2 * R) + (((2 * g + (cq >> 1)) ^ LoadMn<R>::swz(j)) << 4) + (cq & 1) * 8;
+        }
+    }
+    // block b (a wave's own first block included), sub-step s, of the tile at LDS address `tile`
+    __device__ __forceinline__ v8 get(uint32_t tile, int b, int s) const {
+        if constexpr (!TR) {
+            return *(const __attribute__((address_space(3))) v8 *)(uintptr_t)(tile + b * 4096 + (at ^ (s << 5)));
+        } else {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            struct Two {
+                s16x4 lo, hi;
+            };
+            Two t{};
+#if defined(__HIP_DEVICE_COMPILE__)
+            const uint32_t p = tile + 16 * s * (2 * R) + (at ^ ((uint32_t)b << 6));
+            t.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)p);
+            t.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(p + 4 * (2 * R)));
+#endif
+            return __builtin_bit_cast(v8, t);
+        }
+    }
+};
+
+template <int MI, int NI>
+using DenseAcc = f32x16[MI][NI];
+
+template <bool TR, int R>
+struct LoadOf {
+    using type = LoadK<R>;
+};
+template <int R>
+struct LoadOf<true, R> {
+    using type = LoadMn<R>;
+};
+
+constexpr int dense_stage_bytes(int MI, int NI) { return (MI + NI) * 64 * kDenseK * 2; }
+
+template <int N>
+__device__ __forceinline__ void wait_loads_and_meet() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The K loop over steps [k0, k1) (of the tile's K; `left`: k in the step k_last, the
+// operand's last).  GLU: B's blocks are dealt to the waves so that a wave has NI / 2
+// blocks of the tile's first half and the same of its second.  On return every load
+// has landed and the workgroup has met.
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int NS, class LA, class LB>
+__device__ __forceinline__ void dense_loop(LA &la, LB &lb, int k0, int k1, int k_last, int left, uint32_t lds, int wave, int lane,
+                                           DenseAcc<MI, NI> &acc) {
+    constexpr int A_BYTES = MI * 64 * kDenseK * 2, STAGE = dense_stage_bytes(MI, NI), ND = LA::BL + LB::BL;
+    constexpr int NQ = MI * NI, RPQ = (MI + NI + NQ - 1) / NQ;  // MFMAs per sub-step; fragment reads beside each of the first
+    typedef typename T::v8 v8;
+    const int wm = wave >> 1, wn = wave & 1;
+    Frags<T, AT, 64 * MI> fa;
+    Frags<T, BT, 64 * NI> fb;
+    fa.init(lane);
+    fb.init(lane);
+    auto bblock = [&](int ni) { return GLU ? (ni < NI / 2 ? wn * (NI / 2) + ni : NI + wn * (NI / 2) + ni - NI / 2) : wn * NI + ni; };
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[mi][ni][e] = 0.f;
+    u32x4 ra, rb;
+    uint32_t sa, sb;
+    auto open = [&](int step) {  // the buffers of a step; one past the range is empty
+        if (step == k_last && left < kDenseK) la.cut(left), lb.cut(left);
+        const bool in = step < k1;
+        ra = la.stage(step, in), rb = lb.stage(step, in);
+        sa = la.step_off(step), sb = lb.step_off(step);
+    };
+    auto load = [&](uint32_t stage, int i) {
+        if (i < LA::BL)
+            la.load(ra, sa, stage, wave, i);
+        else
+            lb.load(rb, sb, stage + A_BYTES, wave, i - LA::BL);
+    };
+#pragma unroll 1
+    for (int j = 0; j < NS; ++j) {
+        open(k0 + j);
+#pragma unroll
+        for (int i = 0; i < ND; ++i) load(lds + j * STAGE, i);
+    }
+    wait_loads_and_meet<(NS - 1) * ND>();
+    v8 a[2][MI], b[2][NI];
+    auto read = [&](int to, uint32_t stage, int s, int i) {  // i: 0 .. MI + NI - 1
+        if (i < MI)
+            a[to][i] = fa.get(stage, wm * MI + i, s);
+        else
+            b[to][i - MI] = fb.get(stage + A_BYTES, bblock(i - MI), s);
+    };
+#pragma unroll
+    for (int i = 0; i < MI + NI; ++i) read(0, lds, 0, i);
+    uint32_t slot = 0;
+#pragma unroll 1
+    for (int kt = k0; kt < k1; ++kt) {
+        const uint32_t stage = lds + slot * STAGE;
+        slot = slot + 1 == NS ? 0 : slot + 1;
+        const uint32_t next = lds + slot * STAGE;
+        open(kt + NS);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int cur = s & 1;
+            if (s == 3) wait_loads_and_meet<(NS - 2) * ND>();
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                // what this sub-step issues beside its MFMAs, spread over them
+#pragma unroll
+                for (int i = q * RPQ; i < (q + 1) * RPQ && i < MI + NI; ++i) read(cur ^ 1, s == 3 ? next : stage, s == 3 ? 0 : s + 1, i);
+                if (s == 3) {
+#pragma unroll
+                    for (int i = q * ND / NQ; i < (q + 1) * ND / NQ; ++i) load(stage, i);
+                }
+                // operands swapped: a lane then holds four consecutive columns of one row
+                acc[q / NI][q % NI] = T::mfma(b[cur][q % NI], a[cur][q / NI], acc[q / NI][q % NI]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    wait_loads_and_meet<0>();
+}
+
+// The tile's values, 8 consecutive columns of a row at a time, through LDS that the
+// wave has to itself (its own 32 rows x 32 NI columns of fp32): lane l of a block
+// holds row l % 32, columns 8 q + 4 (l / 32) + 0..3 in elements 4 q ...  The chunks of
+// a row are permuted by XOR with the row, so that 16 rows' writes of one column hit
+// different chunks.  For each row and its 8 columns, of the tile: pre(row, column) loads
+// what the output needs besides, some rows ahead; f(row, column, that, v) or, GLU,
+// f(row, column, that, h, u).
+template <int MI, int NI, bool GLU, class P, class F>
+__device__ __forceinline__ void dense_rows(const DenseAcc<MI, NI> &acc, uint32_t lds, int wave, int lane, P &&pre, F &&f) {
+    constexpr int ROW = NI * 128, MASK = NI * 8 < 16 ? NI * 8 - 1 : 15;
+    constexpr int LPR = GLU ? NI * 2 : NI * 4, RPP = 64 / LPR, PASSES = 32 / RPP;  // lanes per row, rows per pass
+    constexpr int AHEAD = PASSES < 4 ? PASSES : 4;
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    const uint32_t st = lds + wave * 32 * ROW;
+    const int wm = wave >> 1, wn = wave & 1, r = lane & 31, hi = lane >> 5;
+    const int c8 = lane % LPR, col = wn * (GLU ? NI * 16 : NI * 32) + c8 * 8;
+    auto get = [&](int row, int c, float (&v)[8]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const f32x4 x = *(const lds_f32x4 *)(uintptr_t)(st + row * ROW + (((2 * c + k) ^ (row & MASK)) << 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * k + e] = x[e];
+        }
+    };
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x16 &c = acc[mi][ni];
+                *(lds_f32x4 *)(uintptr_t)(st + r * ROW + (((ni * 8 + 2 * q + hi) ^ (r & MASK)) << 4)) =
+                    f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+            }
+        const int row0 = wm * MI * 32 + mi * 32;
+#pragma unroll 1
+        for (int p0 = 0; p0 < PASSES; p0 += AHEAD) {
+            decltype(pre(0, 0)) ahead[AHEAD];
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p) ahead[p] = pre(row0 + (p0 + p) * RPP + lane / LPR, col);
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p) {
+                const int row = (p0 + p) * RPP + lane / LPR;
+                float v[8];
+                get(row, c8, v);
+                if constexpr (GLU) {
+                    float u[8];
+                    get(row, LPR + c8, u);
+                    f(row0 + row, col, ahead[p], v, u);
+                } else {
+                    f(row0 + row, col, ahead[p], v);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,258 @@
+// The norm of many gradients together, and the gradients scaled to it.
+//
+//   norm = |s| sqrt(sum of squares)  or  |s| max,   c = min(1, max_norm / (norm + eps)),   out = (s c) g
+//
+// Two passes over the gradients, bound by memory.  Squares are summed in 64 bits (no
+// square of an fp32 number overflows or vanishes there), each workgroup's sum in a slot
+// of its own, and the second pass's workgroups each add the slots in one fixed order,
+// so no launch stands between the passes.  A maximum is that of the magnitudes' bits,
+// where NaN is above infinity.
+//
+// The tensors of a launch come as its arguments (their addresses may be others in the
+// next call).  They are cut into pieces of 16384 elements, a run of consecutive pieces
+// to a workgroup; loads are of whole aligned 16-byte words, the neighbours' elements
+// in a tensor's first and last word left out.
+#pragma once
+
+#include "dense.hpp"
+
+namespace moe {
+
+constexpr int kGradThreads = 512;
+constexpr int kGradPiece = 16384;   // elements
+constexpr int kGradParts = 2048;    // workgroups of the first pass, over all launches (and one more per launch)
+constexpr int kSumTensors = 176, kScaleTensors = 128;  // per launch: arguments below 4 KiB
+
+struct GradTensor {
+    const void *g;
+    int64_t n;  // elements << 2 | type
+};
+template <int N, bool OUT>
+struct GradLaunch {
+    GradTensor t[N];
+    void *out[OUT ? N : 1];
+    int32_t piece[N + 1];  // each tensor's first piece; piece[count]: all of them
+    int32_t count;
+};
+struct GradScalars {
+    double *parts;
+    moe_grad_result *result;
+    const float *coef;  // given: no norm is formed
+    int32_t nparts, kind;
+    float scale, max_norm, eps;
+};
+
+template <class T>
+struct GradVec;  // 16 bytes of elements
+template <>
+struct GradVec<F32> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ float get(const u32x4 &v, int i) { return __uint_as_float(v[i]); }
+};
+template <class T>
+struct GradVec {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ float get(const u32x4 &v, int i) { return T::up((uint16_t)(v[i >> 1] >> (16 * (i & 1)))); }
+};
+
+struct GradSum {
+    double s = 0.0;
+    uint32_t m = 0;
+    __device__ __forceinline__ void add(float v, bool max_of) {
+        if (max_of)
+            m = max(m, __float_as_uint(v) & 0x7fffffffu);
+        else
+            s = fma((double)v, (double)v, s);
+    }
+};
+
+// Elements [e0, e1) of the tensor at g.
+template <class T>
+__device__ __forceinline__ void grad_sum_piece(const void *g, int64_t e0, int64_t e1, bool max_of, GradSum &acc) {
+    constexpr int N = GradVec<T>::N, ES = 16 / N;
+    // word w holds elements w N - lead ... of the tensor
+    const int lead = (int)(((uintptr_t)g & 15) / ES);
+    const u32x4 *p = reinterpret_cast<const u32x4 *>((uintptr_t)g & ~(uintptr_t)15);
+    const int64_t a = e0 + lead, b = e1 + lead;  // in the words' own count
+    const int64_t w0 = a / N, w1 = (b + N - 1) / N;
+    const int64_t in0 = (a + N - 1) / N, in1 = b / N;  // whole words
+    auto whole = [&](const u32x4 &v) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc.add(GradVec<T>::get(v, i), max_of);
+    };
+    constexpr int U = 4;
+    int64_t w = in0 + threadIdx.x;
+    for (; w + (U - 1) * kGradThreads < in1; w += U * kGradThreads) {
+        u32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = p[w + u * kGradThreads];
+#pragma unroll
+        for (int u = 0; u < U; ++u) whole(v[u]);
+    }
+    for (; w < in1; w += kGradThreads) whole(p[w]);
+    // at most one word at each end
+    auto part = [&](int64_t k) {
+        const u32x4 v = p[k];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (k * N + i >= a && k * N + i < b) acc.add(GradVec<T>::get(v, i), max_of);
+    };
+    if (threadIdx.x == 0 && w0 < in0) part(w0);
+    if (threadIdx.x == 64 && in1 < w1 && (in1 > w0 || w0 >= in0)) part(in1);
+}
+
+// A workgroup's sum, on thread 0.
+__device__ __forceinline__ double grad_join(const GradSum &acc, bool max_of, double *lds) {
+    double s = acc.s;
+    uint32_t m = acc.m;
+    for (int o = 32; o >= 1; o >>= 1) {
+        s += __shfl_xor(s, o, 64);
+        m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    }
+    const int wave = threadIdx.x / 64, waves = blockDim.x / 64;
+    if ((threadIdx.x & 63) == 0) lds[wave] = max_of ? (double)__uint_as_float(m) : s;
+    __syncthreads();
+    double r = lds[0];
+    for (int w = 1; w < waves; ++w) {
+        const double v = lds[w];
+        r = max_of ? (v > r || v != v ? v : r) : r + v;
+    }
+    return r;
+}
+
+template <class L, class F>
+__device__ __forceinline__ void grad_pieces(const L &l, bool backwards, F &&f) {
+    const int64_t all = l.piece[l.count];
+    const int first = (int)(all * blockIdx.x / gridDim.x), last = (int)(all * (blockIdx.x + 1) / gridDim.x);
+    if (first >= last) return;
+    const int start = backwards ? last - 1 : first;
+    int lo = 0, hi = l.count;  // the tensor that holds piece `start`: the last with piece[t] <= start
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (l.piece[mid] <= start) lo = mid; else hi = mid;
+    }
+    int t = lo;
+    for (int i = 0; i < last - first; ++i) {
+        const int c = backwards ? last - 1 - i : first + i;
+        if (backwards)
+            while (l.piece[t] > c) --t;
+        else
+            while (l.piece[t + 1] <= c) ++t;
+        const int64_t n = l.t[t].n >> 2, e0 = (int64_t)(c - l.piece[t]) * kGradPiece;
+        f(t, (int)(l.t[t].n & 3), e0, min(n, e0 + kGradPiece));
+    }
+}
+
+template <class L>
+__device__ __forceinline__ void grad_sums_body(const L &l, const GradScalars &k, double *lds) {
+    GradSum acc;
+    const bool max_of = k.kind == MOE_NORM_MAX;
+    grad_pieces(l, false, [&](int t, int type, int64_t e0, int64_t e1) {
+        if (type == MOE_TYPE_FP32)
+            grad_sum_piece<F32>(l.t[t].g, e0, e1, max_of, acc);
+        else if (type == MOE_TYPE_BF16)
+            grad_sum_piece<Bf16>(l.t[t].g, e0, e1, max_of, acc);
+        else
+            grad_sum_piece<Fp16>(l.t[t].g, e0, e1, max_of, acc);
+    });
+    const double s = grad_join(acc, max_of, lds);
+    if (threadIdx.x == 0) k.parts[blockIdx.x] = s;
+}
+
+// The norm's sum, and what it makes of the gradients, from the first pass's parts: on
+// every thread of any workgroup the same.
+__device__ __forceinline__ moe_grad_result grad_result(const GradScalars &k, double *lds) {
+    const bool max_of = k.kind == MOE_NORM_MAX;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < k.nparts; i += blockDim.x) {
+        const double v = k.parts[i];
+        s = max_of ? (v > s || v != v ? v : s) : s + v;
+    }
+    for (int o = 32; o >= 1; o >>= 1) {
+        const double v = __shfl_xor(s, o, 64);
+        s = max_of ? (v > s || v != v ? v : s) : s + v;
+    }
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x / 64] = s;
+    __syncthreads();
+    s = lds[0];
+    for (int w = 1; w < (int)blockDim.x / 64; ++w) {
+        const double v = lds[w];
+        s = max_of ? (v > s || v != v ? v : s) : s + v;
+    }
+    const double scale = k.scale < 0.f ? -(double)k.scale : (double)k.scale;
+    moe_grad_result r;
+    r.sum = max_of ? s * scale : s * scale * scale;
+    const double norm = max_of ? r.sum : sqrt(s) * scale, c = (double)k.max_norm / (norm + (double)k.eps);
+    r.norm = (float)norm;
+    r.coef = (float)(c >= 1.0 ? 1.0 : c);  // NaN stays
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ void grad_scale_piece(const void *g, void *out, int64_t e0, int64_t e1, float f) {
+    constexpr int N = GradVec<T>::N, ES = 16 / N;
+    const int lead = (int)(((uintptr_t)g & 15) / ES);
+    const u32x4 *p = reinterpret_cast<const u32x4 *>((uintptr_t)g & ~(uintptr_t)15);
+    char *o = static_cast<char *>(out);
+    const int64_t a = e0 + lead, b = e1 + lead, w0 = a / N, w1 = (b + N - 1) / N, in0 = (a + N - 1) / N, in1 = b / N;
+    auto scaled = [&](const u32x4 &v) {
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (N == 4)
+                r[i] = __float_as_uint(GradVec<T>::get(v, i) * f);
+            else
+                r[i] = (uint32_t)T::down(GradVec<T>::get(v, 2 * i) * f) | (uint32_t)T::down(GradVec<T>::get(v, 2 * i + 1) * f) << 16;
+        }
+        return r;
+    };
+    auto put = [&](int64_t w, const u32x4 &v) { __builtin_memcpy(o + (w * N - lead) * ES, &v, 16); };
+    constexpr int U = 4;
+    int64_t w = in0 + threadIdx.x;
+    for (; w + (U - 1) * kGradThreads < in1; w += U * kGradThreads) {
+        u32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = p[w + u * kGradThreads];
+#pragma unroll
+        for (int u = 0; u < U; ++u) put(w + u * kGradThreads, scaled(v[u]));
+    }
+    for (; w < in1; w += kGradThreads) put(w, scaled(p[w]));
+    auto part = [&](int64_t k) {
+        const u32x4 v = scaled(p[k]);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (k * N + i >= a && k * N + i < b) {
+                if constexpr (N == 4)
+                    reinterpret_cast<uint32_t *>(out)[k * N + i - lead] = v[i];
+                else
+                    reinterpret_cast<uint16_t *>(out)[k * N + i - lead] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+            }
+    };
+    if (threadIdx.x == 0 && w0 < in0) part(w0);
+    if (threadIdx.x == 64 && in1 < w1 && (in1 > w0 || w0 >= in0)) part(in1);
+}
+
+// Backwards: what the first pass read last is what the cache still holds.
+template <class L>
+__device__ __forceinline__ void grad_scale_body(const L &l, const GradScalars &k, double *lds) {
+    float f;
+    if (k.coef) {
+        f = k.scale * *k.coef;
+    } else {
+        const moe_grad_result r = grad_result(k, lds);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *k.result = r;
+        f = k.scale * r.coef;
+    }
+    grad_pieces(l, true, [&](int t, int type, int64_t e0, int64_t e1) {
+        const void *g = l.t[t].g;
+        if (f == 1.0f && g == l.out[t]) return;
+        if (type == MOE_TYPE_FP32)
+            grad_scale_piece<F32>(g, l.out[t], e0, e1, f);
+        else if (type == MOE_TYPE_BF16)
+            grad_scale_piece<Bf16>(g, l.out[t], e0, e1, f);
+        else
+            grad_scale_piece<Fp16>(g, l.out[t], e0, e1, f);
+    });
+}
+
+}  // namespace moe

@@ -1,0 +1,408 @@
+// Layer norm and its gradient.
+//
+//   m = mean(x), s = 1 / sqrt(mean((x - m)^2) + eps), xh = (x - m) s
+//   y = xh g + b
+//   dx = s (t - mean(t) - xh mean(t xh)) + dres,  t = dy g
+//   dg = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Bound by memory: a row is read once, held in registers through its sums (the
+// variance is that of the differences from the mean, a second sum in registers) and
+// written once.  A thread keeps the same columns for every row it takes, 8 at a time,
+// so gains and biases and the column sums of the gradient stay in its registers.
+// Rows up to 2048 elements are taken by a wave or a part of one (64, 32, 16 or 8
+// lanes: no barrier), longer ones by a workgroup.  The next row's loads are issued
+// before this row's sums.
+//
+// Any row length and stride: where H or a stride is not a multiple of 8, or a pointer
+// not of 16 bytes, the last 8 columns of a row start at H - 8 and overlap those before
+// them (ODD: they are counted once and written twice with the same value), and loads
+// are of elements' alignment.
+#pragma once
+
+#include "dense.hpp"
+#include "norm.hpp"
+
+namespace moe {
+
+// 8 consecutive elements as they lie in memory.
+template <class T>
+struct Chunk {
+    u32x4 v;
+    static constexpr int ES = 2;
+    template <bool ODD>
+    __device__ __forceinline__ void load(const char *p) {
+        if constexpr (ODD)
+            __builtin_memcpy(&v, p, 16);
+        else
+            v = *reinterpret_cast<const u32x4 *>(p);
+    }
+    __device__ __forceinline__ void load_some(const char *p, int n) {
+        v = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) v[e >> 1] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+    }
+    __device__ __forceinline__ void get(float (&o)[8]) const { unpack8<T>(v, o); }
+    template <bool ODD>
+    static __device__ __forceinline__ void store(char *p, const float (&o)[8]) {
+        const u32x4 w = pack8<T>(o);
+        if constexpr (ODD)
+            __builtin_memcpy(p, &w, 16);
+        else
+            *reinterpret_cast<u32x4 *>(p) = w;
+    }
+    static __device__ __forceinline__ void store_some(char *p, const float (&o)[8], int n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) reinterpret_cast<uint16_t *>(p)[e] = T::down(o[e]);
+    }
+};
+template <>
+struct Chunk<F32> {
+    f32x4 v[2];
+    static constexpr int ES = 4;
+    template <bool ODD>
+    __device__ __forceinline__ void load(const char *p) {
+        if constexpr (ODD) {
+            __builtin_memcpy(v, p, 32);
+        } else {
+            v[0] = reinterpret_cast<const f32x4 *>(p)[0];
+            v[1] = reinterpret_cast<const f32x4 *>(p)[1];
+        }
+    }
+    __device__ __forceinline__ void load_some(const char *p, int n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = e < n ? reinterpret_cast<const float *>(p)[e] : 0.f;
+    }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[e >> 2][e & 3];
+    }
+    template <bool ODD>
+    static __device__ __forceinline__ void store(char *p, const float (&o)[8]) {
+        const f32x4 a = f32x4{o[0], o[1], o[2], o[3]}, b = f32x4{o[4], o[5], o[6], o[7]};
+        if constexpr (ODD) {
+            __builtin_memcpy(p, &a, 16);
+            __builtin_memcpy(p + 16, &b, 16);
+        } else {
+            reinterpret_cast<f32x4 *>(p)[0] = a;
+            reinterpret_cast<f32x4 *>(p)[1] = b;
+        }
+    }
+    static __device__ __forceinline__ void store_some(char *p, const float (&o)[8], int n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) reinterpret_cast<float *>(p)[e] = o[e];
+    }
+};
+
+struct LnArgs {
+    const void *x;
+    const float *g, *b;  // b nullable (1 and 0 where null: g too)
+    void *y;
+    float *stats;  // [rows][2]: mean, 1 / std; nullable
+    int64_t rows, ldx, ldy;
+    int H;
+    float eps;
+};
+struct LnBwdArgs {
+    LnArgs f;  // y, b unused; stats read
+    const void *dy, *dres;
+    void *dx;
+    float *part;  // [workgroups][2][H]: sums of dg and of db (null: not wanted)
+};
+
+// The lanes that share a row: `lanes` of a wave (a power of two from 8 on), or the
+// workgroup.
+template <bool WAVE>
+struct Team {
+    int lanes, t, teams, team;  // threads per row, this one's place, teams per workgroup, this one's
+    __device__ __forceinline__ explicit Team(int lanes_) {
+        lanes = WAVE ? lanes_ : blockDim.x;
+        t = WAVE ? threadIdx.x & (lanes - 1) : threadIdx.x;
+        teams = WAVE ? blockDim.x / lanes : 1;
+        team = WAVE ? threadIdx.x / lanes : 0;
+    }
+};
+
+// Sums over a team, on all of its threads, in a fixed order.
+template <bool WAVE, int N>
+struct TeamSum {
+    RowSum<N> sum;
+    int lanes;
+    __device__ __forceinline__ TeamSum(float *lds, int lanes_) : sum(lds), lanes(lanes_) {}
+    __device__ __forceinline__ void operator()(float (&v)[N]) {
+        if constexpr (!WAVE) {
+            sum(v);
+        } else if (lanes == 64) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+        } else {
+            for (int o = lanes / 2; o >= 1; o >>= 1)
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], o, 64);
+        }
+    }
+};
+
+// A thread's columns: chunk i of CH starts at column at[i], of which the elements from
+// skip[i] on count (8: none).
+template <int CH, bool ODD>
+struct Columns {
+    int at[CH], skip[CH], H;
+    __device__ __forceinline__ Columns(int t, int lanes, int H_) : H(H_) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = (i * lanes + t) * 8;
+            at[i] = max(0, min(c, H - 8));
+            skip[i] = c < H ? c - at[i] : 8;
+        }
+    }
+    __device__ __forceinline__ bool in(int i) const { return skip[i] < 8; }
+    // whether element e of chunk i counts; without ODD a chunk counts as a whole
+    __device__ __forceinline__ bool counts(int i, int e) const { return ODD ? e >= skip[i] && e < H : in(i); }
+    template <class C>
+    __device__ __forceinline__ void load(C (&c)[CH], const void *p, int64_t elem) const {
+        const char *q = static_cast<const char *>(p) + elem * C::ES;
+        if (ODD && H < 8) {  // one chunk, which is the row
+            c[0].load_some(q, in(0) ? H : 0);
+#pragma unroll
+            for (int i = 1; i < CH; ++i) c[i] = c[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) c[i].template load<ODD>(q + (int64_t)at[i] * C::ES);
+        }
+    }
+    template <class C>
+    __device__ __forceinline__ void store(int i, void *p, int64_t elem, const float (&v)[8]) const {
+        if (!in(i)) return;
+        char *q = static_cast<char *>(p) + (elem + at[i]) * C::ES;
+        if (ODD && H < 8)
+            C::store_some(q, v, H);
+        else
+            C::template store<ODD>(q, v);
+    }
+    // fp32 values of the columns, `none` where p is null
+    __device__ __forceinline__ void vec(float (&v)[CH][8], const float *p, float none) const {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = p && in(i) && at[i] + e < H ? p[at[i] + e] : none;
+    }
+};
+
+// Gains and biases stay in registers where those last.
+constexpr bool ln_keeps(int CH, bool WAVE) { return WAVE || CH <= 2; }
+
+template <class TI, class TO, int CH, bool WAVE, bool ODD>
+__device__ __forceinline__ void ln_fwd_body(const LnArgs &a, int lanes, float *lds) {
+    const Team<WAVE> team(lanes);
+    const Columns<CH, ODD> col(team.t, team.lanes, a.H);
+    TeamSum<WAVE, 1> sum1(lds, team.lanes);
+    TeamSum<WAVE, 2> sum2(lds + 32, team.lanes);
+    const float inv_h = 1.0f / (float)a.H;
+    int64_t row = (int64_t)blockIdx.x * team.teams + team.team;
+    const int64_t step = (int64_t)gridDim.x * team.teams;
+    if (row >= a.rows) return;  // the whole team, and the whole workgroup where teams meet
+    Chunk<TI> c[CH];
+    col.load(c, a.x, row * a.ldx);
+    float g[CH][8], b[CH][8];
+    if (ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f), col.vec(b, a.b, 0.0f);
+    if constexpr (!WAVE) {
+        norm_clear(lds, 96);
+        __syncthreads();
+    }
+    for (; row < a.rows; row += step) {
+        float x[CH][8], s[1] = {0.f}, s2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            c[i].get(x[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[0] += col.counts(i, e) ? x[i][e] : 0.f;
+        }
+        if (row + step < a.rows) col.load(c, a.x, (row + step) * a.ldx);
+        sum1(s);
+        const float m = s[0] * inv_h;
+        // the differences' own mean is what the mean of the values lost to rounding
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[i][e] -= m;
+                const float d = col.counts(i, e) ? x[i][e] : 0.f;
+                s2[0] += d;
+                s2[1] = fmaf(d, d, s2[1]);
+            }
+        sum2(s2);
+        const float dm = s2[0] * inv_h, var = fmaxf(fmaf(-dm, dm, s2[1] * inv_h), 0.f);
+        const float rstd = __builtin_amdgcn_rsqf(s2[1] == s2[1] ? var + a.eps : s2[1]);  // fmaxf would drop a NaN
+        if (a.stats && team.t == 0) reinterpret_cast<float2 *>(a.stats)[row] = make_float2(m + dm, rstd);
+        if (!ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f), col.vec(b, a.b, 0.0f);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf((x[i][e] - dm) * rstd, g[i][e], b[i][e]);
+            col.template store<Chunk<TO>>(i, a.y, row * a.ldy, o);
+        }
+    }
+}
+
+// SUMS: with the column sums of dg and db.  lds: 64 words for the rows' sums, then, for
+// the waves' column sums, 16 CH words for each lane of a team.
+template <class TI, class TO, int CH, bool WAVE, bool ODD, bool SUMS>
+__device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float *lds) {
+    const LnArgs &a = k.f;
+    const Team<WAVE> team(lanes);
+    const Columns<CH, ODD> col(team.t, team.lanes, a.H);
+    TeamSum<WAVE, 2> sum(lds, team.lanes);
+    const float inv_h = 1.0f / (float)a.H;
+    int64_t row = (int64_t)blockIdx.x * team.teams + team.team;
+    const int64_t step = (int64_t)gridDim.x * team.teams;
+    Chunk<TI> cx[CH], cr[CH];
+    Chunk<TO> cy[CH];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](int64_t r) {
+        col.load(cx, a.x, r * a.ldx);
+        col.load(cy, k.dy, r * a.ldy);
+        if (k.dres) col.load(cr, k.dres, r * a.ldx);
+        const float2 st = reinterpret_cast<const float2 *>(a.stats)[r];
+        mean = st.x, rstd = st.y;
+    };
+    if (row < a.rows) fetch(row);
+    float g[CH][8], dg[SUMS ? CH : 1][8], db[SUMS ? CH : 1][8];
+    if (ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f);
+    if constexpr (SUMS) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.f;
+    }
+    if constexpr (!WAVE) {
+        norm_clear(lds, 64);
+        __syncthreads();
+    }
+    for (; row < a.rows; row += step) {
+        float xh[CH][8], t[CH][8], res[CH][8], s[2] = {0.f, 0.f};
+        const float m = mean, rs = rstd;
+        if (!ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            cx[i].get(xh[i]);
+            cy[i].get(t[i]);
+            if (k.dres) cr[i].get(res[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[i][e] = (xh[i][e] - m) * rs;
+                if constexpr (SUMS) {
+                    dg[i][e] = fmaf(t[i][e], xh[i][e], dg[i][e]);
+                    db[i][e] += t[i][e];
+                }
+                t[i][e] *= g[i][e];
+                if (col.counts(i, e)) {
+                    s[0] += t[i][e];
+                    s[1] = fmaf(t[i][e], xh[i][e], s[1]);
+                }
+            }
+        }
+        if (row + step < a.rows) fetch(row + step);
+        sum(s);
+        const float c0 = s[0] * inv_h, c1 = s[1] * inv_h;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e] = rs * (t[i][e] - fmaf(xh[i][e], c1, c0));
+                if (k.dres) o[e] += res[i][e];
+            }
+            col.template store<Chunk<TI>>(i, k.dx, row * a.ldx, o);
+        }
+    }
+    if constexpr (SUMS) {
+        if (!k.part) return;
+        float *out = k.part + (int64_t)blockIdx.x * 2 * a.H;
+        auto store = [&]() {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                col.template store<Chunk<F32>>(i, out, 0, dg[i]);
+                col.template store<Chunk<F32>>(i, out, a.H, db[i]);
+            }
+        };
+        if constexpr (!WAVE) {
+            store();
+        } else {
+            // the teams of a wave, then its waves in turn
+            for (int o = team.lanes; o < 64; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dg[i][e] += __shfl_xor(dg[i][e], o, 64);
+                        db[i][e] += __shfl_xor(db[i][e], o, 64);
+                    }
+            const int waves = blockDim.x / 64, wave = threadIdx.x / 64;
+            const bool mine = (int)(threadIdx.x & 63) < team.lanes;
+            float *p = lds + 64 + team.t;
+            for (int w = 0; w < waves; ++w) {
+                if (wave == w && mine) {
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float *q = p + (i * 16 + e) * team.lanes, *r = q + 8 * team.lanes;
+                            if (w) dg[i][e] += *q, db[i][e] += *r;
+                            if (w + 1 < waves) *q = dg[i][e], *r = db[i][e];
+                        }
+                    if (w + 1 == waves) store();
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+// dg and db of long rows, from a second reading: a workgroup of 4 waves takes 512
+// columns and every 4 gridDim.y-th row, 8 columns a lane.
+template <class TI, class TO, bool ODD>
+__device__ __forceinline__ void ln_columns_body(const LnBwdArgs &k, float *lds) {
+    const LnArgs &a = k.f;
+    const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
+    const Columns<1, ODD> col(blockIdx.x * 64 + lane, 0, a.H);
+    float dg[8], db[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[e] = db[e] = 0.f;
+    for (int64_t row = (int64_t)blockIdx.y * 4 + wave; row < a.rows; row += 4 * (int64_t)gridDim.y) {
+        Chunk<TI> cx[1];
+        Chunk<TO> cy[1];
+        col.load(cx, a.x, row * a.ldx);
+        col.load(cy, k.dy, row * a.ldy);
+        const float2 st = reinterpret_cast<const float2 *>(a.stats)[row];
+        float x[8], d[8];
+        cx[0].get(x);
+        cy[0].get(d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dg[e] = fmaf(d[e], (x[e] - st.x) * st.y, dg[e]);
+            db[e] += d[e];
+        }
+    }
+    float *out = k.part + (int64_t)blockIdx.y * 2 * a.H;
+    for (int w = 0; w < 4; ++w) {
+        if (wave == w) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float *q = lds + e * 64 + lane, *r = q + 512;
+                if (w) dg[e] += *q, db[e] += *r;
+                if (w < 3) *q = dg[e], *r = db[e];
+            }
+            if (w == 3) {
+                col.template store<Chunk<F32>>(0, out, 0, dg);
+                col.template store<Chunk<F32>>(0, out, a.H, db);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace moe

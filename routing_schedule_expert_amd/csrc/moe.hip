@@ -15,6 +15,7 @@
 #include "common.hpp"
 #include "few.hpp"
 #include "gemm.hpp"
+#include "host.hpp"
 #include "layer.hpp"
 #include "mxbwd.hpp"
 #include "norm.hpp"
@@ -275,34 +276,22 @@ std::vector<TraceRec> g_trace;
 int g_trace_cap = 0;
 int g_trace_used = 0;
 
-struct TraceScope {
-    TraceRec *rec = nullptr;
-    hipStream_t stream;
-    TraceScope(const char *name, hipStream_t s) : stream(s) {
-        if (g_trace_used < g_trace_cap) {
-            rec = &g_trace[g_trace_used++];
-            strncpy(rec->name, name, 31);
-            rec->name[31] = 0;
-            (void)hipEventRecord(rec->start, s);
-        }
-    }
-    ~TraceScope() {
-        if (rec) (void)hipEventRecord(rec->stop, stream);
-    }
-};
+}  // namespace
 
-// Per-device compute-unit count (the persistent grids are sized to it).
-int device_cus() {
-    static int cache[64] = {0};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-        cache[dev] = n;
+moe::TraceScope::TraceScope(const char *name, hipStream_t s) : rec(-1), stream(s) {
+    if (g_trace_used < g_trace_cap) {
+        rec = g_trace_used++;
+        TraceRec &r = g_trace[rec];
+        strncpy(r.name, name, 31);
+        r.name[31] = 0;
+        (void)hipEventRecord(r.start, s);
     }
-    return cache[dev];
 }
+moe::TraceScope::~TraceScope() {
+    if (rec >= 0) (void)hipEventRecord(g_trace[rec].stop, stream);
+}
+
+namespace {
 
 // Persistent GEMM grid: one workgroup per CU, rounded down to a multiple of 8
 // (one per XCD) so the XCD-aware tile order stays exact.
@@ -311,8 +300,6 @@ int gemm_grid() {
     g -= g % 8;
     return g > 0 ? g : 8;
 }
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 int check_desc(const moe_desc *d, bool need_ffn) {
     if (!d) return MOE_EINVAL;
@@ -358,7 +345,6 @@ int sched_chunks(const moe_desc *d) {
 }
 int sched_wg_per_part(const moe_desc *d) { return (sched_chunks(d) + kSchedWaves - 1) / kSchedWaves; }
 
-int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace of the shared expert's identity table: 2 offsets, then the rows.
 int64_t shared_table_bytes(const moe_desc *d) { return 256 + align256(shared_rows(d) * 8); }
@@ -447,8 +433,6 @@ int64_t mx_bwd_ws_bytes(const moe_desc *d) {
 
 constexpr int64_t kBarrierBytes = 256;
 
-int launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
-
 void fill_sched_args(SchedArgs &a, const moe_desc *d, const int32_t *routes, int32_t *counts, int32_t *seg_off,
                      moe_src *phi, int32_t *route_row, char *ws, int wpw) {
     a.routes = routes;
@@ -478,8 +462,6 @@ void fill_sched_args(SchedArgs &a, const moe_desc *d, const int32_t *routes, int
     a.ids8 = d->L <= 255 ? reinterpret_cast<uint8_t *>(ws + sched_ids8_offset(d)) : nullptr;
     a.nblk = (int32_t)sched_nblk(d);
 }
-
-constexpr size_t kMaxLds = 160 * 1024;  // LDS of one gfx950 workgroup
 
 // LDS (bytes) of each schedule body for `wpw` waves per workgroup (stage 0
 // count, 1 finalize, 2 scatter; -1: the largest, for a caller running all three).
@@ -617,7 +599,6 @@ int launch_ffn(const moe_desc *d, const FfnArgs &a, hipStream_t s) {
     return launch_cooperative(reinterpret_cast<const void *>(k_ffn_chunked), grid, args, s);
 }
 
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 int launch_mx_quantize(const uint16_t *src, int64_t rows, int32_t K, uint8_t *q, uint8_t *sc, hipStream_t s,
                        const char *name) {
@@ -1792,13 +1773,6 @@ auto *norm_bwd_kernel(const moe_norm_desc *n) {
 NormArgs norm_args(const moe_norm_desc *n, const uint16_t *y, const void *r, const void *z, const float *g_post,
                    const float *g_pre, float *stats) {
     return NormArgs{y, r, z, g_post, g_pre, nullptr, nullptr, stats, n->rows, n->H, n->gate, n->alpha, n->beta, n->eps};
-}
-
-// NULL or 16-byte aligned, each of them.
-bool all_aligned(std::initializer_list<const void *> ps) {
-    for (const void *p : ps)
-        if (!aligned16(p)) return false;
-    return true;
 }
 
 }  // namespace

@@ -29,6 +29,9 @@ MOE_WS_INVALID_IDS, MOE_WS_BARRIER_STATUS = 0, 1
 MOE_WS_SINGLE_ROUTE = 15
 MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_ELEM = range(3)
 CKPT_BLOCK = 128
+MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_FP32 = range(3)
+MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU = range(4)
+MOE_NORM_L2, MOE_NORM_MAX = range(2)
 
 EXPORTED = (
     "moe_strerror", "moe_capacity_rows", "moe_workspace_bytes", "moe_workspace_field", "moe_schedule",
@@ -41,6 +44,9 @@ EXPORTED = (
     "moe_few_workspace_bytes", "moe_layer_fwd_few", "moe_layer_fwd_few_mx",
     "moe_block_norm_workspace_bytes", "moe_block_norm_fwd", "moe_block_norm_bwd",
     "moe_ckpt_pack", "moe_ckpt_swiglu_bwd", "moe_layer_bwd_ckpt",
+    "moe_gated_ffn_workspace_bytes", "moe_gated_ffn_fwd", "moe_gated_ffn_bwd",
+    "moe_layer_norm_workspace_bytes", "moe_layer_norm_fwd", "moe_layer_norm_bwd",
+    "moe_grad_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "moe_grad_scale",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -59,6 +65,20 @@ class moe_desc(ctypes.Structure):
 class moe_norm_desc(ctypes.Structure):
     _fields_ = ([("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("H", "gate", "res_fp32")] +
                 [(n, ctypes.c_float) for n in ("alpha", "beta", "eps")])
+
+
+class moe_ffn_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "ldx", "ldo")] + [(n, ctypes.c_int32) for n in ("H", "I", "act", "type")])
+
+
+class moe_ln_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "ldx", "ldy")] +
+                [(n, ctypes.c_int32) for n in ("H", "x_type", "y_type")] + [("eps", ctypes.c_float)])
+
+
+class moe_grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 def make_desc(P, Np, K, E, L=None, expert_base=0, pad_rows=256, sched_threads=1024, H=0, I=0, num_batches=1):
@@ -80,7 +100,8 @@ def load() -> ctypes.CDLL:
                           "(or __graft_entry__.build()); there is no fallback path")
     lib = ctypes.CDLL(LIB_PATH)
     P, D, N = ctypes.c_void_p, ctypes.POINTER(moe_desc), ctypes.POINTER(moe_norm_desc)
-    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F, LN, G = ctypes.POINTER(moe_ffn_desc), ctypes.POINTER(moe_ln_desc), ctypes.POINTER(moe_grad)
+    i32, i64, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "moe_capacity_rows": (i64, [D]),
@@ -111,6 +132,16 @@ def load() -> ctypes.CDLL:
         "moe_ckpt_pack": (ctypes.c_int, [P, i64, i32, P, P, P, P]),
         "moe_ckpt_swiglu_bwd": (ctypes.c_int, [P, P, P, P, i64, i32, P, P, P, P, P]),
         "moe_layer_bwd_ckpt": (ctypes.c_int, [D] + [P] * 15 + [sz, P]),
+        "moe_gated_ffn_workspace_bytes": (i64, [F, i32]),
+        "moe_gated_ffn_fwd": (ctypes.c_int, [F] + [P] * 7 + [sz, P]),
+        "moe_gated_ffn_bwd": (ctypes.c_int, [F] + [P] * 9 + [i32, i32, P, sz, P]),
+        "moe_layer_norm_workspace_bytes": (i64, [LN]),
+        "moe_layer_norm_fwd": (ctypes.c_int, [LN] + [P] * 6),
+        "moe_layer_norm_bwd": (ctypes.c_int, [LN] + [P] * 9 + [sz, P]),
+        "moe_grad_workspace_bytes": (i64, [i32]),
+        "moe_grad_norm": (ctypes.c_int, [G, i32, i32, f32, f32, f32, P, P, sz, P]),
+        "moe_grad_clip": (ctypes.c_int, [G, i32, i32, f32, f32, f32, P, P, sz, P]),
+        "moe_grad_scale": (ctypes.c_int, [G, i32, P, f32, P]),
         "moe_trace_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_trace_read": (ctypes.c_int, [P, P, ctypes.c_int]),
     }
@@ -750,3 +781,256 @@ def moe_layer_bwd_ckpt(d, dOut, w, X, phi, route_row, seg_off, q, scales, W13, W
             _buf("W2", W2, bf, d.L * H * I, dev), _buf("dX", dX, bf, n * H, dev), _buf("dW13", dW13, f32, d.L * 2 * I * H, dev),
             _buf("dW2", dW2, f32, d.L * H * I, dev), _buf("dw", dw, f32, n * d.K, dev), _buf("ws", ws, torch.uint8, 0, dev)]
     return _run("moe_layer_bwd_ckpt", dev, stream, ctypes.byref(d), *args, 0 if ws is None else ws.numel())
+
+
+# ---------------------------------------------------------------------------
+# The gated feed-forward block.
+# ---------------------------------------------------------------------------
+
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16, torch.float32: MOE_TYPE_FP32}
+_DTYPES = {v: k for k, v in _TYPES.items()}
+
+
+def _type(dtype) -> int:
+    if dtype not in _TYPES:
+        raise ValueError(f"unsupported element type {dtype}")
+    return _TYPES[dtype]
+
+
+def make_ffn_desc(rows, H, I, act=MOE_ACT_SILU, dtype=torch.bfloat16, ldx=0, ldo=0):
+    """ldx, ldo: elements from one row of X and dX, and of out and dOut, to the next (0: H)."""
+    return moe_ffn_desc(rows, ldx, ldo, H, I, act, _type(dtype))
+
+
+def gated_ffn_workspace_bytes(n: moe_ffn_desc, bwd: bool = False) -> int:
+    b = load().moe_gated_ffn_workspace_bytes(ctypes.byref(n), int(bwd))
+    if b < 0:
+        raise MoeError(MOE_EINVAL, "moe_gated_ffn_workspace_bytes")
+    return int(b)
+
+
+def _rows(name: str, t, dtype, rows: int, H: int, ld: int, dev: int):
+    """Device pointer of a tensor of `rows` rows of H elements, ld apart (0: H)."""
+    if t is None:
+        return None
+    ld = ld or H
+    if ld == H and t.is_contiguous():
+        return _buf(name, t, dtype, rows * H, dev)
+    if t.dim() != 2 or t.dtype != dtype or t.get_device() != dev or t.shape[0] < rows or t.shape[1] != H or t.stride(1) != 1 or (
+            rows > 1 and t.stride(0) != ld):
+        raise ValueError(f"{name}: needs {rows} rows of {H} elements of {dtype}, {ld} apart, on cuda:{dev}, got {tuple(t.shape)} with "
+                         f"strides {t.stride()} of {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def moe_gated_ffn_fwd(n, X, W13, W2, HU, A, out, ws, stream=None):
+    R, H, I, dev, dt = n.rows, n.H, n.I, X.get_device(), _DTYPES.get(n.type)
+    args = [_rows("X", X, dt, R, H, n.ldx, dev), _buf("W13", W13, dt, 2 * I * H, dev), _buf("W2", W2, dt, H * I, dev),
+            _buf("HU", HU, dt, 2 * R * I, dev), _buf("A", A, dt, R * I, dev), _rows("out", out, dt, R, H, n.ldo, dev),
+            _buf("ws", ws, torch.uint8, 0, dev)]
+    return _run("moe_gated_ffn_fwd", dev, stream, ctypes.byref(n), *args, 0 if ws is None else ws.numel())
+
+
+def moe_gated_ffn_bwd(n, dOut, X, HU, A, W13, W2, dX, dW13, dW2, ws, accumulate=False, stream=None):
+    R, H, I, dev, dt = n.rows, n.H, n.I, X.get_device(), _DTYPES.get(n.type)
+    wt = next((t.dtype for t in (dW13, dW2) if t is not None), torch.float32)
+    args = [_rows("dOut", dOut, dt, R, H, n.ldo, dev), _rows("X", X, dt, R, H, n.ldx, dev), _buf("HU", HU, dt, 2 * R * I, dev),
+            _buf("A", A, dt, R * I, dev), _buf("W13", W13, dt, 2 * I * H, dev), _buf("W2", W2, dt, H * I, dev),
+            _rows("dX", dX, dt, R, H, n.ldx, dev), _buf("dW13", dW13, wt, 2 * I * H, dev), _buf("dW2", dW2, wt, H * I, dev)]
+    return _run("moe_gated_ffn_bwd", dev, stream, ctypes.byref(n), *args, _type(wt), int(accumulate), _buf("ws", ws, torch.uint8, 0, dev),
+                0 if ws is None else ws.numel())
+
+
+@dataclass
+class FfnBuffers:
+    out: torch.Tensor
+    HU: torch.Tensor | None
+    A: torch.Tensor
+    ws: torch.Tensor
+
+
+def _alloc_rows(rows, H, ld, dtype, device):
+    return torch.empty((rows, ld or H), dtype=dtype, device=device)[:, :H]
+
+
+def alloc_gated_ffn(n: moe_ffn_desc, device, save_hu: bool = True) -> FfnBuffers:
+    """Outputs and workspace of the forward; save_hu=False: no pre-activations for a backward."""
+    dt = _DTYPES[n.type]
+    return FfnBuffers(
+        out=_alloc_rows(n.rows, n.H, n.ldo, dt, device),
+        HU=torch.empty((n.rows, 2 * n.I), dtype=dt, device=device) if save_hu else None,
+        A=torch.empty((n.rows, n.I), dtype=dt, device=device),
+        ws=torch.empty(max(gated_ffn_workspace_bytes(n), 256), dtype=torch.uint8, device=device),
+    )
+
+
+def gated_ffn_fwd(n, X, W13, W2, b: FfnBuffers, stream=None):
+    return moe_gated_ffn_fwd(n, X, W13, W2, b.HU, b.A, b.out, b.ws, stream)
+
+
+@dataclass
+class FfnGrads:
+    dX: torch.Tensor | None
+    dW13: torch.Tensor | None
+    dW2: torch.Tensor | None
+    ws: torch.Tensor
+
+
+def alloc_gated_ffn_bwd(n: moe_ffn_desc, device, dx: bool = True, dw: bool = True, dw_dtype=torch.float32) -> FfnGrads:
+    """Gradients (dx=False, dw=False: without those of X, of the weights) and workspace of the backward."""
+    return FfnGrads(
+        dX=_alloc_rows(n.rows, n.H, n.ldx, _DTYPES[n.type], device) if dx else None,
+        dW13=torch.empty((2 * n.I, n.H), dtype=dw_dtype, device=device) if dw else None,
+        dW2=torch.empty((n.H, n.I), dtype=dw_dtype, device=device) if dw else None,
+        ws=torch.empty(max(gated_ffn_workspace_bytes(n, True), 256), dtype=torch.uint8, device=device),
+    )
+
+
+def gated_ffn_bwd(n, dOut, X, HU, A, W13, W2, b: FfnGrads, accumulate=False, stream=None):
+    """A=None: the activations are computed again from HU."""
+    return moe_gated_ffn_bwd(n, dOut, X, HU, A, W13, W2, b.dX, b.dW13, b.dW2, b.ws, accumulate, stream)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm.
+# ---------------------------------------------------------------------------
+
+def make_layer_norm_desc(rows, H, x_dtype=torch.bfloat16, y_dtype=None, eps=1e-5, ldx=0, ldy=0):
+    """y_dtype: None for x's; ldx, ldy: elements from one row of x, dx, dres, and of y, dy, to the next (0: H)."""
+    return moe_ln_desc(rows, ldx, ldy, H, _type(x_dtype), _type(y_dtype or x_dtype), eps)
+
+
+def layer_norm_workspace_bytes(n: moe_ln_desc) -> int:
+    b = load().moe_layer_norm_workspace_bytes(ctypes.byref(n))
+    if b < 0:
+        raise MoeError(MOE_EINVAL, "moe_layer_norm_workspace_bytes")
+    return int(b)
+
+
+def moe_layer_norm_fwd(n, x, g, b, y, stats, stream=None):
+    R, H, dev, f32 = n.rows, n.H, x.get_device(), torch.float32
+    args = [_rows("x", x, _DTYPES.get(n.x_type), R, H, n.ldx, dev), _buf("g", g, f32, H, dev), _buf("b", b, f32, H, dev),
+            _rows("y", y, _DTYPES.get(n.y_type), R, H, n.ldy, dev), _buf("stats", stats, f32, 2 * R, dev)]
+    return _run("moe_layer_norm_fwd", dev, stream, ctypes.byref(n), *args)
+
+
+def moe_layer_norm_bwd(n, x, g, stats, dy, dres, dx, dg, db, ws, stream=None):
+    R, H, dev, f32, tx = n.rows, n.H, x.get_device(), torch.float32, _DTYPES.get(n.x_type)
+    args = [_rows("x", x, tx, R, H, n.ldx, dev), _buf("g", g, f32, H, dev), _buf("stats", stats, f32, 2 * R, dev),
+            _rows("dy", dy, _DTYPES.get(n.y_type), R, H, n.ldy, dev), _rows("dres", dres, tx, R, H, n.ldx, dev),
+            _rows("dx", dx, tx, R, H, n.ldx, dev), _buf("dg", dg, f32, H, dev), _buf("db", db, f32, H, dev),
+            _buf("ws", ws, torch.uint8, 0, dev)]
+    return _run("moe_layer_norm_bwd", dev, stream, ctypes.byref(n), *args, 0 if ws is None else ws.numel())
+
+
+@dataclass
+class LayerNormBuffers:
+    y: torch.Tensor
+    stats: torch.Tensor | None
+
+
+def alloc_layer_norm(n: moe_ln_desc, device, stats: bool = True) -> LayerNormBuffers:
+    return LayerNormBuffers(
+        y=_alloc_rows(n.rows, n.H, n.ldy, _DTYPES[n.y_type], device),
+        stats=torch.empty((n.rows, 2), dtype=torch.float32, device=device) if stats else None,
+    )
+
+
+def layer_norm_fwd(n, x, g, b, bufs: LayerNormBuffers, stream=None):
+    return moe_layer_norm_fwd(n, x, g, b, bufs.y, bufs.stats, stream)
+
+
+@dataclass
+class LayerNormGrads:
+    dx: torch.Tensor
+    dg: torch.Tensor | None
+    db: torch.Tensor | None
+    ws: torch.Tensor | None
+    both: torch.Tensor | None  # dg and db, which the call writes together
+
+
+def alloc_layer_norm_bwd(n: moe_ln_desc, device, weight: bool = True, bias: bool = True) -> LayerNormGrads:
+    """Gradients and workspace of moe_layer_norm_bwd; weight=False: of x alone, bias=False: no db to show."""
+    both = torch.empty((2, n.H), dtype=torch.float32, device=device) if weight or bias else None
+    return LayerNormGrads(
+        dx=_alloc_rows(n.rows, n.H, n.ldx, _DTYPES[n.x_type], device),
+        dg=both[0] if weight else None,
+        db=both[1] if bias else None,
+        ws=torch.empty(max(layer_norm_workspace_bytes(n), 256), dtype=torch.uint8, device=device) if both is not None else None,
+        both=both,
+    )
+
+
+def layer_norm_bwd(n, x, g, stats, dy, dres, b: LayerNormGrads, stream=None):
+    dg, db = (None, None) if b.both is None else (b.both[0], b.both[1])
+    return moe_layer_norm_bwd(n, x, g, stats, dy, dres, b.dx, dg, db, b.ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# Norm and clipping of gradients.
+# ---------------------------------------------------------------------------
+
+@dataclass
+class GradList:
+    """Gradients and where their scaled values go (out: the gradients themselves), as
+    the library takes them, with the result and the workspace of its calls.  It holds
+    the tensors; a gradient that is allocated anew each step needs a new list."""
+    grads: list
+    out: list
+    table: object
+    dev: int
+    result: torch.Tensor  # 16 bytes: sum (float64), norm, coef (float32)
+    ws: torch.Tensor
+
+    @property
+    def sum(self):
+        return self.result.view(torch.float64)[:1]
+
+    @property
+    def norm(self):
+        return self.result.view(torch.float32)[2:3]
+
+    @property
+    def coef(self):
+        return self.result.view(torch.float32)[3:4]
+
+
+def make_grad_list(grads, out=None, device=None) -> GradList:
+    """grads: contiguous fp32, bf16 or fp16 tensors of one GPU; out: as many of the same types
+    and sizes (None: the gradients themselves); device: needed where grads is empty."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"{len(grads)} gradients, {len(out)} outputs")
+    dev = grads[0].get_device() if grads else torch.device(device).index
+    if dev is None or dev < 0:
+        raise TypeError("device buffers must be CUDA (HIP) torch tensors")
+    table = (moe_grad * max(1, len(grads)))()
+    for i, (g, o) in enumerate(zip(grads, out)):
+        if o.numel() != g.numel():
+            raise ValueError(f"out {i}: {o.numel()} elements for a gradient of {g.numel()}")
+        table[i] = moe_grad(_buf(f"gradient {i}", g, g.dtype, 0, dev), _buf(f"out {i}", o, g.dtype, 0, dev), g.numel(), _type(g.dtype), 0)
+    device = torch.device("cuda", dev)
+    return GradList(grads, out, table, dev, torch.zeros(16, dtype=torch.uint8, device=device),
+                    torch.empty(load().moe_grad_workspace_bytes(len(grads)), dtype=torch.uint8, device=device))
+
+
+def _grad_call(name, gl, max_norm, kind, scale, eps, stream):
+    _run(name, gl.dev, stream, gl.table, len(gl.grads), kind, scale, max_norm, eps, gl.result.data_ptr(), gl.ws.data_ptr(), gl.ws.numel())
+    return gl
+
+
+def grad_norm(gl: GradList, max_norm=1.0, kind=MOE_NORM_L2, scale=1.0, eps=1e-6, stream=None) -> GradList:
+    """Leaves gl.sum, gl.norm and gl.coef."""
+    return _grad_call("moe_grad_norm", gl, max_norm, kind, scale, eps, stream)
+
+
+def grad_clip(gl: GradList, max_norm, kind=MOE_NORM_L2, scale=1.0, eps=1e-6, stream=None) -> GradList:
+    """Leaves gl.sum, gl.norm, gl.coef and the scaled gradients in gl.out."""
+    return _grad_call("moe_grad_clip", gl, max_norm, kind, scale, eps, stream)
+
+
+def grad_scale(gl: GradList, coef, scale=1.0, stream=None) -> GradList:
+    """Leaves scale * coef * gradient in gl.out; coef: a float on the device."""
+    _run("moe_grad_scale", gl.dev, stream, gl.table, len(gl.grads), _buf("coef", coef, torch.float32, 1, gl.dev), scale)
+    return gl
