@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseArgs g, Out out) {
 }
 
 template <class TI, class TO, int CH, bool WAVE, bool ODD>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_fwd(LnArgs a, int lanes) {
+__global__ __launch_bounds__(WAVE ? 256 : 1024, !WAVE && CH == 1 && sizeof(Chunk<TI>) == 16 ? 8 : 4) void k_ln_fwd(LnArgs a, int lanes) {
     ln_fwd_body<TI, TO, CH, WAVE, ODD>(a, lanes, reinterpret_cast<float *>(block_lds));
 }
 
@@ -73,7 +73,10 @@ __device__ __forceinline__ const __attribute__((address_space(4))) L &first_argu
 
 __global__ __launch_bounds__(kGradThreads) void k_grad_sums(GradLaunch<kSumTensors, false>, GradScalars k) {
     __shared__ double lds[kGradThreads / 64];
-    grad_sums_body(first_argument<GradLaunch<kSumTensors, false>>(), k, lds);
+    if (k.kind == MOE_NORM_MAX)
+        grad_sums_body<true>(first_argument<GradLaunch<kSumTensors, false>>(), k, lds);
+    else
+        grad_sums_body<false>(first_argument<GradLaunch<kSumTensors, false>>(), k, lds);
 }
 
 __global__ __launch_bounds__(kGradThreads) void k_grad_scale(GradLaunch<kScaleTensors, true>, GradScalars k) {
@@ -279,7 +282,7 @@ int ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_t *X, cons
 
 int64_t ln_ldx(const moe_ln_desc *n) { return n->ldx ? n->ldx : n->H; }
 int64_t ln_ldy(const moe_ln_desc *n) { return n->ldy ? n->ldy : n->H; }
-constexpr int kLnWaveH = 2048, kLnMaxH = 32768, kLnSumH = 8192;
+constexpr int kLnWaveH = 512, kLnMaxH = 32768, kLnSumH = 8192;
 
 int ln_check(const moe_ln_desc *n) {
     if (!n || n->rows < 0 || n->H < 1 || n->ldx < 0 || n->ldy < 0 || ln_ldx(n) < n->H || ln_ldy(n) < n->H || !(n->eps >= 0.0f) ||
@@ -301,9 +304,9 @@ LnPlan ln_plan(const moe_ln_desc *n) {
     const int c = (n->H + 7) / 8;
     p.wave = n->H <= kLnWaveH;
     if (p.wave) {
-        p.chunks = n->H <= 512 ? 1 : n->H <= 1024 ? 2 : 4;
+        p.chunks = 1;
         p.lanes = 8;
-        while (p.lanes * p.chunks < c) p.lanes *= 2;
+        while (p.lanes < c) p.lanes *= 2;
         p.threads = 256;
         p.teams = p.threads / p.lanes;
     } else {
@@ -331,20 +334,14 @@ bool ln_aligned(const void *p, int type) { return ((uintptr_t)p & (type == MOE_T
 
 template <class TI, class TO, bool ODD>
 auto *ln_fwd_kernel(const LnPlan &p) {
-    if (p.wave)
-        return p.chunks == 1   ? k_ln_fwd<TI, TO, 1, true, ODD>
-               : p.chunks == 2 ? k_ln_fwd<TI, TO, 2, true, ODD>
-                               : k_ln_fwd<TI, TO, 4, true, ODD>;
+    if (p.wave) return k_ln_fwd<TI, TO, 1, true, ODD>;
     return p.chunks == 1   ? k_ln_fwd<TI, TO, 1, false, ODD>
            : p.chunks == 2 ? k_ln_fwd<TI, TO, 2, false, ODD>
                            : k_ln_fwd<TI, TO, 4, false, ODD>;
 }
 template <class TI, class TO, bool ODD>
 auto *ln_bwd_kernel(const LnPlan &p) {
-    if (p.wave)
-        return p.chunks == 1   ? k_ln_bwd<TI, TO, 1, true, ODD, true>
-               : p.chunks == 2 ? k_ln_bwd<TI, TO, 2, true, ODD, true>
-                               : k_ln_bwd<TI, TO, 4, true, ODD, true>;
+    if (p.wave) return k_ln_bwd<TI, TO, 1, true, ODD, true>;
     return p.chunks == 1   ? k_ln_bwd<TI, TO, 1, false, ODD, true>
            : p.chunks == 2 ? k_ln_bwd<TI, TO, 2, false, ODD, false>
                            : k_ln_bwd<TI, TO, 4, false, ODD, false>;
@@ -406,17 +403,13 @@ bool grad_fill(GradLaunch<N, OUT> &l, const moe_grad *t, int32_t n, int32_t *at)
 }
 
 int grad_launches(int32_t n) { return (n + kSumTensors - 1) / kSumTensors; }
-int64_t grad_ws_bytes(int32_t n) { return 8 * (int64_t)(kGradParts + grad_launches(n)); }
+int64_t grad_ws_bytes(int32_t n) { return 8ll * kGradParts * std::max(1, grad_launches(n)); }
 
 int launch_grad_sums(const moe_grad *t, int32_t n, GradScalars &k, hipStream_t s) {
-    int64_t all = 0;
-    for (int i = 0; i < n; ++i) all += grad_pieces_of(t[i].numel);
     double *parts = k.parts;
     GradLaunch<kSumTensors, false> l;
     for (int32_t at = 0; grad_fill(l, t, n, &at);) {
-        // its share of the slots, one at least
-        const int64_t pieces = l.piece[l.count], share = std::max<int64_t>(1, pieces * kGradParts / std::max(all, pieces));
-        const int grid = (int)std::min(pieces, share);
+        const int grid = std::min(l.piece[l.count], kGradParts);
         GradScalars a = k;
         a.parts = parts;
         {
@@ -436,9 +429,8 @@ int launch_grad_result(const GradScalars &k, hipStream_t s) {
     return launch_status();
 }
 
-int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s, bool *any) {
+int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s) {
     GradLaunch<kScaleTensors, true> l;
-    *any = false;
     // from the last tensors to the first, as within a launch: the cache holds what was read last
     for (int32_t end = n; end > 0;) {
         int32_t begin = end, taken = 0;
@@ -449,7 +441,6 @@ int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStr
             TraceScope tr("grad_scale", s);
             hipLaunchKernelGGL(k_grad_scale, dim3(grid), dim3(kGradThreads), 0, s, l, k);
             if (launch_status() != MOE_OK) return MOE_EHIP;
-            *any = true;
         }
         end = begin;
     }
@@ -511,8 +502,8 @@ int moe_layer_norm_fwd(const moe_ln_desc *n, const void *x, const float *g, cons
         return MOE_EINVAL;
     const LnPlan p = ln_plan(n);
     const LnArgs a{x, g, b, y, stats, n->rows, ln_ldx(n), ln_ldy(n), n->H, n->eps};
-    const bool odd = !ln_even(n, x, a.ldx) || !ln_even(n, y, a.ldy);
-    const int64_t per_cu = p.wave ? 8 : std::max(1, 1024 / p.threads);
+    const bool odd = !ln_even(n, x, a.ldx) || !ln_even(n, y, a.ldy) || !all_aligned({g, b});
+    const int64_t per_cu = p.wave ? 8 : std::max(1, (p.chunks == 1 && n->x_type != MOE_TYPE_FP32 ? 2048 : 1024) / p.threads);
     const int grid = (int)std::min<int64_t>((n->rows + p.teams - 1) / p.teams, per_cu * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);
     return ln_typed(n, odd, [&](auto ti, auto to, auto is_odd) {
@@ -539,9 +530,10 @@ int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, cons
         const bool long_rows = n->H > kLnSumH;
         LnBwdArgs a{LnArgs{x, g, nullptr, nullptr, const_cast<float *>(stats), n->rows, ln_ldx(n), ln_ldy(n), n->H, n->eps}, dy, dres, dx,
                     dg ? static_cast<float *>(ws) : nullptr};
-        const bool odd = !ln_even(n, x, a.f.ldx) || !ln_even(n, dy, a.f.ldy) || !ln_even(n, dres, a.f.ldx) || !ln_even(n, dx, a.f.ldx);
+        const bool odd = !ln_even(n, x, a.f.ldx) || !ln_even(n, dy, a.f.ldy) || !ln_even(n, dres, a.f.ldx) || !ln_even(n, dx, a.f.ldx) ||
+                         !aligned16(g);
         const int grid = ln_groups(n);
-        const size_t lds = 256 + (p.wave ? 64 * (size_t)p.chunks * p.lanes : 0);
+        const size_t lds = 256 + (p.wave ? 64 * (size_t)p.lanes : 0);
         int r = ln_typed(n, odd, [&](auto ti, auto to, auto is_odd) {
             using TI = decltype(ti);
             using TO = decltype(to);
@@ -596,9 +588,14 @@ int moe_grad_clip(const moe_grad *t, int32_t n, int32_t kind, float scale, float
     GradScalars k{static_cast<double *>(ws), result, nullptr, 0, kind, scale, max_norm, eps};
     rc = launch_grad_sums(t, n, k, s);
     if (rc != MOE_OK) return rc;
-    bool any;
-    rc = launch_grad_scale(t, n, k, s, &any);
-    return rc != MOE_OK || any ? rc : launch_grad_result(k, s);
+    // one launch's slots are added by every workgroup of the second pass; more than that, once
+    const bool alone = k.nparts > kGradParts || k.nparts == 0;
+    if (alone) {
+        rc = launch_grad_result(k, s);
+        if (rc != MOE_OK) return rc;
+        k.coef = &result->coef;
+    }
+    return launch_grad_scale(t, n, k, s);
 }
 
 int moe_grad_scale(const moe_grad *t, int32_t n, const float *coef, float scale, void *stream) {
@@ -606,8 +603,7 @@ int moe_grad_scale(const moe_grad *t, int32_t n, const float *coef, float scale,
     if (rc != MOE_OK) return rc;
     if (!coef || !aligned4(coef) || scale != scale) return MOE_EINVAL;
     GradScalars k{nullptr, nullptr, coef, 0, MOE_NORM_L2, scale, 0.f, 0.f};
-    bool any;
-    return launch_grad_scale(t, n, k, static_cast<hipStream_t>(stream), &any);
+    return launch_grad_scale(t, n, k, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

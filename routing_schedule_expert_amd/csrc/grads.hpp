@@ -9,8 +9,8 @@
 // where NaN is above infinity.
 //
 // The tensors of a launch come as its arguments (their addresses may be others in the
-// next call).  They are cut into pieces of 16384 elements, a run of consecutive pieces
-// to a workgroup; loads are of whole aligned 16-byte words, the neighbours' elements
+// next call).  They are cut into pieces of 16384 elements, dealt to the workgroups in turn;
+// loads are of whole aligned 16-byte words, the neighbours' elements
 // in a tensor's first and last word left out.
 #pragma once
 
@@ -20,7 +20,7 @@ namespace moe {
 
 constexpr int kGradThreads = 512;
 constexpr int kGradPiece = 16384;   // elements
-constexpr int kGradParts = 2048;    // workgroups of the first pass, over all launches (and one more per launch)
+constexpr int kGradParts = 2048;    // workgroups of a launch of the first pass at most
 constexpr int kSumTensors = 176, kScaleTensors = 128;  // per launch: arguments below 4 KiB
 
 struct GradTensor {
@@ -55,30 +55,36 @@ struct GradVec {
     static __device__ __forceinline__ float get(const u32x4 &v, int i) { return T::up((uint16_t)(v[i >> 1] >> (16 * (i & 1)))); }
 };
 
+// MAX: the largest magnitude's bits, otherwise the sum of squares.
+template <bool MAX>
 struct GradSum {
     double s = 0.0;
     uint32_t m = 0;
-    __device__ __forceinline__ void add(float v, bool max_of) {
-        if (max_of)
+    __device__ __forceinline__ void add(float v) {
+        if constexpr (MAX)
             m = max(m, __float_as_uint(v) & 0x7fffffffu);
         else
             s = fma((double)v, (double)v, s);
     }
 };
+// What the arguments point at is global memory; the compiler, which sees a pointer
+// loaded from memory, cannot know.
+typedef __attribute__((address_space(1))) u32x4 global_u32x4;
+__device__ __forceinline__ const global_u32x4 *grad_words(const void *g) { return (const global_u32x4 *)((uintptr_t)g & ~(uintptr_t)15); }
 
 // Elements [e0, e1) of the tensor at g.
-template <class T>
-__device__ __forceinline__ void grad_sum_piece(const void *g, int64_t e0, int64_t e1, bool max_of, GradSum &acc) {
+template <class T, bool MAX>
+__device__ __forceinline__ void grad_sum_piece(const void *g, int64_t e0, int64_t e1, GradSum<MAX> &acc) {
     constexpr int N = GradVec<T>::N, ES = 16 / N;
     // word w holds elements w N - lead ... of the tensor
     const int lead = (int)(((uintptr_t)g & 15) / ES);
-    const u32x4 *p = reinterpret_cast<const u32x4 *>((uintptr_t)g & ~(uintptr_t)15);
+    const global_u32x4 *p = grad_words(g);
     const int64_t a = e0 + lead, b = e1 + lead;  // in the words' own count
     const int64_t w0 = a / N, w1 = (b + N - 1) / N;
     const int64_t in0 = (a + N - 1) / N, in1 = b / N;  // whole words
-    auto whole = [&](const u32x4 &v) {
+    auto whole = [&](u32x4 v) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc.add(GradVec<T>::get(v, i), max_of);
+        for (int i = 0; i < N; ++i) acc.add(GradVec<T>::get(v, i));
     };
     constexpr int U = 4;
     int64_t w = in0 + threadIdx.x;
@@ -95,14 +101,15 @@ __device__ __forceinline__ void grad_sum_piece(const void *g, int64_t e0, int64_
         const u32x4 v = p[k];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (k * N + i >= a && k * N + i < b) acc.add(GradVec<T>::get(v, i), max_of);
+            if (k * N + i >= a && k * N + i < b) acc.add(GradVec<T>::get(v, i));
     };
     if (threadIdx.x == 0 && w0 < in0) part(w0);
     if (threadIdx.x == 64 && in1 < w1 && (in1 > w0 || w0 >= in0)) part(in1);
 }
 
 // A workgroup's sum, on thread 0.
-__device__ __forceinline__ double grad_join(const GradSum &acc, bool max_of, double *lds) {
+template <bool MAX>
+__device__ __forceinline__ double grad_join(const GradSum<MAX> &acc, double *lds) {
     double s = acc.s;
     uint32_t m = acc.m;
     for (int o = 32; o >= 1; o >>= 1) {
@@ -110,30 +117,23 @@ __device__ __forceinline__ double grad_join(const GradSum &acc, bool max_of, dou
         m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
     }
     const int wave = threadIdx.x / 64, waves = blockDim.x / 64;
-    if ((threadIdx.x & 63) == 0) lds[wave] = max_of ? (double)__uint_as_float(m) : s;
+    if ((threadIdx.x & 63) == 0) lds[wave] = MAX ? (double)__uint_as_float(m) : s;
     __syncthreads();
     double r = lds[0];
     for (int w = 1; w < waves; ++w) {
         const double v = lds[w];
-        r = max_of ? (v > r || v != v ? v : r) : r + v;
+        r = MAX ? (v > r || v != v ? v : r) : r + v;
     }
     return r;
 }
 
+// f(tensor, type, from, to) of the workgroup's pieces: every gridDim.x-th.
 template <class L, class F>
 __device__ __forceinline__ void grad_pieces(const L &l, bool backwards, F &&f) {
-    const int64_t all = l.piece[l.count];
-    const int first = (int)(all * blockIdx.x / gridDim.x), last = (int)(all * (blockIdx.x + 1) / gridDim.x);
-    if (first >= last) return;
-    const int start = backwards ? last - 1 : first;
-    int lo = 0, hi = l.count;  // the tensor that holds piece `start`: the last with piece[t] <= start
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (l.piece[mid] <= start) lo = mid; else hi = mid;
-    }
-    int t = lo;
-    for (int i = 0; i < last - first; ++i) {
-        const int c = backwards ? last - 1 - i : first + i;
+    const int all = l.piece[l.count];
+    int t = backwards ? l.count - 1 : 0;
+    for (int i = blockIdx.x; i < all; i += gridDim.x) {
+        const int c = backwards ? all - 1 - i : i;
         if (backwards)
             while (l.piece[t] > c) --t;
         else
@@ -143,19 +143,18 @@ __device__ __forceinline__ void grad_pieces(const L &l, bool backwards, F &&f) {
     }
 }
 
-template <class L>
+template <bool MAX, class L>
 __device__ __forceinline__ void grad_sums_body(const L &l, const GradScalars &k, double *lds) {
-    GradSum acc;
-    const bool max_of = k.kind == MOE_NORM_MAX;
+    GradSum<MAX> acc;
     grad_pieces(l, false, [&](int t, int type, int64_t e0, int64_t e1) {
         if (type == MOE_TYPE_FP32)
-            grad_sum_piece<F32>(l.t[t].g, e0, e1, max_of, acc);
+            grad_sum_piece<F32>(l.t[t].g, e0, e1, acc);
         else if (type == MOE_TYPE_BF16)
-            grad_sum_piece<Bf16>(l.t[t].g, e0, e1, max_of, acc);
+            grad_sum_piece<Bf16>(l.t[t].g, e0, e1, acc);
         else
-            grad_sum_piece<Fp16>(l.t[t].g, e0, e1, max_of, acc);
+            grad_sum_piece<Fp16>(l.t[t].g, e0, e1, acc);
     });
-    const double s = grad_join(acc, max_of, lds);
+    const double s = grad_join(acc, lds);
     if (threadIdx.x == 0) k.parts[blockIdx.x] = s;
 }
 
@@ -192,10 +191,11 @@ template <class T>
 __device__ __forceinline__ void grad_scale_piece(const void *g, void *out, int64_t e0, int64_t e1, float f) {
     constexpr int N = GradVec<T>::N, ES = 16 / N;
     const int lead = (int)(((uintptr_t)g & 15) / ES);
-    const u32x4 *p = reinterpret_cast<const u32x4 *>((uintptr_t)g & ~(uintptr_t)15);
-    char *o = static_cast<char *>(out);
+    const global_u32x4 *p = grad_words(g);
+    typedef __attribute__((address_space(1))) char global_char;
+    global_char *o = (global_char *)out;
     const int64_t a = e0 + lead, b = e1 + lead, w0 = a / N, w1 = (b + N - 1) / N, in0 = (a + N - 1) / N, in1 = b / N;
-    auto scaled = [&](const u32x4 &v) {
+    auto scaled = [&](u32x4 v) {
         u32x4 r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -206,7 +206,12 @@ __device__ __forceinline__ void grad_scale_piece(const void *g, void *out, int64
         }
         return r;
     };
-    auto put = [&](int64_t w, const u32x4 &v) { __builtin_memcpy(o + (w * N - lead) * ES, &v, 16); };
+    // whole words of g are words of out where both start alike, and 16 bytes of any alignment otherwise
+    struct __attribute__((packed, aligned(2))) Loose {
+        u32x4 v;
+    };
+    typedef __attribute__((address_space(1))) Loose global_loose;
+    auto put = [&](int64_t w, u32x4 v) { ((global_loose *)(o + (w * N - lead) * ES))->v = v; };
     constexpr int U = 4;
     int64_t w = in0 + threadIdx.x;
     for (; w + (U - 1) * kGradThreads < in1; w += U * kGradThreads) {
@@ -223,9 +228,9 @@ __device__ __forceinline__ void grad_scale_piece(const void *g, void *out, int64
         for (int i = 0; i < N; ++i)
             if (k * N + i >= a && k * N + i < b) {
                 if constexpr (N == 4)
-                    reinterpret_cast<uint32_t *>(out)[k * N + i - lead] = v[i];
+                    ((__attribute__((address_space(1))) uint32_t *)o)[k * N + i - lead] = v[i];
                 else
-                    reinterpret_cast<uint16_t *>(out)[k * N + i - lead] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+                    ((__attribute__((address_space(1))) uint16_t *)o)[k * N + i - lead] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
             }
     };
     if (threadIdx.x == 0 && w0 < in0) part(w0);

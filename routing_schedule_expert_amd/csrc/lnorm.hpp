@@ -9,9 +9,10 @@
 // variance is that of the differences from the mean, a second sum in registers) and
 // written once.  A thread keeps the same columns for every row it takes, 8 at a time,
 // so gains and biases and the column sums of the gradient stay in its registers.
-// Rows up to 2048 elements are taken by a wave or a part of one (64, 32, 16 or 8
-// lanes: no barrier), longer ones by a workgroup.  The next row's loads are issued
-// before this row's sums.
+// Rows up to 512 elements are taken by a wave or a part of one (64, 32, 16 or 8
+// lanes: no barrier), longer ones by a workgroup.  Up to 8192 elements (one chunk a
+// thread) the loads of the next row (forward: of the two next) are in flight during
+// this row's sums; longer rows are loaded as they come, and gains and biases with them.
 //
 // Any row length and stride: where H or a stride is not a multiple of 8, or a pointer
 // not of 16 bytes, the last 8 columns of a row start at H - 8 and overlap those before
@@ -36,6 +37,8 @@ struct Chunk {
         else
             v = *reinterpret_cast<const u32x4 *>(p);
     }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int elem) { v = buffer_load16_nt(b, elem * 2); }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, int elem, const float (&o)[8]) { buffer_store16(b, elem * 2, pack8<T>(o)); }
     __device__ __forceinline__ void load_some(const char *p, int n) {
         v = u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -69,6 +72,14 @@ struct Chunk<F32> {
             v[0] = reinterpret_cast<const f32x4 *>(p)[0];
             v[1] = reinterpret_cast<const f32x4 *>(p)[1];
         }
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int elem) {
+        v[0] = __builtin_bit_cast(f32x4, buffer_load16_nt(b, elem * 4));
+        v[1] = __builtin_bit_cast(f32x4, buffer_load16_nt(b, elem * 4 + 16));
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, int elem, const float (&o)[8]) {
+        buffer_store16(b, elem * 4, __builtin_bit_cast(u32x4, f32x4{o[0], o[1], o[2], o[3]}));
+        buffer_store16(b, elem * 4 + 16, __builtin_bit_cast(u32x4, f32x4{o[4], o[5], o[6], o[7]}));
     }
     __device__ __forceinline__ void load_some(const char *p, int n) {
 #pragma unroll
@@ -146,23 +157,35 @@ struct TeamSum {
 };
 
 // A thread's columns: chunk i of CH starts at column at[i], of which the elements from
-// skip[i] on count (8: none).
-template <int CH, bool ODD>
+// skip[i] on count (8: none).  BUF: the row is the workgroup's and even, and a raw buffer, so that neither a
+// row past the last one nor a thread without columns needs a branch around its loads
+// and stores: with one, the compiler could not count which of them it waits for.
+template <int CH, bool ODD, bool BUF>
 struct Columns {
+    static_assert(!BUF || !ODD, "raw buffers are of whole chunks");
     int at[CH], skip[CH], H;
     __device__ __forceinline__ Columns(int t, int lanes, int H_) : H(H_) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = (i * lanes + t) * 8;
-            at[i] = max(0, min(c, H - 8));
+            at[i] = BUF ? c : max(0, min(c, H - 8));  // past a buffer's end: zeros
             skip[i] = c < H ? c - at[i] : 8;
         }
     }
     __device__ __forceinline__ bool in(int i) const { return skip[i] < 8; }
     // whether element e of chunk i counts; without ODD a chunk counts as a whole
     __device__ __forceinline__ bool counts(int i, int e) const { return ODD ? e >= skip[i] && e < H : in(i); }
+    // of the row that starts at element `elem` (none: nothing is loaded that counts)
     template <class C>
-    __device__ __forceinline__ void load(C (&c)[CH], const void *p, int64_t elem) const {
+    __device__ __forceinline__ void load(C (&c)[CH], const void *p, int64_t elem, bool some = true) const {
+        if constexpr (BUF) {
+            some = some && p;
+            const __amdgpu_buffer_rsrc_t b = raw_buffer(static_cast<const char *>(p) + (some ? elem * C::ES : 0), some ? (uint32_t)(H * C::ES) : 0u);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) c[i].load(b, at[i]);
+            return;
+        }
+        if (!some || !p) return;
         const char *q = static_cast<const char *>(p) + elem * C::ES;
         if (ODD && H < 8) {  // one chunk, which is the row
             c[0].load_some(q, in(0) ? H : 0);
@@ -175,6 +198,10 @@ struct Columns {
     }
     template <class C>
     __device__ __forceinline__ void store(int i, void *p, int64_t elem, const float (&v)[8]) const {
+        if constexpr (BUF) {
+            C::store(raw_buffer(static_cast<char *>(p) + elem * C::ES, (uint32_t)(H * C::ES)), at[i], v);
+            return;
+        }
         if (!in(i)) return;
         char *q = static_cast<char *>(p) + (elem + at[i]) * C::ES;
         if (ODD && H < 8)
@@ -182,45 +209,80 @@ struct Columns {
         else
             C::template store<ODD>(q, v);
     }
-    // fp32 values of the columns, `none` where p is null
-    __device__ __forceinline__ void vec(float (&v)[CH][8], const float *p, float none) const {
+    // fp32 values of chunk i's columns, `none` where p is null
+    __device__ __forceinline__ void vec(int i, float (&v)[8], const float *p, float none) const {
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = p && in(i) && at[i] + e < H ? p[at[i] + e] : none;
+        for (int e = 0; e < 8; ++e) v[e] = none;
+        if (!p) return;
+        Chunk<F32> c;
+        const char *q = reinterpret_cast<const char *>(p);
+        if constexpr (BUF)
+            c.load(raw_buffer(p, (uint32_t)H * 4), at[i]);
+        else if (ODD && H < 8)
+            c.load_some(q, in(i) ? H : 0);
+        else
+            c.template load<ODD>(q + (int64_t)at[i] * 4);
+        c.get(v);
     }
 };
-
-// Gains and biases stay in registers where those last.
-constexpr bool ln_keeps(int CH, bool WAVE) { return WAVE || CH <= 2; }
 
 template <class TI, class TO, int CH, bool WAVE, bool ODD>
 __device__ __forceinline__ void ln_fwd_body(const LnArgs &a, int lanes, float *lds) {
     const Team<WAVE> team(lanes);
-    const Columns<CH, ODD> col(team.t, team.lanes, a.H);
+    const Columns<CH, ODD, !WAVE && !ODD> col(team.t, team.lanes, a.H);
     TeamSum<WAVE, 1> sum1(lds, team.lanes);
     TeamSum<WAVE, 2> sum2(lds + 32, team.lanes);
     const float inv_h = 1.0f / (float)a.H;
     int64_t row = (int64_t)blockIdx.x * team.teams + team.team;
     const int64_t step = (int64_t)gridDim.x * team.teams;
     if (row >= a.rows) return;  // the whole team, and the whole workgroup where teams meet
-    Chunk<TI> c[CH];
-    col.load(c, a.x, row * a.ldx);
-    float g[CH][8], b[CH][8];
-    if (ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f), col.vec(b, a.b, 0.0f);
+    constexpr int AHEAD = CH == 1 ? 2 : 1;
+    constexpr bool BUF = !WAVE && !ODD;
+    Chunk<TI> c[AHEAD][CH];
+    auto fetch = [&](Chunk<TI> (&to)[CH], int64_t r) { col.load(to, a.x, r * a.ldx, r < a.rows); };
+    // the stores of a row: y's, and mean and 1 / std by its first thread
+    auto put = [&](int64_t r, bool some, int i, const float (&o)[8]) {
+        if (!BUF || some) col.template store<Chunk<TO>>(i, a.y, r * a.ldy, o);
+        else Chunk<TO>::store(raw_buffer(a.y, 0), 0, o);
+    };
+    auto put_stats = [&](int64_t r, bool some, float m, float rstd) {
+        if constexpr (BUF) {
+            some = some && a.stats;
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(m), __float_as_uint(rstd)}, raw_buffer(a.stats + (some ? 2 * r : 0), some ? 8u : 0u),
+                                                  team.t * 8, 0, 0);
+        } else if (some && a.stats && team.t == 0) {
+            reinterpret_cast<float2 *>(a.stats)[r] = make_float2(m, rstd);
+        }
+    };
+    // As many stores that go nowhere stand between the first rows' loads as between the
+    // later ones', so that the compiler may count on them: it waits for a row's loads and
+    // not for the next row's.
+#pragma unroll
+    for (int k = 0; k < (CH == 1 ? AHEAD : 0); ++k) {
+        fetch(c[k], row + k * step);
+        if constexpr (BUF) {
+            const float nothing[8] = {};
+            put_stats(0, false, 0.f, 0.f);
+            put(0, false, 0, nothing);
+        }
+    }
+    float g[8], b[8];
+    if (CH == 1) col.vec(0, g, a.g, 1.0f), col.vec(0, b, a.b, 0.0f);
     if constexpr (!WAVE) {
         norm_clear(lds, 96);
         __syncthreads();
     }
-    for (; row < a.rows; row += step) {
+    auto one = [&](Chunk<TI> (&cur)[CH]) {
         float x[CH][8], s[1] = {0.f}, s2[2] = {0.f, 0.f};
+        if (CH > 1) fetch(cur, row);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            c[i].get(x[i]);
+            cur[i].get(x[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[0] += col.counts(i, e) ? x[i][e] : 0.f;
         }
-        if (row + step < a.rows) col.load(c, a.x, (row + step) * a.ldx);
+        if (CH == 1) fetch(cur, row + AHEAD * step);
         sum1(s);
         const float m = s[0] * inv_h;
         // the differences' own mean is what the mean of the values lost to rounding
@@ -236,25 +298,33 @@ __device__ __forceinline__ void ln_fwd_body(const LnArgs &a, int lanes, float *l
         sum2(s2);
         const float dm = s2[0] * inv_h, var = fmaxf(fmaf(-dm, dm, s2[1] * inv_h), 0.f);
         const float rstd = __builtin_amdgcn_rsqf(s2[1] == s2[1] ? var + a.eps : s2[1]);  // fmaxf would drop a NaN
-        if (a.stats && team.t == 0) reinterpret_cast<float2 *>(a.stats)[row] = make_float2(m + dm, rstd);
-        if (!ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f), col.vec(b, a.b, 0.0f);
+        put_stats(row, true, m + dm, rstd);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+            if (CH > 1) col.vec(i, g, a.g, 1.0f), col.vec(i, b, a.b, 0.0f);
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = fmaf((x[i][e] - dm) * rstd, g[i][e], b[i][e]);
-            col.template store<Chunk<TO>>(i, a.y, row * a.ldy, o);
+            for (int e = 0; e < 8; ++e) o[e] = fmaf((x[i][e] - dm) * rstd, g[e], b[e]);
+            put(row, true, i, o);
+            if (CH > 1) __builtin_amdgcn_sched_barrier(0);  // one chunk's gains in registers at a time
         }
+        row += step;
+    };
+    // the buffers in turn, by name: copied, a load would be waited for
+    while (row < a.rows) {
+        one(c[0]);
+        if (AHEAD > 1 && row < a.rows) one(c[AHEAD - 1]);
     }
 }
 
-// SUMS: with the column sums of dg and db.  lds: 64 words for the rows' sums, then, for
-// the waves' column sums, 16 CH words for each lane of a team.
+// SUMS: with the column sums of dg and db (CH = 1).  lds: 64 words for the rows' sums,
+// then, for the waves' column sums, 16 words for each lane of a team.
 template <class TI, class TO, int CH, bool WAVE, bool ODD, bool SUMS>
 __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float *lds) {
+    static_assert(CH == 1 || !SUMS, "the column sums take one chunk's registers");
     const LnArgs &a = k.f;
     const Team<WAVE> team(lanes);
-    const Columns<CH, ODD> col(team.t, team.lanes, a.H);
+    const Columns<CH, ODD, !WAVE && !ODD> col(team.t, team.lanes, a.H);
     TeamSum<WAVE, 2> sum(lds, team.lanes);
     const float inv_h = 1.0f / (float)a.H;
     int64_t row = (int64_t)blockIdx.x * team.teams + team.team;
@@ -263,71 +333,83 @@ __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float
     Chunk<TO> cy[CH];
     float mean = 0.f, rstd = 0.f;
     auto fetch = [&](int64_t r) {
-        col.load(cx, a.x, r * a.ldx);
-        col.load(cy, k.dy, r * a.ldy);
-        if (k.dres) col.load(cr, k.dres, r * a.ldx);
-        const float2 st = reinterpret_cast<const float2 *>(a.stats)[r];
+        const bool some = r < a.rows;
+        col.load(cx, a.x, r * a.ldx, some);
+        col.load(cy, k.dy, r * a.ldy, some);
+        if (CH == 1) col.load(cr, k.dres, r * a.ldx, some);
+        const float2 st = reinterpret_cast<const float2 *>(a.stats)[min(r, a.rows - 1)];
         mean = st.x, rstd = st.y;
     };
-    if (row < a.rows) fetch(row);
-    float g[CH][8], dg[SUMS ? CH : 1][8], db[SUMS ? CH : 1][8];
-    if (ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f);
-    if constexpr (SUMS) {
+    if (CH == 1) fetch(row);
+    float g[8], dg[8], db[8];
+    if (CH == 1) col.vec(0, g, a.g, 1.0f);
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.f;
-    }
+    for (int e = 0; e < 8; ++e) dg[e] = db[e] = 0.f;
     if constexpr (!WAVE) {
         norm_clear(lds, 64);
         __syncthreads();
     }
     for (; row < a.rows; row += step) {
-        float xh[CH][8], t[CH][8], res[CH][8], s[2] = {0.f, 0.f};
+        if (CH > 1) fetch(row);
+        float xh[8], t[8], res[8], s[2] = {0.f, 0.f};
         const float m = mean, rs = rstd;
-        if (!ln_keeps(CH, WAVE)) col.vec(g, a.g, 1.0f);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            cx[i].get(xh[i]);
-            cy[i].get(t[i]);
-            if (k.dres) cr[i].get(res[i]);
+        // xh and dy g of a chunk; with more than one they are made again for the output
+        auto make = [&](int i) {
+            if (CH > 1) col.vec(i, g, a.g, 1.0f);
+            cx[i].get(xh);
+            cy[i].get(t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                xh[i][e] = (xh[i][e] - m) * rs;
+                xh[e] = (xh[e] - m) * rs;
                 if constexpr (SUMS) {
-                    dg[i][e] = fmaf(t[i][e], xh[i][e], dg[i][e]);
-                    db[i][e] += t[i][e];
+                    dg[e] = fmaf(t[e], xh[e], dg[e]);
+                    db[e] += t[e];
                 }
-                t[i][e] *= g[i][e];
-                if (col.counts(i, e)) {
-                    s[0] += t[i][e];
-                    s[1] = fmaf(t[i][e], xh[i][e], s[1]);
-                }
+                t[e] *= g[e];
             }
+        };
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            make(i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col.counts(i, e)) {
+                    s[0] += t[e];
+                    s[1] = fmaf(t[e], xh[e], s[1]);
+                }
+            if (CH > 1) __builtin_amdgcn_sched_barrier(0);
         }
-        if (row + step < a.rows) fetch(row + step);
+        if (CH == 1) {
+            cr[0].get(res);
+            fetch(row + step);
+        }
         sum(s);
         const float c0 = s[0] * inv_h, c1 = s[1] * inv_h;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+            if (CH > 1) {
+                make(i);
+                if (k.dres && col.in(i)) {
+                    cr[0].template load<ODD>(static_cast<const char *>(k.dres) + (row * a.ldx + col.at[i]) * Chunk<TI>::ES);
+                    cr[0].get(res);
+                }
+            }
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                o[e] = rs * (t[i][e] - fmaf(xh[i][e], c1, c0));
-                if (k.dres) o[e] += res[i][e];
+                o[e] = rs * (t[e] - fmaf(xh[e], c1, c0));
+                if (k.dres) o[e] += res[e];
             }
             col.template store<Chunk<TI>>(i, k.dx, row * a.ldx, o);
+            if (CH > 1) __builtin_amdgcn_sched_barrier(0);
         }
     }
     if constexpr (SUMS) {
         if (!k.part) return;
         float *out = k.part + (int64_t)blockIdx.x * 2 * a.H;
         auto store = [&]() {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                col.template store<Chunk<F32>>(i, out, 0, dg[i]);
-                col.template store<Chunk<F32>>(i, out, a.H, db[i]);
-            }
+            col.template store<Chunk<F32>>(0, out, 0, dg);
+            col.template store<Chunk<F32>>(0, out, a.H, db);
         };
         if constexpr (!WAVE) {
             store();
@@ -335,25 +417,21 @@ __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float
             // the teams of a wave, then its waves in turn
             for (int o = team.lanes; o < 64; o <<= 1)
 #pragma unroll
-                for (int i = 0; i < CH; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dg[i][e] += __shfl_xor(dg[i][e], o, 64);
-                        db[i][e] += __shfl_xor(db[i][e], o, 64);
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    dg[e] += __shfl_xor(dg[e], o, 64);
+                    db[e] += __shfl_xor(db[e], o, 64);
+                }
             const int waves = blockDim.x / 64, wave = threadIdx.x / 64;
             const bool mine = (int)(threadIdx.x & 63) < team.lanes;
             float *p = lds + 64 + team.t;
             for (int w = 0; w < waves; ++w) {
                 if (wave == w && mine) {
 #pragma unroll
-                    for (int i = 0; i < CH; ++i)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float *q = p + (i * 16 + e) * team.lanes, *r = q + 8 * team.lanes;
-                            if (w) dg[i][e] += *q, db[i][e] += *r;
-                            if (w + 1 < waves) *q = dg[i][e], *r = db[i][e];
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        float *q = p + e * team.lanes, *r = q + 8 * team.lanes;
+                        if (w) dg[e] += *q, db[e] += *r;
+                        if (w + 1 < waves) *q = dg[e], *r = db[e];
+                    }
                     if (w + 1 == waves) store();
                 }
                 __syncthreads();
@@ -368,7 +446,7 @@ template <class TI, class TO, bool ODD>
 __device__ __forceinline__ void ln_columns_body(const LnBwdArgs &k, float *lds) {
     const LnArgs &a = k.f;
     const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
-    const Columns<1, ODD> col(blockIdx.x * 64 + lane, 0, a.H);
+    const Columns<1, ODD, false> col(blockIdx.x * 64 + lane, 0, a.H);
     float dg[8], db[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[e] = db[e] = 0.f;
