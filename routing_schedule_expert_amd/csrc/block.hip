@@ -1,7 +1,7 @@
 // C-ABI entry points and kernels of a dense block's operators (gfx950): the gated
 // feed-forward block, layer norm, and the clipping of gradients.  Their arguments and
 // errors are documented in include/moe.h; the device code lives in dense.hpp, ffn.hpp,
-// lnorm.hpp and grads.hpp.
+// skinny.hpp, lnorm.hpp and grads.hpp.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -10,6 +10,7 @@
 #include "grads.hpp"
 #include "host.hpp"
 #include "lnorm.hpp"
+#include "skinny.hpp"
 
 using namespace moe;
 
@@ -35,6 +36,11 @@ __global__ __launch_bounds__(kDenseThreads, 1) void k_wgrads(DenseArgs g1, MatOu
         dense_body<T, MI, NI, true, true, false, NS>(g1, o1, block_lds_address(), b, blocks1);
     else
         dense_body<T, MI, NI, true, true, false, NS>(g2, o2, block_lds_address(), b - blocks1, gridDim.x - blocks1);
+}
+
+template <class T, int NT, int NW, bool GLU>
+__global__ __launch_bounds__(64 * NW, 1) void k_skinny(SkinnyArgs g) {
+    skinny_body<T, NT, NW, GLU>(g, block_lds_address());
 }
 
 template <bool GLU, class Out>
@@ -180,6 +186,10 @@ int ffn_check(const moe_ffn_desc *n) {
     return MOE_OK;
 }
 
+// A few rows go by the weights' stream.
+constexpr int kSkinnyRows = 64;
+bool ffn_skinny(const moe_ffn_desc *n) { return n->rows <= kSkinnyRows; }
+
 struct FfnPlans {
     DensePlan up, down;          // forward
     DensePlan act, dx, dw1, dw2;  // backward
@@ -213,16 +223,36 @@ int64_t ffn_ws_bytes(const moe_ffn_desc *n, bool bwd) {
     if (n->rows == 0) return 0;
     const FfnPlans p = ffn_plans(n);
     const int64_t R = n->rows, H = n->H, I = n->I;
-    if (!bwd) return std::max(dense_part_bytes(p.up, R, I, true), dense_part_bytes(p.down, R, H, false));
+    if (!bwd) return ffn_skinny(n) ? 0 : std::max(dense_part_bytes(p.up, R, I, true), dense_part_bytes(p.down, R, H, false));
     const int64_t dw = dense_part_bytes(p.dw1, 2 * I, H, false) + dense_part_bytes(p.dw2, H, I, false);
     return ffn_bwd_base(n) + std::max(dw, std::max(dense_part_bytes(p.act, R, I, false), dense_part_bytes(p.dx, R, H, false)));
+}
+
+template <class T, bool GLU>
+int launch_skinny(const SkinnyArgs &g, hipStream_t s, const char *name) {
+    const int units = up_to(g.N, GLU ? 8 : 16);
+    // 8 waves where the workgroups are no more than the CUs, 4 where two can share one
+    const bool wide = units <= device_cus() && g.M <= 16;
+    const int waves = wide ? 8 : 4, nt = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
+    TraceScope tr(name, s);
+    auto *fn = wide      ? k_skinny<T, 1, 8, GLU>
+               : nt == 1 ? k_skinny<T, 1, 4, GLU>
+               : nt == 2 ? k_skinny<T, 2, 4, GLU>
+                         : k_skinny<T, 4, 4, GLU>;
+    hipLaunchKernelGGL(fn, dim3(units), dim3(64 * waves), skinny_lds(nt, waves), s, g);
+    return launch_status();
 }
 
 template <class T>
 int ffn_fwd(const moe_ffn_desc *n, const uint16_t *X, const uint16_t *W13, const uint16_t *W2, uint16_t *HU, uint16_t *A,
             uint16_t *out, void *ws, hipStream_t s) {
-    const FfnPlans p = ffn_plans(n);
     const int R = (int)n->rows, H = n->H, I = n->I;
+    if (ffn_skinny(n)) {
+        const int rc = launch_skinny<T, true>(SkinnyArgs{X, W13, ffn_ldx(n), H, R, I, H, A, I, HU, n->act}, s, "ffn_up");
+        if (rc != MOE_OK) return rc;
+        return launch_skinny<T, false>(SkinnyArgs{A, W2, I, I, R, H, I, out, ffn_ldo(n), nullptr, 0}, s, "ffn_down");
+    }
+    const FfnPlans p = ffn_plans(n);
     const DenseArgs up = dense_args(p.up, X, ffn_ldx(n), W13, H, R, I, H, ws);
     int rc = launch_dense<T, false, false, true>(p.up, up, GluOut<T>{HU, A, I, n->act}, s, "ffn_up");
     if (rc != MOE_OK) return rc;

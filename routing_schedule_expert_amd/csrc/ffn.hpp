@@ -55,6 +55,13 @@ __device__ __forceinline__ void activation(int kind, const float (&x)[8], float 
     }
 }
 
+__device__ __forceinline__ float activation1(int kind, float h) {
+    const float x[8] = {h, h, h, h, h, h, h, h};
+    float v[8], none[8];
+    activation<false>(kind, x, v, none);
+    return v[0];
+}
+
 // One product: D[M][N] = A B^T over K.  For the gate / up product N counts the columns
 // of a (I), B has 2 N rows.
 struct DenseArgs {

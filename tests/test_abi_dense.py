@@ -56,7 +56,7 @@ def test_ffn_refusals():
         assert fwd(ffn(), **{k: None}) == EINVAL, k
     for k in names:
         assert fwd(ffn(), **{k: BAD}) == EINVAL, k
-    small = ffn(rows=1, H=2048, I=8)  # one tile: cut along K
+    small = ffn(rows=70, H=2048, I=8)  # few tiles: cut along K
     need = ops.gated_ffn_workspace_bytes(small)
     assert need > 0 and fwd(small, need - 1) == ENOSPC and fwd(small, ws=None) == EINVAL
     for n, code in ((ffn(H=260), EUNSUP), (ffn(I=12), EUNSUP), (ffn(act=9), EINVAL), (ffn(ldx=12), EINVAL), (ffn(ldx=268), EUNSUP),
