@@ -23,19 +23,24 @@ namespace {
 extern __shared__ char block_lds[];
 __device__ __forceinline__ uint32_t block_lds_address() { return (uint32_t)(uintptr_t)(lds_char *)block_lds; }
 
-template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int NS, class Out>
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int SLOTS, class Out>
 __global__ __launch_bounds__(kDenseThreads, 1) void k_dense(DenseArgs g, Out out) {
-    dense_body<T, MI, NI, AT, BT, GLU, NS>(g, out, block_lds_address(), blockIdx.x, gridDim.x);
+    dense_body<T, MI, NI, AT, BT, GLU, SLOTS>(g, out, block_lds_address(), blockIdx.x, gridDim.x);
 }
 
-// Both weight gradients in one launch.
-template <class T, int MI, int NI, int NS>
-__global__ __launch_bounds__(kDenseThreads, 1) void k_wgrads(DenseArgs g1, MatOut<T> o1, int blocks1, DenseArgs g2, MatOut<T> o2) {
-    const int b = blockIdx.x;
-    if (b < blocks1)
-        dense_body<T, MI, NI, true, true, false, NS>(g1, o1, block_lds_address(), b, blocks1);
+// The gradients of both weights and of the input in one launch: none needs another, and
+// shorter tiles (of fewer steps along K), which come last, fill the CUs that the last
+// round of the longer ones leaves.
+template <class T, int MI, int NI, int SLOTS>
+__global__ __launch_bounds__(kDenseThreads, 1) void k_grads(DenseArgs g1, MatOut<T> o1, int blocks1, DenseArgs g2, MatOut<T> o2, int blocks2,
+                                                            DenseArgs g3, MatOut<T> o3, int blocks3, int third_first) {
+    const int b = blockIdx.x - (third_first ? blocks3 : 0), c = b - blocks1, d = third_first ? (int)blockIdx.x : c - blocks2;
+    if (d >= 0 && d < blocks3)
+        dense_body<T, MI, NI, false, true, false, SLOTS>(g3, o3, block_lds_address(), d, blocks3);
+    else if (b < blocks1)
+        dense_body<T, MI, NI, true, true, false, SLOTS>(g1, o1, block_lds_address(), b, blocks1);
     else
-        dense_body<T, MI, NI, true, true, false, NS>(g2, o2, block_lds_address(), b - blocks1, gridDim.x - blocks1);
+        dense_body<T, MI, NI, true, true, false, SLOTS>(g2, o2, block_lds_address(), c, blocks2);
 }
 
 template <class T, int NT, int NW, bool GLU>
@@ -110,65 +115,115 @@ int launch_zero(float *p, int64_t words, hipStream_t s) {
 // Gated feed-forward block.
 // ---------------------------------------------------------------------------
 
-// A product's tile and its cut along K.
-enum DenseTile { kTileL = 0, kTileS = 1, kTileX = 2 };
-struct DensePlan {
-    DenseTile tile;
-    int mt, nt, splits, steps;
-    int blocks() const { return mt * nt * splits; }
-};
-
 int up_to(int64_t n, int d) { return (int)((n + d - 1) / d); }
 
-DensePlan dense_plan(int M, int N, int K, bool glu) {
-    static const int bm[] = {256, 128, 64}, bn[] = {256, 128, 128};
-    DensePlan p{};
-    const int steps = std::max(1, up_to(K, kDenseK));
-    for (int t = kTileL; t <= kTileX; ++t) {
-        p.tile = (DenseTile)t;
-        p.mt = up_to(M, bm[t]);
-        p.nt = up_to(N, glu ? bn[t] / 2 : bn[t]);
-        if ((int64_t)p.mt * p.nt >= 192) break;
+// The tiles: 64 MI x 64 NI outputs, a ring of SLOTS operand tiles.  The 128 x 128 tile has
+// a short ring, so that two workgroups share a CU, and a long one for when there is one
+// at most.
+enum DenseTile { kTileL, kTileS2, kTileS, kTileX, kTiles };
+struct DenseShape {
+    int mi, ni, slots, per_cu;
+    float step, ends;  // us: a step of 64 k with every CU at work, and what a tile takes besides
+};
+constexpr DenseShape kShape[kTiles] = {{4, 4, 5, 1, 1.4f, 9.f}, {2, 2, 5, 2, 0.85f, 6.f}, {2, 2, 9, 1, 0.5f, 6.f}, {1, 2, 9, 1, 0.35f, 5.f}};
+
+// A product: its sizes (GLU: N of a, B has 2 N rows), its tiles and its cut along K.
+struct DensePlan {
+    int M, N, K;
+    bool glu;
+    int mt, nt, splits, steps;
+    int blocks() const { return mt * nt * splits; }
+    int64_t part_bytes() const { return splits > 1 ? align256((int64_t)splits * M * N * (glu ? 2 : 1) * 4) : 0; }
+    int all_steps() const { return std::max(1, up_to(K, kDenseK)); }
+};
+DensePlan dense_product(int M, int N, int K, bool glu = false) { return DensePlan{M, N, K, glu, 0, 0, 1, 0}; }
+
+// The tile for the products of one launch, and their cuts along K.  The time of each
+// choice is estimated from a step's and a tile's measured times: all tiles at once where the CUs
+// hold them, otherwise their sum over the CUs, and the largest's last round.  A cut costs the
+// second pass (kJoin and the parts' bytes).
+DenseTile dense_plan(DensePlan *p, int n) {
+    constexpr float kJoin = 5.f, kPerMiB = 0.4f;
+    constexpr int kCus = 256;  // of every gfx950; also where a workspace is sized without one
+    DenseTile best = kTileL;
+    float least = 1e30f;
+    DensePlan chosen[3];
+    for (int t = 0; t < kTiles; ++t) {
+        const DenseShape &k = kShape[t];
+        for (int cut = 1; cut <= 16; cut *= 2) {
+            DensePlan q[3];
+            float sum = 0.f, most = 0.f, join = 0.f;
+            int blocks = 0;
+            bool useful = cut == 1;
+            for (int i = 0; i < n; ++i) {
+                q[i] = p[i];
+                q[i].mt = up_to(q[i].M, 64 * k.mi);
+                q[i].nt = up_to(q[i].N, (q[i].glu ? 32 : 64) * k.ni);
+                const int all = q[i].all_steps();
+                q[i].steps = std::max(4, up_to(all, cut));
+                q[i].splits = up_to(all, q[i].steps);
+                if (q[i].splits == 1) q[i].steps = all;
+                useful |= q[i].splits > 1;
+                const float one = q[i].steps * k.step + k.ends;
+                sum += one * q[i].blocks();
+                most = std::max(most, one);
+                blocks += q[i].blocks();
+                if (q[i].splits > 1) join += kJoin + kPerMiB * (float)(q[i].part_bytes() >> 20);
+            }
+            if (!useful || (cut > 1 && blocks > kCus * k.per_cu)) break;
+            const int room = kCus * k.per_cu;
+            const float time = (blocks <= room ? most : std::max(most, sum / room + 0.3f * most)) + join;
+            if (time < least) {
+                least = time;
+                best = (DenseTile)t;
+                std::copy(q, q + n, chosen);
+            }
+        }
     }
-    p.splits = 1;
-    const int tiles = p.mt * p.nt;
-    if (tiles < 128) p.splits = std::max(1, std::min(std::min(steps / 4, 256 / tiles), 16));
-    p.steps = up_to(steps, p.splits);
-    p.splits = up_to(steps, p.steps);
-    return p;
-}
-int64_t dense_part_bytes(const DensePlan &p, int64_t M, int64_t N, bool glu) {
-    return p.splits > 1 ? align256(p.splits * M * N * (glu ? 2 : 1) * 4) : 0;
+    std::copy(chosen, chosen + n, p);
+    return best;
 }
 
-DenseArgs dense_args(const DensePlan &p, const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int M, int N, int K,
-                     void *part) {
-    return DenseArgs{A, B, lda, ldb, M, N, K, p.mt, p.nt, p.splits, p.steps, static_cast<float *>(part)};
+DenseArgs dense_args(const DensePlan &p, const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, void *part) {
+    return DenseArgs{A, B, lda, ldb, p.M, p.N, p.K, p.mt, p.nt, p.splits, p.steps, static_cast<float *>(part)};
 }
 
-constexpr int kStagesL = 2, kStagesS = 4, kStagesX = 4;
-size_t dense_lds(DenseTile t) {
-    return t == kTileL   ? kStagesL * dense_stage_bytes(4, 4)
-           : t == kTileS ? kStagesS * dense_stage_bytes(2, 2)
-                         : kStagesX * dense_stage_bytes(1, 2);
-}
+size_t dense_lds(DenseTile t) { return dense_lds_bytes(kShape[t].mi, kShape[t].ni, kShape[t].slots); }
 
 template <class T, bool AT, bool BT, bool GLU, class Out>
-int launch_dense(const DensePlan &p, const DenseArgs &g, const Out &out, hipStream_t s, const char *name) {
-    {
-        TraceScope tr(name, s);
-        auto *fn = p.tile == kTileL   ? k_dense<T, 4, 4, AT, BT, GLU, kStagesL, Out>
-                   : p.tile == kTileS ? k_dense<T, 2, 2, AT, BT, GLU, kStagesS, Out>
-                                      : k_dense<T, 1, 2, AT, BT, GLU, kStagesX, Out>;
-        hipLaunchKernelGGL(fn, dim3(p.blocks()), dim3(kDenseThreads), dense_lds(p.tile), s, g, out);
-    }
-    int rc = launch_status();
-    if (rc != MOE_OK || p.splits == 1) return rc;
+auto *dense_kernel(DenseTile t) {
+    return t == kTileL    ? k_dense<T, 4, 4, AT, BT, GLU, kShape[kTileL].slots, Out>
+           : t == kTileS2 ? k_dense<T, 2, 2, AT, BT, GLU, kShape[kTileS2].slots, Out>
+           : t == kTileS  ? k_dense<T, 2, 2, AT, BT, GLU, kShape[kTileS].slots, Out>
+                          : k_dense<T, 1, 2, AT, BT, GLU, kShape[kTileX].slots, Out>;
+}
+template <class T>
+auto *grads_kernel(DenseTile t) {
+    return t == kTileL    ? k_grads<T, 4, 4, kShape[kTileL].slots>
+           : t == kTileS2 ? k_grads<T, 2, 2, kShape[kTileS2].slots>
+           : t == kTileS  ? k_grads<T, 2, 2, kShape[kTileS].slots>
+                          : k_grads<T, 1, 2, kShape[kTileX].slots>;
+}
+
+template <bool GLU, class Out>
+int launch_join(const DensePlan &p, const DenseArgs &g, const Out &out, hipStream_t s) {
+    if (p.splits == 1) return MOE_OK;
     TraceScope tr("dense_join", s);
     auto *join = k_dense_join<GLU, Out>;
     const int64_t n = (int64_t)g.M * (g.N / 8);
     hipLaunchKernelGGL(join, dim3((int)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, s, g, out);
     return launch_status();
+}
+
+template <class T, bool AT, bool BT, bool GLU, class Out>
+int launch_dense(DenseTile t, const DensePlan &p, const DenseArgs &g, const Out &out, hipStream_t s, const char *name) {
+    {
+        TraceScope tr(name, s);
+        auto *fn = dense_kernel<T, AT, BT, GLU, Out>(t);
+        hipLaunchKernelGGL(fn, dim3(p.blocks()), dim3(kDenseThreads), dense_lds(t), s, g, out);
+    }
+    const int rc = launch_status();
+    return rc != MOE_OK ? rc : launch_join<GLU>(p, g, out, s);
 }
 
 int64_t ffn_ldx(const moe_ffn_desc *n) { return n->ldx ? n->ldx : n->H; }
@@ -190,42 +245,31 @@ int ffn_check(const moe_ffn_desc *n) {
 constexpr int kSkinnyRows = 64;
 bool ffn_skinny(const moe_ffn_desc *n) { return n->rows <= kSkinnyRows; }
 
-struct FfnPlans {
-    DensePlan up, down;          // forward
-    DensePlan act, dx, dw1, dw2;  // backward
-};
-FfnPlans ffn_plans(const moe_ffn_desc *n) {
-    const int R = (int)n->rows, H = n->H, I = n->I;
-    FfnPlans p;
-    p.up = dense_plan(R, I, H, true);
-    p.down = dense_plan(R, H, I, false);
-    p.act = dense_plan(R, I, H, false);
-    p.dx = dense_plan(R, H, 2 * I, false);
-    p.dw1 = dense_plan(2 * I, H, R, false);
-    p.dw2 = dense_plan(H, I, R, false);
-    // the two weight gradients share a launch and its tile
-    if (p.dw1.tile != p.dw2.tile) {
-        DensePlan &o = p.dw1.tile < p.dw2.tile ? p.dw2 : p.dw1;
-        const bool first = &o == &p.dw1;
-        const DenseTile t = first ? p.dw2.tile : p.dw1.tile;
-        static const int bm[] = {256, 128, 64}, bn[] = {256, 128, 128};
-        o.tile = t;
-        o.mt = up_to(first ? 2 * I : H, bm[t]);
-        o.nt = up_to(first ? H : I, bn[t]);
-    }
-    return p;
-}
-
-// dHU, a (where it was not kept), then the parts of one product at a time (both weight
-// gradients': one after the other)
+// dHU and a (where it was not kept), then the parts of a launch's products
 int64_t ffn_bwd_base(const moe_ffn_desc *n) { return align256(n->rows * 4 * n->I) + align256(n->rows * 2 * n->I); }
+
+// Forward: gate / up, down.  Backward: activations; then the gradients of W13, W2 and X in one launch.
+struct FfnFwdPlan {
+    DensePlan up, down;
+    DenseTile tup, tdown;
+    explicit FfnFwdPlan(const moe_ffn_desc *n)
+        : up(dense_product((int)n->rows, n->I, n->H, true)), down(dense_product((int)n->rows, n->H, n->I)), tup(dense_plan(&up, 1)),
+          tdown(dense_plan(&down, 1)) {}
+    int64_t ws_bytes() const { return std::max(up.part_bytes(), down.part_bytes()); }
+};
+struct FfnBwdPlan {
+    DensePlan act, g[3];
+    DenseTile tact, tg;
+    explicit FfnBwdPlan(const moe_ffn_desc *n)
+        : act(dense_product((int)n->rows, n->I, n->H)),
+          g{dense_product(2 * n->I, n->H, (int)n->rows), dense_product(n->H, n->I, (int)n->rows), dense_product((int)n->rows, n->H, 2 * n->I)},
+          tact(dense_plan(&act, 1)), tg(dense_plan(g, 3)) {}
+    int64_t ws_bytes() const { return std::max(act.part_bytes(), g[0].part_bytes() + g[1].part_bytes() + g[2].part_bytes()); }
+};
 int64_t ffn_ws_bytes(const moe_ffn_desc *n, bool bwd) {
     if (n->rows == 0) return 0;
-    const FfnPlans p = ffn_plans(n);
-    const int64_t R = n->rows, H = n->H, I = n->I;
-    if (!bwd) return ffn_skinny(n) ? 0 : std::max(dense_part_bytes(p.up, R, I, true), dense_part_bytes(p.down, R, H, false));
-    const int64_t dw = dense_part_bytes(p.dw1, 2 * I, H, false) + dense_part_bytes(p.dw2, H, I, false);
-    return ffn_bwd_base(n) + std::max(dw, std::max(dense_part_bytes(p.act, R, I, false), dense_part_bytes(p.dx, R, H, false)));
+    if (bwd) return ffn_bwd_base(n) + FfnBwdPlan(n).ws_bytes();
+    return ffn_skinny(n) ? 0 : FfnFwdPlan(n).ws_bytes();
 }
 
 template <class T, bool GLU>
@@ -252,58 +296,41 @@ int ffn_fwd(const moe_ffn_desc *n, const uint16_t *X, const uint16_t *W13, const
         if (rc != MOE_OK) return rc;
         return launch_skinny<T, false>(SkinnyArgs{A, W2, I, I, R, H, I, out, ffn_ldo(n), nullptr, 0}, s, "ffn_down");
     }
-    const FfnPlans p = ffn_plans(n);
-    const DenseArgs up = dense_args(p.up, X, ffn_ldx(n), W13, H, R, I, H, ws);
-    int rc = launch_dense<T, false, false, true>(p.up, up, GluOut<T>{HU, A, I, n->act}, s, "ffn_up");
+    const FfnFwdPlan p(n);
+    const DenseArgs up = dense_args(p.up, X, ffn_ldx(n), W13, H, ws);
+    const int rc = launch_dense<T, false, false, true>(p.tup, p.up, up, GluOut<T>{HU, A, I, n->act}, s, "ffn_up");
     if (rc != MOE_OK) return rc;
-    const DenseArgs down = dense_args(p.down, A, I, W2, I, R, H, I, ws);
-    return launch_dense<T, false, false, false>(p.down, down, MatOut<T>{out, ffn_ldo(n), 0, 0}, s, "ffn_down");
-}
-
-template <class T>
-int launch_wgrads(const FfnPlans &p, const DenseArgs &g1, const MatOut<T> &o1, const DenseArgs &g2, const MatOut<T> &o2, hipStream_t s) {
-    const int b1 = o1.p ? p.dw1.blocks() : 0, b2 = o2.p ? p.dw2.blocks() : 0;
-    const DenseTile t = p.dw1.tile;
-    {
-        TraceScope tr("ffn_wgrads", s);
-        auto *fn = t == kTileL   ? k_wgrads<T, 4, 4, kStagesL>
-                   : t == kTileS ? k_wgrads<T, 2, 2, kStagesS>
-                                 : k_wgrads<T, 1, 2, kStagesX>;
-        hipLaunchKernelGGL(fn, dim3(b1 + b2), dim3(kDenseThreads), dense_lds(t), s, g1, o1, b1, g2, o2);
-    }
-    auto join = [&](const DensePlan &q, const DenseArgs &g, const MatOut<T> &o) {
-        if (!o.p || q.splits == 1) return launch_status();
-        TraceScope tr("dense_join", s);
-        auto *fn = k_dense_join<false, MatOut<T>>;
-        const int64_t m = (int64_t)g.M * (g.N / 8);
-        hipLaunchKernelGGL(fn, dim3((int)std::min<int64_t>((m + 255) / 256, 2048)), dim3(256), 0, s, g, o);
-        return launch_status();
-    };
-    const int rc = join(p.dw1, g1, o1);
-    return rc != MOE_OK ? rc : join(p.dw2, g2, o2);
+    const DenseArgs down = dense_args(p.down, A, I, W2, I, ws);
+    return launch_dense<T, false, false, false>(p.tdown, p.down, down, MatOut<T>{out, ffn_ldo(n), 0, 0}, s, "ffn_down");
 }
 
 template <class T>
 int ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_t *X, const uint16_t *HU, const uint16_t *A, const uint16_t *W13,
             const uint16_t *W2, uint16_t *dX, void *dW13, void *dW2, int f32, int add, void *ws, hipStream_t s) {
-    const FfnPlans p = ffn_plans(n);
-    const int R = (int)n->rows, H = n->H, I = n->I;
+    FfnBwdPlan p(n);
+    const int H = n->H, I = n->I;
     const int64_t ldx = ffn_ldx(n), ldo = ffn_ldo(n);
     char *w = static_cast<char *>(ws);
     uint16_t *dHU = reinterpret_cast<uint16_t *>(w), *a = reinterpret_cast<uint16_t *>(w + align256(n->rows * 4 * n->I));
     char *part = w + ffn_bwd_base(n);
-    const DenseArgs act = dense_args(p.act, dOut, ldo, W2, I, R, I, H, part);
-    int rc = launch_dense<T, false, true, false>(p.act, act, GluBwdOut<T>{HU, dHU, A || !dW2 ? nullptr : a, I, n->act}, s, "ffn_bwd_act");
+    const DenseArgs act = dense_args(p.act, dOut, ldo, W2, I, part);
+    int rc = launch_dense<T, false, true, false>(p.tact, p.act, act, GluBwdOut<T>{HU, dHU, A || !dW2 ? nullptr : a, I, n->act}, s, "ffn_bwd_act");
     if (rc != MOE_OK) return rc;
-    if (dX) {
-        const DenseArgs dx = dense_args(p.dx, dHU, 2 * I, W13, H, R, H, 2 * I, part);
-        rc = launch_dense<T, false, true, false>(p.dx, dx, MatOut<T>{dX, ldx, 0, 0}, s, "ffn_bwd_dx");
-        if (rc != MOE_OK) return rc;
+    const DenseArgs g[3] = {dense_args(p.g[0], dHU, 2 * I, X, ldx, part), dense_args(p.g[1], dOut, ldo, A ? A : a, I, part + p.g[0].part_bytes()),
+                            dense_args(p.g[2], dHU, 2 * I, W13, H, part + p.g[0].part_bytes() + p.g[1].part_bytes())};
+    const MatOut<T> o[3] = {{dW13, H, f32, add}, {dW2, I, f32, add}, {dX, ldx, 0, 0}};
+    int blocks[3];
+    for (int i = 0; i < 3; ++i) blocks[i] = o[i].p ? p.g[i].blocks() : 0;
+    {
+        TraceScope tr("ffn_bwd_grads", s);
+        auto *fn = grads_kernel<T>(p.tg);
+        hipLaunchKernelGGL(fn, dim3(blocks[0] + blocks[1] + blocks[2]), dim3(kDenseThreads), dense_lds(p.tg), s, g[0], o[0], blocks[0], g[1], o[1],
+                           blocks[1], g[2], o[2], blocks[2], (int)(p.g[2].steps > p.g[0].steps));
     }
-    if (!dW13 && !dW2) return MOE_OK;
-    const DenseArgs dw1 = dense_args(p.dw1, dHU, 2 * I, X, ldx, 2 * I, H, R, part);
-    const DenseArgs dw2 = dense_args(p.dw2, dOut, ldo, A ? A : a, I, H, I, R, part + dense_part_bytes(p.dw1, 2 * I, H, false));
-    return launch_wgrads<T>(p, dw1, MatOut<T>{dW13, H, f32, add}, dw2, MatOut<T>{dW2, I, f32, add}, s);
+    rc = launch_status();
+    for (int i = 0; i < 3 && rc == MOE_OK; ++i)
+        if (o[i].p) rc = launch_join<false>(p.g[i], g[i], o[i], s);
+    return rc;
 }
 
 // ---------------------------------------------------------------------------

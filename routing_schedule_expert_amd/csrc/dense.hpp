@@ -226,22 +226,32 @@ struct LoadOf<true, R> {
     using type = LoadMn<R>;
 };
 
-constexpr int dense_stage_bytes(int MI, int NI) { return (MI + NI) * 64 * kDenseK * 2; }
-
 template <int N>
 __device__ __forceinline__ void wait_loads_and_meet() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// LDS of a tile: a ring of SLOTS operand tiles, an odd number, A and B in turn.
+constexpr int dense_slot_bytes(int MI, int NI) { return (MI > NI ? MI : NI) * 64 * kDenseK * 2; }
+constexpr int dense_lds_bytes(int MI, int NI, int SLOTS) { return SLOTS * dense_slot_bytes(MI, NI); }
+
 // The K loop over steps [k0, k1) (of the tile's K; `left`: k in the step k_last, the
 // operand's last).  GLU: B's blocks are dealt to the waves so that a wave has NI / 2
 // blocks of the tile's first half and the same of its second.  On return every load
 // has landed and the workgroup has met.
-template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int NS, class LA, class LB>
+//
+// The ring holds A and B of the step in hand and of the AHEAD - 1 that follow, and A of
+// one more.  Past a step's barrier its two slots are free: B of step + AHEAD goes to A's,
+// A of the step after to B's.  The loads are spread: a CU takes one of 1 KiB in 16
+// cycles, so the 64 of a 256 x 256 step need half of its MFMAs' time, and issued in the
+// quarter of it past the barrier they held up the waves' MFMAs (2,923 cycles a step
+// with two slots of both operands, 2,661 with no memory behind them, 2,139 without loads).
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int SLOTS, class LA, class LB>
 __device__ __forceinline__ void dense_loop(LA &la, LB &lb, int k0, int k1, int k_last, int left, uint32_t lds, int wave, int lane,
                                            DenseAcc<MI, NI> &acc) {
-    constexpr int A_BYTES = MI * 64 * kDenseK * 2, STAGE = dense_stage_bytes(MI, NI), ND = LA::BL + LB::BL;
+    static_assert(SLOTS % 2 == 1 && SLOTS >= 5, "A and B in turn");
+    constexpr int SLOT = dense_slot_bytes(MI, NI), AHEAD = SLOTS / 2, NA = LA::BL, NB = LB::BL;
     constexpr int NQ = MI * NI, RPQ = (MI + NI + NQ - 1) / NQ;  // MFMAs per sub-step; fragment reads beside each of the first
     typedef typename T::v8 v8;
     const int wm = wave >> 1, wn = wave & 1;
@@ -258,53 +268,60 @@ __device__ __forceinline__ void dense_loop(LA &la, LB &lb, int k0, int k1, int k
             for (int e = 0; e < 16; ++e) acc[mi][ni][e] = 0.f;
     u32x4 ra, rb;
     uint32_t sa, sb;
-    auto open = [&](int step) {  // the buffers of a step; one past the range is empty
-        if (step == k_last && left < kDenseK) la.cut(left), lb.cut(left);
-        const bool in = step < k1;
-        ra = la.stage(step, in), rb = lb.stage(step, in);
-        sa = la.step_off(step), sb = lb.step_off(step);
+    auto open_a = [&](int step) {  // a step past the range is an empty buffer
+        if (step == k_last && left < kDenseK) la.cut(left);
+        ra = la.stage(step, step < k1), sa = la.step_off(step);
     };
-    auto load = [&](uint32_t stage, int i) {
-        if (i < LA::BL)
-            la.load(ra, sa, stage, wave, i);
-        else
-            lb.load(rb, sb, stage + A_BYTES, wave, i - LA::BL);
+    auto open_b = [&](int step) {
+        if (step == k_last && left < kDenseK) lb.cut(left);
+        rb = lb.stage(step, step < k1), sb = lb.step_off(step);
     };
-#pragma unroll 1
-    for (int j = 0; j < NS; ++j) {
-        open(k0 + j);
 #pragma unroll
-        for (int i = 0; i < ND; ++i) load(lds + j * STAGE, i);
+    for (int j = 0; j < AHEAD; ++j) {
+        open_a(k0 + j), open_b(k0 + j);
+#pragma unroll
+        for (int i = 0; i < NA; ++i) la.load(ra, sa, lds + 2 * j * SLOT, wave, i);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) lb.load(rb, sb, lds + (2 * j + 1) * SLOT, wave, i);
     }
-    wait_loads_and_meet<(NS - 1) * ND>();
+    wait_loads_and_meet<(AHEAD - 1) * (NA + NB)>();
     v8 a[2][MI], b[2][NI];
-    auto read = [&](int to, uint32_t stage, int s, int i) {  // i: 0 .. MI + NI - 1
-        if (i < MI)
-            a[to][i] = fa.get(stage, wm * MI + i, s);
+    auto read = [&](int to, uint32_t sa_, uint32_t sb_, int s, int i) {  // i: 0 .. MI + NI - 1; what the first MFMAs take first
+        if (i == 0 || i > MI)
+            b[to][i == 0 ? 0 : i - MI] = fb.get(sb_, bblock(i == 0 ? 0 : i - MI), s);
         else
-            b[to][i - MI] = fb.get(stage + A_BYTES, bblock(i - MI), s);
+            a[to][i - 1] = fa.get(sa_, wm * MI + i - 1, s);
     };
+    uint32_t slot = 0;  // of A of the step in hand
+    auto after = [](uint32_t at, int n) { return at + n >= (uint32_t)SLOTS ? at + n - SLOTS : at + n; };
 #pragma unroll
-    for (int i = 0; i < MI + NI; ++i) read(0, lds, 0, i);
-    uint32_t slot = 0;
+    for (int i = 0; i < MI + NI; ++i) read(0, lds, lds + SLOT, 0, i);
 #pragma unroll 1
     for (int kt = k0; kt < k1; ++kt) {
-        const uint32_t stage = lds + slot * STAGE;
-        slot = slot + 1 == NS ? 0 : slot + 1;
-        const uint32_t next = lds + slot * STAGE;
-        open(kt + NS);
+        const uint32_t pa = lds + slot * SLOT, pb = lds + after(slot, 1) * SLOT;
+        const uint32_t last = lds + after(slot, SLOTS - 1) * SLOT;  // B's slot of the step before
+        slot = after(slot, 2);
+        const uint32_t na = lds + slot * SLOT, nb = lds + after(slot, 1) * SLOT;
+        open_a(kt + AHEAD);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int cur = s & 1;
-            if (s == 3) wait_loads_and_meet<(NS - 2) * ND>();
+            if (s == 3) {
+                wait_loads_and_meet<(AHEAD - 1) * NA + (AHEAD - 2) * NB>();
+                open_b(kt + AHEAD);
+            }
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 // what this sub-step issues beside its MFMAs, spread over them
 #pragma unroll
-                for (int i = q * RPQ; i < (q + 1) * RPQ && i < MI + NI; ++i) read(cur ^ 1, s == 3 ? next : stage, s == 3 ? 0 : s + 1, i);
+                for (int i = q * RPQ; i < (q + 1) * RPQ && i < MI + NI; ++i) read(cur ^ 1, s == 3 ? na : pa, s == 3 ? nb : pb, s == 3 ? 0 : s + 1, i);
                 if (s == 3) {
 #pragma unroll
-                    for (int i = q * ND / NQ; i < (q + 1) * ND / NQ; ++i) load(stage, i);
+                    for (int i = q * NB / NQ; i < (q + 1) * NB / NQ; ++i) lb.load(rb, sb, pa, wave, i);
+                }
+                if (s < 2) {
+#pragma unroll
+                    for (int i = (s * NQ + q) * NA / (2 * NQ); i < (s * NQ + q + 1) * NA / (2 * NQ); ++i) la.load(ra, sa, last, wave, i);
                 }
                 // operands swapped: a lane then holds four consecutive columns of one row
                 acc[q / NI][q % NI] = T::mfma(b[cur][q % NI], a[cur][q / NI], acc[q / NI][q % NI]);
@@ -369,6 +386,56 @@ __device__ __forceinline__ void dense_rows(const DenseAcc<MI, NI> &acc, uint32_t
                 }
             }
         }
+    }
+}
+
+// The same for outputs that are 16-bit values of the tile's own: N matrices of COLS
+// columns a wave (one of 32 NI, or GLU's a, h and u of 16 NI each), packed before they
+// go through LDS.  value(m, x): matrix m's four values from the accumulators' four, x of
+// a tile's columns or, GLU, x[0] of its first half and x[1] of its second.  put(m, row,
+// column, 16 bytes).  Half the LDS traffic of dense_rows, and nothing but loads and
+// stores past it.
+template <class T, int MI, int NI, bool GLU, int N, class V, class P>
+__device__ __forceinline__ void dense_rows16(const DenseAcc<MI, NI> &acc, uint32_t lds, int wave, int lane, V &&value, P &&put) {
+    constexpr int NC = GLU ? NI / 2 : NI, RB = NC * 64, W = 256 / RB;   // blocks across; bytes of a row; rows of a window
+    constexpr int G = N > 1 && MI > 2 ? MI / 2 : MI, PLANE = 32 * G * RB;  // blocks down at a time
+    constexpr int LPR = RB / 16, RPP = 64 / LPR, PASSES = 32 * G / RPP, AHEAD = PASSES < 8 ? PASSES : 8;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    const uint32_t st = lds + wave * (N * PLANE);
+    const int wm = wave >> 1, wn = wave & 1, hi = lane >> 5;
+    // chunk c (16 bytes) of a row
+    auto at = [&](int row, int c) { return (uint32_t)((row / W) * 256 + (((((row % W) * (16 / W)) | c) ^ ((row / W) & 15)) << 4)); };
+#pragma unroll
+    for (int g = 0; g < MI; g += G) {
+#pragma unroll
+        for (int mi = 0; mi < G; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < NC; ++ni)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16 &c0 = acc[g + mi][ni], &c1 = acc[g + mi][GLU ? ni + NC : ni];
+                    float x[2][4], o[N][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[0][e] = c0[4 * q + e], x[1][e] = c1[4 * q + e];
+                    value(x, o);
+#pragma unroll
+                    for (int m = 0; m < N; ++m)
+                        *(lds_u32x2 *)(uintptr_t)(st + m * PLANE + at(mi * 32 + (lane & 31), ni * 4 + q) + hi * 8) =
+                            u32x2{(uint32_t)T::down(o[m][0]) | (uint32_t)T::down(o[m][1]) << 16, (uint32_t)T::down(o[m][2]) | (uint32_t)T::down(o[m][3]) << 16};
+                }
+        const int c = lane % LPR, col = (wn * NC) * 32 + c * 8, row0 = wm * MI * 32 + g * 32;
+#pragma unroll
+        for (int m = 0; m < N; ++m)
+#pragma unroll 1
+            for (int p0 = 0; p0 < PASSES; p0 += AHEAD) {
+                u32x4 v[AHEAD];
+#pragma unroll
+                for (int p = 0; p < AHEAD; ++p) v[p] = *(const lds_u32x4 *)(uintptr_t)(st + m * PLANE + at((p0 + p) * RPP + lane / LPR, c));
+#pragma unroll
+                for (int p = 0; p < AHEAD; ++p) put(m, row0 + (p0 + p) * RPP + lane / LPR, col, v[p]);
+            }
     }
 }
 

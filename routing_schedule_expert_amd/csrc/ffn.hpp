@@ -18,11 +18,11 @@
 namespace moe {
 
 // v = act(x), d = act'(x) (GRAD)
-template <bool GRAD>
-__device__ __forceinline__ void activation(int kind, const float (&x)[8], float (&v)[8], float (&d)[8]) {
+template <bool GRAD, int N>
+__device__ __forceinline__ void activation(int kind, const float (&x)[N], float (&v)[N], float (&d)[N]) {
     if (kind == MOE_ACT_SILU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-x[e]));
             v[e] = x[e] * s;
             if (GRAD) d[e] = s * fmaf(x[e], 1.0f - s, 1.0f);
@@ -30,7 +30,7 @@ __device__ __forceinline__ void activation(int kind, const float (&x)[8], float 
     } else if (kind == MOE_ACT_GELU) {
         // x Phi(x); by erfc, which keeps its relative accuracy in the lower tail
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const float c = 0.5f * erfcf(-0.70710678f * x[e]);
             v[e] = x[e] * c;
             if (GRAD) d[e] = fmaf(x[e] * 0.39894228f, __expf(-0.5f * x[e] * x[e]), c);
@@ -38,7 +38,7 @@ __device__ __forceinline__ void activation(int kind, const float (&x)[8], float 
     } else if (kind == MOE_ACT_GELU_TANH) {
         // (1 + tanh(w)) / 2 = sigmoid(2 w), w = sqrt(2 / pi) (x + 0.044715 x^3)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const float x2 = x[e] * x[e], s = __builtin_amdgcn_rcpf(1.0f + __expf(-1.5957691f * x[e] * fmaf(0.044715f, x2, 1.0f)));
             v[e] = x[e] * s;
             if (GRAD) {
@@ -48,7 +48,7 @@ __device__ __forceinline__ void activation(int kind, const float (&x)[8], float 
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             v[e] = x[e] > 0.f ? x[e] : x[e] == x[e] ? 0.f : x[e];
             if (GRAD) d[e] = x[e] > 0.f ? 1.0f : 0.f;
         }
@@ -56,8 +56,8 @@ __device__ __forceinline__ void activation(int kind, const float (&x)[8], float 
 }
 
 __device__ __forceinline__ float activation1(int kind, float h) {
-    const float x[8] = {h, h, h, h, h, h, h, h};
-    float v[8], none[8];
+    const float x[1] = {h};
+    float v[1], none[1];
     activation<false>(kind, x, v, none);
     return v[0];
 }
@@ -87,7 +87,7 @@ __device__ __forceinline__ int dense_xcd_order(int block, int total) {
     return x * per + min(x, rest) + i;
 }
 
-template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int NS, class F>
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int SLOTS, class F>
 __device__ __forceinline__ void dense_tile(const DenseArgs &g, int tile, int split, uint32_t lds, const F &f) {
     constexpr int BM = 64 * MI, BN = GLU ? 32 * NI : 64 * NI;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -110,8 +110,19 @@ __device__ __forceinline__ void dense_tile(const DenseArgs &g, int tile, int spl
     }
     const int total = (g.K + kDenseK - 1) / kDenseK, k0 = split * g.steps, k1 = min(total, k0 + g.steps);
     DenseAcc<MI, NI> acc;
-    dense_loop<T, MI, NI, AT, BT, GLU, NS>(la, lb, k0, k1, total - 1, g.K - (total - 1) * kDenseK, lds, wave, lane, acc);
+    dense_loop<T, MI, NI, AT, BT, GLU, SLOTS>(la, lb, k0, k1, total - 1, g.K - (total - 1) * kDenseK, lds, wave, lane, acc);
     auto in = [&](int r, int c) { return m0 + r < g.M && n0 + c < g.N; };
+    // outputs that are 16-bit values of the tile alone have a way of their own
+    if constexpr (F::kPacked > 0) {
+        if (f.packed()) {
+            dense_rows16<T, MI, NI, GLU, F::kPacked>(
+                acc, lds, wave, lane, [&](const float (&x)[2][4], auto &o) { f.values(x, o); },
+                [&](int m, int r, int c, const u32x4 &v) {
+                    if (in(r, c)) f.put(m, m0 + r, n0 + c, v);
+                });
+            return;
+        }
+    }
     typedef decltype(f.pre(0, 0)) Pre;
     dense_rows<MI, NI, GLU>(
         acc, lds, wave, lane, [&](int r, int c) { return in(r, c) ? f.pre(m0 + r, n0 + c) : Pre{}; },
@@ -137,6 +148,20 @@ template <class T>
 struct GluOut {
     uint16_t *HU, *A;
     int I, act;
+    static constexpr int kPacked = 3;  // a, h, u
+    __device__ __forceinline__ bool packed() const { return true; }
+    __device__ __forceinline__ void values(const float (&x)[2][4], float (&o)[3][4]) const {
+        float none[4];
+        activation<false>(act, x[0], o[0], none);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][e] *= x[1][e], o[1][e] = x[0][e], o[2][e] = x[1][e];
+    }
+    __device__ __forceinline__ void put(int m, int64_t r, int c, const u32x4 &v) const {
+        if (m == 0)
+            store16(A + r * I + c, v);
+        else if (HU)
+            store16(HU + r * 2 * I + (m - 1) * I + c, v);
+    }
     __device__ __forceinline__ Nothing pre(int64_t, int) const { return {}; }
     __device__ __forceinline__ void operator()(int64_t r, int c, Nothing, const float (&h)[8], const float (&u)[8]) const {
         float a[8], none[8];
@@ -157,6 +182,7 @@ struct GluBwdOut {
     const uint16_t *HU;
     uint16_t *dHU, *A;  // A nullable
     int I, act;
+    static constexpr int kPacked = 0;
     struct Kept {
         u32x4 h, u;
     };
@@ -188,6 +214,13 @@ struct MatOut {
     void *p;
     int64_t ld;
     int f32, add;
+    static constexpr int kPacked = 1;
+    __device__ __forceinline__ bool packed() const { return !f32; }
+    __device__ __forceinline__ void values(const float (&x)[2][4], float (&o)[1][4]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][e] = x[0][e];
+    }
+    __device__ __forceinline__ void put(int, int64_t r, int c, const u32x4 &v) const { store16(static_cast<uint16_t *>(p) + r * ld + c, v); }
     struct Old {
         f32x4 v[2];
     };
@@ -216,6 +249,7 @@ struct PartOut {
     float *p;
     int64_t ld;
     int N;
+    static constexpr int kPacked = 0;
     __device__ __forceinline__ Nothing pre(int64_t, int) const { return {}; }
     __device__ __forceinline__ void operator()(int64_t r, int c, Nothing, const float (&v)[8]) const { store_f32x8(p + r * ld + c, v); }
     __device__ __forceinline__ void operator()(int64_t r, int c, Nothing, const float (&h)[8], const float (&u)[8]) const {
@@ -225,15 +259,15 @@ struct PartOut {
 };
 
 // Workgroup's share of a product: one tile and one part of K, tiles of a part together.
-template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int NS, class Out>
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int SLOTS, class Out>
 __device__ __forceinline__ void dense_body(const DenseArgs &g, const Out &out, uint32_t lds, int block, int blocks) {
     const int id = dense_xcd_order(block, blocks), tiles = g.mt * g.nt;
     const int split = id / tiles, tile = id - split * tiles;
     if (g.splits == 1) {
-        dense_tile<T, MI, NI, AT, BT, GLU, NS>(g, tile, 0, lds, out);
+        dense_tile<T, MI, NI, AT, BT, GLU, SLOTS>(g, tile, 0, lds, out);
     } else {
         const int64_t ld = GLU ? 2 * (int64_t)g.N : g.N;
-        dense_tile<T, MI, NI, AT, BT, GLU, NS>(g, tile, split, lds, PartOut{g.part + split * (g.M * ld), ld, g.N});
+        dense_tile<T, MI, NI, AT, BT, GLU, SLOTS>(g, tile, split, lds, PartOut{g.part + split * (g.M * ld), ld, g.N});
     }
 }
 
