@@ -23,24 +23,24 @@ namespace {
 extern __shared__ char block_lds[];
 __device__ __forceinline__ uint32_t block_lds_address() { return (uint32_t)(uintptr_t)(lds_char *)block_lds; }
 
-template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int SLOTS, class Out>
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int STAGES, class Out>
 __global__ __launch_bounds__(kDenseThreads, 1) void k_dense(DenseArgs g, Out out) {
-    dense_body<T, MI, NI, AT, BT, GLU, SLOTS>(g, out, block_lds_address(), blockIdx.x, gridDim.x);
+    dense_body<T, MI, NI, AT, BT, GLU, STAGES>(g, out, block_lds_address(), blockIdx.x, gridDim.x);
 }
 
 // The gradients of both weights and of the input in one launch: none needs another, and
 // shorter tiles (of fewer steps along K), which come last, fill the CUs that the last
 // round of the longer ones leaves.
-template <class T, int MI, int NI, int SLOTS>
+template <class T, int MI, int NI, int STAGES>
 __global__ __launch_bounds__(kDenseThreads, 1) void k_grads(DenseArgs g1, MatOut<T> o1, int blocks1, DenseArgs g2, MatOut<T> o2, int blocks2,
                                                             DenseArgs g3, MatOut<T> o3, int blocks3, int third_first) {
     const int b = blockIdx.x - (third_first ? blocks3 : 0), c = b - blocks1, d = third_first ? (int)blockIdx.x : c - blocks2;
     if (d >= 0 && d < blocks3)
-        dense_body<T, MI, NI, false, true, false, SLOTS>(g3, o3, block_lds_address(), d, blocks3);
+        dense_body<T, MI, NI, false, true, false, STAGES>(g3, o3, block_lds_address(), d, blocks3);
     else if (b < blocks1)
-        dense_body<T, MI, NI, true, true, false, SLOTS>(g1, o1, block_lds_address(), b, blocks1);
+        dense_body<T, MI, NI, true, true, false, STAGES>(g1, o1, block_lds_address(), b, blocks1);
     else
-        dense_body<T, MI, NI, true, true, false, SLOTS>(g2, o2, block_lds_address(), c, blocks2);
+        dense_body<T, MI, NI, true, true, false, STAGES>(g2, o2, block_lds_address(), c, blocks2);
 }
 
 template <class T, int NT, int NW, bool GLU>
@@ -117,15 +117,15 @@ int launch_zero(float *p, int64_t words, hipStream_t s) {
 
 int up_to(int64_t n, int d) { return (int)((n + d - 1) / d); }
 
-// The tiles: 64 MI x 64 NI outputs, a ring of SLOTS operand tiles.  The 128 x 128 tile has
-// a short ring, so that two workgroups share a CU, and a long one for when there is one
-// at most.
+// The tiles: 64 MI x 64 NI outputs, stages of dense_loop_deep (0: dense_loop).  The 128 x 128
+// tile has a short ring, so that two workgroups share a CU, and a deep one for when there
+// is one at most.
 enum DenseTile { kTileL, kTileS2, kTileS, kTileX, kTiles };
 struct DenseShape {
-    int mi, ni, slots, per_cu;
+    int mi, ni, stages, per_cu;
     float step, ends;  // us: a step of 64 k with every CU at work, and what a tile takes besides
 };
-constexpr DenseShape kShape[kTiles] = {{4, 4, 5, 1, 1.4f, 9.f}, {2, 2, 5, 2, 0.85f, 6.f}, {2, 2, 9, 1, 0.5f, 6.f}, {1, 2, 9, 1, 0.35f, 5.f}};
+constexpr DenseShape kShape[kTiles] = {{4, 4, 0, 1, 1.4f, 9.f}, {2, 2, 0, 2, 0.85f, 6.f}, {2, 2, 5, 1, 0.42f, 6.f}, {1, 2, 6, 1, 0.3f, 5.f}};
 
 // A product: its sizes (GLU: N of a, B has 2 N rows), its tiles and its cut along K.
 struct DensePlan {
@@ -188,21 +188,21 @@ DenseArgs dense_args(const DensePlan &p, const uint16_t *A, int64_t lda, const u
     return DenseArgs{A, B, lda, ldb, p.M, p.N, p.K, p.mt, p.nt, p.splits, p.steps, static_cast<float *>(part)};
 }
 
-size_t dense_lds(DenseTile t) { return dense_lds_bytes(kShape[t].mi, kShape[t].ni, kShape[t].slots); }
+size_t dense_lds(DenseTile t) { return dense_lds_bytes(kShape[t].mi, kShape[t].ni, kShape[t].stages); }
 
 template <class T, bool AT, bool BT, bool GLU, class Out>
 auto *dense_kernel(DenseTile t) {
-    return t == kTileL    ? k_dense<T, 4, 4, AT, BT, GLU, kShape[kTileL].slots, Out>
-           : t == kTileS2 ? k_dense<T, 2, 2, AT, BT, GLU, kShape[kTileS2].slots, Out>
-           : t == kTileS  ? k_dense<T, 2, 2, AT, BT, GLU, kShape[kTileS].slots, Out>
-                          : k_dense<T, 1, 2, AT, BT, GLU, kShape[kTileX].slots, Out>;
+    return t == kTileL    ? k_dense<T, 4, 4, AT, BT, GLU, kShape[kTileL].stages, Out>
+           : t == kTileS2 ? k_dense<T, 2, 2, AT, BT, GLU, kShape[kTileS2].stages, Out>
+           : t == kTileS  ? k_dense<T, 2, 2, AT, BT, GLU, kShape[kTileS].stages, Out>
+                          : k_dense<T, 1, 2, AT, BT, GLU, kShape[kTileX].stages, Out>;
 }
 template <class T>
 auto *grads_kernel(DenseTile t) {
-    return t == kTileL    ? k_grads<T, 4, 4, kShape[kTileL].slots>
-           : t == kTileS2 ? k_grads<T, 2, 2, kShape[kTileS2].slots>
-           : t == kTileS  ? k_grads<T, 2, 2, kShape[kTileS].slots>
-                          : k_grads<T, 1, 2, kShape[kTileX].slots>;
+    return t == kTileL    ? k_grads<T, 4, 4, kShape[kTileL].stages>
+           : t == kTileS2 ? k_grads<T, 2, 2, kShape[kTileS2].stages>
+           : t == kTileS  ? k_grads<T, 2, 2, kShape[kTileS].stages>
+                          : k_grads<T, 1, 2, kShape[kTileX].stages>;
 }
 
 template <bool GLU, class Out>

@@ -232,26 +232,30 @@ __device__ __forceinline__ void wait_loads_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// LDS of a tile: a ring of SLOTS operand tiles, an odd number, A and B in turn.
-constexpr int dense_slot_bytes(int MI, int NI) { return (MI > NI ? MI : NI) * 64 * kDenseK * 2; }
-constexpr int dense_lds_bytes(int MI, int NI, int SLOTS) { return SLOTS * dense_slot_bytes(MI, NI); }
+constexpr int kDenseSlots = 5;  // of dense_loop's ring
+constexpr int dense_stage_bytes(int MI, int NI) { return (MI + NI) * 64 * kDenseK * 2; }
+// LDS of a tile: dense_loop's ring (STAGES 0), or that many stages of dense_loop_deep's
+constexpr int dense_lds_bytes(int MI, int NI, int STAGES) {
+    return STAGES ? STAGES * dense_stage_bytes(MI, NI) : kDenseSlots * (MI > NI ? MI : NI) * 64 * kDenseK * 2;
+}
 
 // The K loop over steps [k0, k1) (of the tile's K; `left`: k in the step k_last, the
 // operand's last).  GLU: B's blocks are dealt to the waves so that a wave has NI / 2
 // blocks of the tile's first half and the same of its second.  On return every load
 // has landed and the workgroup has met.
 //
-// The ring holds A and B of the step in hand and of the AHEAD - 1 that follow, and A of
+// The ring of SLOTS operand tiles, an odd number, holds A and B of the step in hand and of the AHEAD - 1 that follow, and A of
 // one more.  Past a step's barrier its two slots are free: B of step + AHEAD goes to A's,
 // A of the step after to B's.  The loads are spread: a CU takes one of 1 KiB in 16
 // cycles, so the 64 of a 256 x 256 step need half of its MFMAs' time, and issued in the
 // quarter of it past the barrier they held up the waves' MFMAs (2,923 cycles a step
 // with two slots of both operands, 2,661 with no memory behind them, 2,139 without loads).
-template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int SLOTS, class LA, class LB>
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, class LA, class LB>
 __device__ __forceinline__ void dense_loop(LA &la, LB &lb, int k0, int k1, int k_last, int left, uint32_t lds, int wave, int lane,
                                            DenseAcc<MI, NI> &acc) {
+    constexpr int SLOTS = kDenseSlots;
     static_assert(SLOTS % 2 == 1 && SLOTS >= 5, "A and B in turn");
-    constexpr int SLOT = dense_slot_bytes(MI, NI), AHEAD = SLOTS / 2, NA = LA::BL, NB = LB::BL;
+    constexpr int SLOT = (MI > NI ? MI : NI) * 64 * kDenseK * 2, AHEAD = SLOTS / 2, NA = LA::BL, NB = LB::BL;
     constexpr int NQ = MI * NI, RPQ = (MI + NI + NQ - 1) / NQ;  // MFMAs per sub-step; fragment reads beside each of the first
     typedef typename T::v8 v8;
     const int wm = wave >> 1, wn = wave & 1;
@@ -296,8 +300,9 @@ __device__ __forceinline__ void dense_loop(LA &la, LB &lb, int k0, int k1, int k
     auto after = [](uint32_t at, int n) { return at + n >= (uint32_t)SLOTS ? at + n - SLOTS : at + n; };
 #pragma unroll
     for (int i = 0; i < MI + NI; ++i) read(0, lds, lds + SLOT, 0, i);
+    int kt = k0;  // one step at least
 #pragma unroll 1
-    for (int kt = k0; kt < k1; ++kt) {
+    do {
         const uint32_t pa = lds + slot * SLOT, pb = lds + after(slot, 1) * SLOT;
         const uint32_t last = lds + after(slot, SLOTS - 1) * SLOT;  // B's slot of the step before
         slot = after(slot, 2);
@@ -328,8 +333,106 @@ __device__ __forceinline__ void dense_loop(LA &la, LB &lb, int k0, int k1, int k
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-    }
+    } while (++kt < k1);
     wait_loads_and_meet<0>();
+}
+
+// The same for small tiles, whose MFMAs of a sub-step (4 of a 128 x 128 tile's wave) end
+// before a fragment read for the next has come back: fragments are read two sub-steps
+// ahead, into four sets.  The barrier stands before the step's third sub-step, where the
+// first reads of the next stage are; the stage of the step before is then free for the
+// one STAGES - 1 further on, whose loads are spread over the step that follows.
+template <class T, int MI, int NI, bool AT, bool BT, bool GLU, int STAGES, class LA, class LB>
+__device__ __forceinline__ void dense_loop_deep(LA &la, LB &lb, int k0, int k1, int k_last, int left, uint32_t lds, int wave, int lane,
+                                                DenseAcc<MI, NI> &acc) {
+    static_assert(STAGES >= 4, "the stage before, the one in hand, the next and one that lands");
+    constexpr int A_BYTES = MI * 64 * kDenseK * 2, STAGE = dense_stage_bytes(MI, NI), NA = LA::BL, ND = NA + LB::BL;
+    constexpr int NQ = MI * NI, RPQ = (MI + NI + NQ - 1) / NQ;
+    typedef typename T::v8 v8;
+    const int wm = wave >> 1, wn = wave & 1;
+    Frags<T, AT, 64 * MI> fa;
+    Frags<T, BT, 64 * NI> fb;
+    fa.init(lane);
+    fb.init(lane);
+    auto bblock = [&](int ni) { return GLU ? (ni < NI / 2 ? wn * (NI / 2) + ni : NI + wn * (NI / 2) + ni - NI / 2) : wn * NI + ni; };
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[mi][ni][e] = 0.f;
+    u32x4 ra, rb;
+    uint32_t sa, sb;
+    auto open = [&](int step) {  // a step past the range is an empty buffer
+        if (step == k_last && left < kDenseK) la.cut(left), lb.cut(left);
+        const bool in = step < k1;
+        ra = la.stage(step, in), rb = lb.stage(step, in);
+        sa = la.step_off(step), sb = lb.step_off(step);
+    };
+    auto load = [&](uint32_t stage, int i) {
+        if (i < NA)
+            la.load(ra, sa, stage, wave, i);
+        else
+            lb.load(rb, sb, stage + A_BYTES, wave, i - NA);
+    };
+    // loads [0, ND) of a stage over the sub-steps 2, 3, 0, 1: the first of place p of 4 NQ
+    auto first = [](int p) { return p * ND / (4 * NQ); };
+#pragma unroll
+    for (int j = 0; j < STAGES - 1; ++j) {
+        open(k0 + j);
+#pragma unroll
+        for (int i = 0; i < (j < STAGES - 2 ? ND : first(2 * NQ)); ++i) load(lds + j * STAGE, i);
+    }
+    wait_loads_and_meet<(STAGES - 3) * ND + first(2 * NQ)>();
+    v8 a[4][MI], b[4][NI];
+    auto read = [&](int s, uint32_t stage, int i) {
+        if (i == 0 || i > MI)
+            b[s][i == 0 ? 0 : i - MI] = fb.get(stage + A_BYTES, bblock(i == 0 ? 0 : i - MI), s);
+        else
+            a[s][i - 1] = fa.get(stage, wm * MI + i - 1, s);
+    };
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int i = 0; i < MI + NI; ++i) read(s, lds, i);
+        __builtin_amdgcn_sched_barrier(0);  // in the loop's order, or its first wait is for all of them
+    }
+    uint32_t slot = 0;
+    auto after = [](uint32_t at, int n) { return at + n >= (uint32_t)STAGES ? at + n - STAGES : at + n; };
+    int kt = k0;  // one step at least
+#pragma unroll 1
+    do {
+        const uint32_t stage = lds + slot * STAGE, before = lds + after(slot, STAGES - 1) * STAGE, filling = lds + after(slot, STAGES - 2) * STAGE;
+        slot = after(slot, 1);
+        const uint32_t next = lds + slot * STAGE;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s == 2) {
+                // every read of the stage before has been used; this one's are in flight
+                asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 3) * ND) : "memory");
+                open(kt + STAGES - 1);
+            }
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+                for (int i = q * RPQ; i < (q + 1) * RPQ && i < MI + NI; ++i) read((s + 2) & 3, s < 2 ? stage : next, i);
+                const int p = ((s + 2) & 3) * NQ + q;
+#pragma unroll
+                for (int i = first(p); i < first(p + 1); ++i) load(s < 2 ? filling : before, i);
+                acc[q / NI][q % NI] = T::mfma(b[s][q % NI], a[s][q / NI], acc[q / NI][q % NI]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } while (++kt < k1);
+    wait_loads_and_meet<0>();
+}
+
+// Elements 4 q ... of an accumulator, where they are used: moved out of the accumulation
+// registers all at once, ahead of the branches to the ways out, they would not fit.
+__device__ __forceinline__ f32x4 dense_take(const f32x16 &c, int q) {
+    float a = c[4 * q], b = c[4 * q + 1], d = c[4 * q + 2], e = c[4 * q + 3];
+    asm volatile("" : "+v"(a), "+v"(b), "+v"(d), "+v"(e));
+    return f32x4{a, b, d, e};
 }
 
 // The tile's values, 8 consecutive columns of a row at a time, through LDS that the
@@ -362,9 +465,8 @@ __device__ __forceinline__ void dense_rows(const DenseAcc<MI, NI> &acc, uint32_t
         for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const f32x16 &c = acc[mi][ni];
-                *(lds_f32x4 *)(uintptr_t)(st + r * ROW + (((ni * 8 + 2 * q + hi) ^ (r & MASK)) << 4)) =
-                    f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+                const f32x4 v = dense_take(acc[mi][ni], q);
+                *(lds_f32x4 *)(uintptr_t)(st + r * ROW + (((ni * 8 + 2 * q + hi) ^ (r & MASK)) << 4)) = v;
             }
         const int row0 = wm * MI * 32 + mi * 32;
 #pragma unroll 1
@@ -415,15 +517,16 @@ __device__ __forceinline__ void dense_rows16(const DenseAcc<MI, NI> &acc, uint32
             for (int ni = 0; ni < NC; ++ni)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const f32x16 &c0 = acc[g + mi][ni], &c1 = acc[g + mi][GLU ? ni + NC : ni];
+                    const f32x4 c0 = dense_take(acc[g + mi][ni], q), c1 = GLU ? dense_take(acc[g + mi][GLU ? ni + NC : ni], q) : c0;
                     float x[2][4], o[N][4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[0][e] = c0[4 * q + e], x[1][e] = c1[4 * q + e];
+                    for (int e = 0; e < 4; ++e) x[0][e] = c0[e], x[1][e] = c1[e];
                     value(x, o);
 #pragma unroll
                     for (int m = 0; m < N; ++m)
                         *(lds_u32x2 *)(uintptr_t)(st + m * PLANE + at(mi * 32 + (lane & 31), ni * 4 + q) + hi * 8) =
                             u32x2{(uint32_t)T::down(o[m][0]) | (uint32_t)T::down(o[m][1]) << 16, (uint32_t)T::down(o[m][2]) | (uint32_t)T::down(o[m][3]) << 16};
+                    __builtin_amdgcn_sched_barrier(0);  // a few accumulators in registers at a time
                 }
         const int c = lane % LPR, col = (wn * NC) * 32 + c * 8, row0 = wm * MI * 32 + g * 32;
 #pragma unroll
