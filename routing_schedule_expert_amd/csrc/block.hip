@@ -138,10 +138,16 @@ struct DensePlan {
 };
 DensePlan dense_product(int M, int N, int K, bool glu = false) { return DensePlan{M, N, K, glu, 0, 0, 1, 0}; }
 
-// The tile for the products of one launch, and their cuts along K.  The time of each
-// choice is estimated from a step's and a tile's measured times: all tiles at once where the CUs
-// hold them, otherwise their sum over the CUs, and the largest's last round.  A cut costs the
-// second pass (kJoin and the parts' bytes).
+// The tile for the products of one launch, and their cuts along K: the least of the times
+// estimated from a step's and a tile's measured ones (kShape) for each choice.  One product
+// goes in rounds of the tiles that the CUs hold, where a CU with one of its two tiles
+// takes 0.6 of the time; several, by the sum of their tiles' times and part of the
+// longest's.  A cut costs the second pass (kJoin and the parts' bytes).  Measured against the
+// others forced, us, 256 x 256 / 128 x 128 shared / alone / 64 x 128, taken in brackets:
+// up of 333 rows (H 1032, I 520) 30 / 13 / 13 / [10], of 1,021 (2056, 1032) 55 / 27 / [25] / 36, of 600
+// (4096, 4096) 87 / [56] / 69 / 75, of 3,000 (2048, 1024) 54 / [34] / 40 / 46, of 8,192 (7168, 2048) [366] / 460; of 128
+// rows (7168, 2048) uncut 125 / 60 / 48 / 37, in four parts of K [16 + 5].  A 128 x 256 tile was
+// never ahead of the better of its neighbours by more than 6%.
 DenseTile dense_plan(DensePlan *p, int n) {
     constexpr float kJoin = 5.f, kPerMiB = 0.4f;
     constexpr int kCus = 256;  // of every gfx950; also where a workspace is sized without one
@@ -172,7 +178,12 @@ DenseTile dense_plan(DensePlan *p, int n) {
             }
             if (!useful || (cut > 1 && blocks > kCus * k.per_cu)) break;
             const int room = kCus * k.per_cu;
-            const float time = (blocks <= room ? most : std::max(most, sum / room + 0.3f * most)) + join;
+            const int rest = blocks % room;
+            float time = join;
+            if (n > 1)
+                time += std::max(most, sum / room + 0.3f * most);
+            else
+                time += most * ((float)(blocks / room) + (rest == 0 ? 0.f : rest <= kCus && k.per_cu > 1 ? 0.6f : 1.f));
             if (time < least) {
                 least = time;
                 best = (DenseTile)t;
@@ -419,7 +430,13 @@ int ln_typed(const moe_ln_desc *n, bool odd, F &&f) {
 // Gradients.
 // ---------------------------------------------------------------------------
 
-int64_t grad_pieces_of(int64_t n) { return (n + kGradPiece - 1) / kGradPiece; }
+int64_t grad_pieces_of(int64_t n, int elems) { return (n + elems - 1) / elems; }
+// few elements (up to what a launch's workgroups take in one small piece each): small pieces
+int grad_elems(const moe_grad *t, int32_t n) {
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) all += t[i].numel;
+    return all <= (int64_t)kGradParts * kGradPieceFew ? kGradPieceFew : kGradPiece;
+}
 
 int grad_check(const moe_grad *t, int32_t n, bool out) {
     if (n < 0 || (n > 0 && !t)) return MOE_EINVAL;
@@ -441,13 +458,14 @@ bool grad_scalars_ok(int32_t kind, float scale, float max_norm, float eps) {
 
 // Tensors [*at, ...) that a launch takes, as many as fit; false when none is left.
 template <int N, bool OUT>
-bool grad_fill(GradLaunch<N, OUT> &l, const moe_grad *t, int32_t n, int32_t *at) {
+bool grad_fill(GradLaunch<N, OUT> &l, const moe_grad *t, int32_t n, int32_t *at, int elems) {
     l.count = 0;
+    l.elems = elems;
     int64_t pieces = 0;
     while (*at < n && l.count < N) {
         const moe_grad &k = t[*at];
         if (k.numel) {
-            const int64_t p = grad_pieces_of(k.numel);
+            const int64_t p = grad_pieces_of(k.numel, elems);
             l.t[l.count] = GradTensor{k.g, k.numel << 2 | k.type};
             if constexpr (OUT) l.out[l.count] = k.out;
             l.piece[l.count++] = (int32_t)pieces;
@@ -465,7 +483,8 @@ int64_t grad_ws_bytes(int32_t n) { return 8ll * kGradParts * std::max(1, grad_la
 int launch_grad_sums(const moe_grad *t, int32_t n, GradScalars &k, hipStream_t s) {
     double *parts = k.parts;
     GradLaunch<kSumTensors, false> l;
-    for (int32_t at = 0; grad_fill(l, t, n, &at);) {
+    const int elems = grad_elems(t, n);
+    for (int32_t at = 0; grad_fill(l, t, n, &at, elems);) {
         const int grid = std::min(l.piece[l.count], kGradParts);
         GradScalars a = k;
         a.parts = parts;
@@ -488,12 +507,13 @@ int launch_grad_result(const GradScalars &k, hipStream_t s) {
 
 int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s) {
     GradLaunch<kScaleTensors, true> l;
+    const int elems = grad_elems(t, n);
     // from the last tensors to the first, as within a launch: the cache holds what was read last
     for (int32_t end = n; end > 0;) {
         int32_t begin = end, taken = 0;
         while (begin > 0 && taken < kScaleTensors) taken += t[--begin].numel > 0;
         int32_t at = begin;
-        if (grad_fill(l, t, end, &at)) {
+        if (grad_fill(l, t, end, &at, elems)) {
             const int grid = (int)std::min<int64_t>(l.piece[l.count], 8 * device_cus());
             TraceScope tr("grad_scale", s);
             hipLaunchKernelGGL(k_grad_scale, dim3(grid), dim3(kGradThreads), 0, s, l, k);

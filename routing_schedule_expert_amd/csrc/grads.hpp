@@ -9,7 +9,7 @@
 // where NaN is above infinity.
 //
 // The tensors of a launch come as its arguments (their addresses may be others in the
-// next call).  They are cut into pieces of 16384 elements, dealt to the workgroups in turn;
+// next call).  They are cut into pieces, dealt to the workgroups in turn;
 // loads are of whole aligned 16-byte words, the neighbours' elements
 // in a tensor's first and last word left out.
 #pragma once
@@ -19,7 +19,9 @@
 namespace moe {
 
 constexpr int kGradThreads = 512;
-constexpr int kGradPiece = 16384;   // elements
+// Elements of a piece: 16384 stream best (2.5 GB), but leave most CUs without one where there
+// are few (5 tensors of 100,000 elements: 9 pieces of 16384, 51 of 2048).
+constexpr int kGradPiece = 16384, kGradPieceFew = 2048;
 constexpr int kGradParts = 2048;    // workgroups of a launch of the first pass at most
 constexpr int kSumTensors = 176, kScaleTensors = 128;  // per launch: arguments below 4 KiB
 
@@ -33,6 +35,7 @@ struct GradLaunch {
     void *out[OUT ? N : 1];
     int32_t piece[N + 1];  // each tensor's first piece; piece[count]: all of them
     int32_t count;
+    int32_t elems;  // of a piece
 };
 struct GradScalars {
     double *parts;
@@ -138,8 +141,8 @@ __device__ __forceinline__ void grad_pieces(const L &l, bool backwards, F &&f) {
             while (l.piece[t] > c) --t;
         else
             while (l.piece[t + 1] <= c) ++t;
-        const int64_t n = l.t[t].n >> 2, e0 = (int64_t)(c - l.piece[t]) * kGradPiece;
-        f(t, (int)(l.t[t].n & 3), e0, min(n, e0 + kGradPiece));
+        const int64_t n = l.t[t].n >> 2, e0 = (int64_t)(c - l.piece[t]) * l.elems;
+        f(t, (int)(l.t[t].n & 3), e0, min(n, e0 + l.elems));
     }
 }
 

@@ -947,6 +947,7 @@ class LayerNormGrads:
     db: torch.Tensor | None
     ws: torch.Tensor | None
     both: torch.Tensor | None  # dg and db, which the call writes together
+    rows_of_both: tuple  # the two, whether or not they are asked for
 
 
 def alloc_layer_norm_bwd(n: moe_ln_desc, device, weight: bool = True, bias: bool = True) -> LayerNormGrads:
@@ -958,12 +959,12 @@ def alloc_layer_norm_bwd(n: moe_ln_desc, device, weight: bool = True, bias: bool
         db=both[1] if bias else None,
         ws=torch.empty(max(layer_norm_workspace_bytes(n), 256), dtype=torch.uint8, device=device) if both is not None else None,
         both=both,
+        rows_of_both=(None, None) if both is None else tuple(both),
     )
 
 
 def layer_norm_bwd(n, x, g, stats, dy, dres, b: LayerNormGrads, stream=None):
-    dg, db = (None, None) if b.both is None else (b.both[0], b.both[1])
-    return moe_layer_norm_bwd(n, x, g, stats, dy, dres, b.dx, dg, db, b.ws, stream)
+    return moe_layer_norm_bwd(n, x, g, stats, dy, dres, b.dx, *b.rows_of_both, b.ws, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -979,20 +980,11 @@ class GradList:
     out: list
     table: object
     dev: int
-    result: torch.Tensor  # 16 bytes: sum (float64), norm, coef (float32)
+    result: torch.Tensor  # 16 bytes, of which sum (float64), norm and coef (float32) are views
+    sum: torch.Tensor
+    norm: torch.Tensor
+    coef: torch.Tensor
     ws: torch.Tensor
-
-    @property
-    def sum(self):
-        return self.result.view(torch.float64)[:1]
-
-    @property
-    def norm(self):
-        return self.result.view(torch.float32)[2:3]
-
-    @property
-    def coef(self):
-        return self.result.view(torch.float32)[3:4]
 
 
 def make_grad_list(grads, out=None, device=None) -> GradList:
@@ -1011,7 +1003,9 @@ def make_grad_list(grads, out=None, device=None) -> GradList:
             raise ValueError(f"out {i}: {o.numel()} elements for a gradient of {g.numel()}")
         table[i] = moe_grad(_buf(f"gradient {i}", g, g.dtype, 0, dev), _buf(f"out {i}", o, g.dtype, 0, dev), g.numel(), _type(g.dtype), 0)
     device = torch.device("cuda", dev)
-    return GradList(grads, out, table, dev, torch.zeros(16, dtype=torch.uint8, device=device),
+    result = torch.zeros(16, dtype=torch.uint8, device=device)
+    floats = result.view(torch.float32)
+    return GradList(grads, out, table, dev, result, result.view(torch.float64)[:1], floats[2:3], floats[3:4],
                     torch.empty(load().moe_grad_workspace_bytes(len(grads)), dtype=torch.uint8, device=device))
 
 
