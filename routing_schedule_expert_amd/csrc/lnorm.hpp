@@ -336,7 +336,8 @@ __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float
         const bool some = r < a.rows;
         col.load(cx, a.x, r * a.ldx, some);
         col.load(cy, k.dy, r * a.ldy, some);
-        if (CH == 1) col.load(cr, k.dres, r * a.ldx, some);
+        // dx may take dres' place: where columns overlap, all of dres is read before any of dx is written
+        if (CH == 1 || ODD) col.load(cr, k.dres, r * a.ldx, some);
         const float2 st = reinterpret_cast<const float2 *>(a.stats)[min(r, a.rows - 1)];
         mean = st.x, rstd = st.y;
     };
@@ -389,10 +390,8 @@ __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float
         for (int i = 0; i < CH; ++i) {
             if (CH > 1) {
                 make(i);
-                if (k.dres && col.in(i)) {
-                    cr[0].template load<ODD>(static_cast<const char *>(k.dres) + (row * a.ldx + col.at[i]) * Chunk<TI>::ES);
-                    cr[0].get(res);
-                }
+                if (!ODD && k.dres && col.in(i)) cr[i].template load<ODD>(static_cast<const char *>(k.dres) + (row * a.ldx + col.at[i]) * Chunk<TI>::ES);
+                cr[i].get(res);
             }
             float o[8];
 #pragma unroll

@@ -146,7 +146,7 @@ def test_strides_and_starts(H, ldx, ldy, off, tx, ty):
     check_bwd(c, c["g"], True)
 
 
-@pytest.mark.parametrize("H", [72, 1031, 4096, 7168, 12288])
+@pytest.mark.parametrize("H", [5, 72, 1031, 4096, 7168, 7171, 12288, 12299, 20001])
 def test_in_place(H):
     c = make(50, H)
     want = check_fwd(c, c["g"], c["b"])
