@@ -247,7 +247,7 @@ int ffn_check(const moe_ffn_desc *n) {
     // a tile's rows, and 64 rows of an MN-contiguous operand, are raw buffers below 2 GiB
     constexpr int64_t kLd = 1 << 20;
     if (n->H % 8 || n->I % 8 || n->H > 65536 || n->I > 65536 || n->ldx % 8 || n->ldo % 8 || ffn_ldx(n) > kLd || ffn_ldo(n) > kLd ||
-        (int64_t)n->H * n->I >= (1ll << 30) || n->rows >= (1ll << 30))
+        (int64_t)n->H * n->I >= (1ll << 30) || n->rows >= (1ll << 30) || n->rows * std::max(n->H, 2 * n->I) >= (1ll << 40))
         return MOE_EUNSUPPORTED;
     return MOE_OK;
 }
