@@ -737,9 +737,11 @@ enum {
  * Outputs must not overlap inputs or each other.  Pointers 16-byte aligned; what lies
  * between rows (ldx, ldo > H) is neither read nor written.  A row's out, HU, A and dX
  * depend on that row alone.  Every sum is fp32, in an order that depends on the sizes
- * only: repeated calls give bitwise the same.
+ * only: repeated calls give bitwise the same.  fp16 values past 65504 become infinite.
+ * The shared expert's gradient: HU and A are moe_layer_fwd_shared's HUs and As, whose padding rows
+ * are not read.
  * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for H, I or a stride that is not a
- * multiple of 8 or past its limit, I * H >= 2^30 or rows >= 2^30.  With rows = 0 the row buffers
+ * multiple of 8 or past its limit, I * H >= 2^30, rows >= 2^30 or rows * max(H, 2I) >= 2^40.  With rows = 0 the row buffers
  * may be NULL.  moe_gated_ffn_workspace_bytes returns -1 for an n that the calls refuse.
  */
 enum {
@@ -799,11 +801,12 @@ int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, cons
  * moe_grad_clip — the norm of many gradients together, and the gradients scaled to it:
  *     norm = sqrt(sum of (scale g)^2) over all of them     (MOE_NORM_L2)
  *          = the largest |scale g|                         (MOE_NORM_MAX)
- *     coef = min(1, max_norm / (norm + eps)),   out = (scale coef) g, rounded once
+ *     coef = min(1, max_norm / (norm + eps)) (1 where both are 0),   out = (scale coef) g, rounded once
  *   t, n    host array of n (>= 0) tensors: g, out (g itself, or a buffer that overlaps no
- *           gradient), numel (>= 0), type (MOE_TYPE_*; of both).  Element alignment is
- *           enough; out of the alignment of g (modulo 16) runs fastest.  Read during the
- *           call only, and not kept
+ *           gradient and no other out), numel (>= 0), type (MOE_TYPE_*; of both).  No two
+ *           gradients overlap.  Element alignment is enough (whole 16-byte words are read, of
+ *           which a neighbour's elements are left out and never written); out of the alignment
+ *           of g (modulo 16) runs fastest.  Read during the call only, and not kept
  *   scale   applied before the norm (1 / ranks, 1 / loss scale)
  *   max_norm >= 0, eps >= 0
  *   result  device: sum (of the squares of scale g, or their maximum, in 64 bits: what

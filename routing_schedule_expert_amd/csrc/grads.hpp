@@ -184,7 +184,8 @@ __device__ __forceinline__ moe_grad_result grad_result(const GradScalars &k, dou
     const double scale = k.scale < 0.f ? -(double)k.scale : (double)k.scale;
     moe_grad_result r;
     r.sum = max_of ? s * scale : s * scale * scale;
-    const double norm = max_of ? r.sum : sqrt(s) * scale, c = (double)k.max_norm / (norm + (double)k.eps);
+    const double norm = max_of ? r.sum : sqrt(s) * scale, below = norm + (double)k.eps;
+    const double c = below == 0.0 ? 1.0 : (double)k.max_norm / below;
     r.norm = (float)norm;
     r.coef = (float)(c >= 1.0 ? 1.0 : c);  // NaN stays
     return r;

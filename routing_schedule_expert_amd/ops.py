@@ -988,8 +988,9 @@ class GradList:
 
 
 def make_grad_list(grads, out=None, device=None) -> GradList:
-    """grads: contiguous fp32, bf16 or fp16 tensors of one GPU; out: as many of the same types
-    and sizes (None: the gradients themselves); device: needed where grads is empty."""
+    """grads: contiguous fp32, bf16 or fp16 tensors of one GPU, none of which overlaps another;
+    out: as many of the same types and sizes (None: the gradients themselves); device: needed
+    where grads is empty."""
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):
@@ -997,11 +998,18 @@ def make_grad_list(grads, out=None, device=None) -> GradList:
     dev = grads[0].get_device() if grads else torch.device(device).index
     if dev is None or dev < 0:
         raise TypeError("device buffers must be CUDA (HIP) torch tensors")
-    table = (moe_grad * max(1, len(grads)))()
+    table, spans = (moe_grad * max(1, len(grads)))(), []
     for i, (g, o) in enumerate(zip(grads, out)):
         if o.numel() != g.numel():
             raise ValueError(f"out {i}: {o.numel()} elements for a gradient of {g.numel()}")
+        if o is not g and o.data_ptr() != g.data_ptr():
+            spans.append((o.data_ptr(), o.data_ptr() + o.numel() * o.element_size(), f"out {i}"))
+        spans.append((g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), f"gradient {i}"))
         table[i] = moe_grad(_buf(f"gradient {i}", g, g.dtype, 0, dev), _buf(f"out {i}", o, g.dtype, 0, dev), g.numel(), _type(g.dtype), 0)
+    spans = sorted(s for s in spans if s[0] < s[1])
+    for a, b in zip(spans, spans[1:]):
+        if b[0] < a[1]:
+            raise ValueError(f"{a[2]} and {b[2]} overlap")
     device = torch.device("cuda", dev)
     result = torch.zeros(16, dtype=torch.uint8, device=device)
     floats = result.view(torch.float32)

@@ -108,6 +108,8 @@ def test_scale_and_bounds():
     assert float(gl.coef) == 1.0 and all(torch.equal(a, b) for a, b in zip(same, grads))
     zeros = [torch.zeros(100, device=dev())]
     assert float(check(zeros).norm) == 0.0
+    gl = ops.grad_clip(ops.make_grad_list(zeros), 0.0, eps=0.0)
+    assert float(gl.norm) == 0.0 and float(gl.coef) == 1.0 and not bool(zeros[0].any())
 
 
 def test_values_whose_squares_leave_fp32():
@@ -189,6 +191,12 @@ def test_lists_that_do_not_fit():
     for bad in ([t.cpu()], [t.double()], [t.view(10, 10).t()]):
         with pytest.raises((ValueError, TypeError)):
             ops.make_grad_list(bad)
+    for bad in ([t, t], [t, t[50:]], [t[:51], t[50:]]):
+        with pytest.raises(ValueError):
+            ops.make_grad_list(bad)
+    with pytest.raises(ValueError):
+        ops.make_grad_list([t[:50], t[50:]], [t[50:], torch.empty_like(t[:50])])
+    ops.make_grad_list([t[:50], t[50:50], t[50:]])
     for out in ([], [t[:50]], [t.bfloat16()]):
         with pytest.raises((ValueError, TypeError)):
             ops.make_grad_list([t], out)
