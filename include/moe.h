@@ -741,8 +741,8 @@ enum {
  * The shared expert's gradient: HU and A are moe_layer_fwd_shared's HUs and As, whose padding rows
  * are not read.
  * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for H, I or a stride that is not a
- * multiple of 8 or past its limit, I * H >= 2^30, rows >= 2^30 or rows * max(H, 2I) >= 2^40.  With rows = 0 the row buffers
- * may be NULL.  moe_gated_ffn_workspace_bytes returns -1 for an n that the calls refuse.
+ * multiple of 8 or past its limit, I * H >= 2^30, rows >= 2^30 or rows * max(H, 2I) >= 2^36.  With rows = 0 the
+ * row buffers may be NULL.  moe_gated_ffn_workspace_bytes returns -1 for an n that the calls refuse.
  */
 enum {
     MOE_ACT_SILU = 0,

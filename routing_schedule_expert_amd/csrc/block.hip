@@ -244,10 +244,11 @@ int ffn_check(const moe_ffn_desc *n) {
     if (!n || n->rows < 0 || n->H < 1 || n->I < 1 || n->act < MOE_ACT_SILU || n->act > MOE_ACT_RELU ||
         (n->type != MOE_TYPE_BF16 && n->type != MOE_TYPE_FP16) || n->ldx < 0 || n->ldo < 0 || ffn_ldx(n) < n->H || ffn_ldo(n) < n->H)
         return MOE_EINVAL;
-    // a tile's rows, and 64 rows of an MN-contiguous operand, are raw buffers below 2 GiB
+    // a tile's rows, and 64 rows of an MN-contiguous operand, are raw buffers below 2 GiB; a grid has less than 2^32
+    // threads, 2^24 tiles (of 128 x 128, 64 columns of a, where there are that many)
     constexpr int64_t kLd = 1 << 20;
     if (n->H % 8 || n->I % 8 || n->H > 65536 || n->I > 65536 || n->ldx % 8 || n->ldo % 8 || ffn_ldx(n) > kLd || ffn_ldo(n) > kLd ||
-        (int64_t)n->H * n->I >= (1ll << 30) || n->rows >= (1ll << 30) || n->rows * std::max(n->H, 2 * n->I) >= (1ll << 40))
+        (int64_t)n->H * n->I >= (1ll << 30) || n->rows >= (1ll << 30) || n->rows * std::max(n->H, 2 * n->I) >= (1ll << 36))
         return MOE_EUNSUPPORTED;
     return MOE_OK;
 }

@@ -31,7 +31,8 @@ def test_ffn_sizes():
     assert ops.gated_ffn_workspace_bytes(ffn(rows=16384, H=7168, I=2048), True) == 16384 * 6 * 2048
     assert ops.gated_ffn_workspace_bytes(ffn(rows=100), True) >= 100 * 6 * 136
     bad = [ffn(rows=-1), ffn(H=0), ffn(I=0), ffn(act=4), ffn(act=-1), ffn(H=260), ffn(I=132), ffn(H=65544), ffn(I=65544), ffn(ldx=256), ffn(ldo=8),
-           ffn(ldx=268), ffn(ldo=-8), ffn(ldx=(1 << 20) + 8), ffn(H=32768, I=32768), ffn(rows=1 << 30), ffn(rows=1 << 25, H=32768), ffn(rows=1 << 25, I=16384), ffn(dtype=torch.float32)]
+           ffn(ldx=268), ffn(ldo=-8), ffn(ldx=(1 << 20) + 8), ffn(H=32768, I=32768), ffn(rows=1 << 30), ffn(rows=1 << 25, H=2048), ffn(rows=1 << 25, I=1024),
+           ffn(dtype=torch.float32)]
     for n in bad:
         assert lib.moe_gated_ffn_workspace_bytes(ctypes.byref(n), 0) == lib.moe_gated_ffn_workspace_bytes(ctypes.byref(n), 1) == -1
     assert lib.moe_gated_ffn_workspace_bytes(ctypes.byref(ffn()), 2) == -1
