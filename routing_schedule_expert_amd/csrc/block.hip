@@ -43,9 +43,9 @@ __global__ __launch_bounds__(kDenseThreads, 1) void k_grads(DenseArgs g1, MatOut
         dense_body<T, MI, NI, true, true, false, STAGES>(g2, o2, block_lds_address(), c, blocks2);
 }
 
-template <class T, int NT, int NW, bool GLU>
-__global__ __launch_bounds__(64 * NW, 1) void k_skinny(SkinnyArgs g) {
-    skinny_body<T, NT, NW, GLU>(g, block_lds_address());
+template <class T, int NT, bool GLU>
+__global__ __launch_bounds__(64 * kSkinnyWaves, 1) void k_skinny(SkinnyArgs g) {
+    skinny_body<T, NT, GLU>(g, block_lds_address());
 }
 
 template <bool GLU, class Out>
@@ -253,7 +253,8 @@ int ffn_check(const moe_ffn_desc *n) {
     return MOE_OK;
 }
 
-// A few rows go by the weights' stream.
+// A few rows go by the weights' stream.  Both products, us, by it / by dense_plan's tiles cut along K: H = 7168, I = 2048,
+// 8 rows 22 / 36, 32 rows 29 / 37, 64 rows 38 / 40; H = 2048, I = 1024, 8 rows 10 / 23, 64 rows 15 / 27.
 constexpr int kSkinnyRows = 64;
 bool ffn_skinny(const moe_ffn_desc *n) { return n->rows <= kSkinnyRows; }
 
@@ -287,15 +288,10 @@ int64_t ffn_ws_bytes(const moe_ffn_desc *n, bool bwd) {
 template <class T, bool GLU>
 int launch_skinny(const SkinnyArgs &g, hipStream_t s, const char *name) {
     const int units = up_to(g.N, GLU ? 8 : 16);
-    // 8 waves where the workgroups are no more than the CUs, 4 where two can share one
-    const bool wide = units <= device_cus() && g.M <= 16;
-    const int waves = wide ? 8 : 4, nt = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
+    const int nt = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
     TraceScope tr(name, s);
-    auto *fn = wide      ? k_skinny<T, 1, 8, GLU>
-               : nt == 1 ? k_skinny<T, 1, 4, GLU>
-               : nt == 2 ? k_skinny<T, 2, 4, GLU>
-                         : k_skinny<T, 4, 4, GLU>;
-    hipLaunchKernelGGL(fn, dim3(units), dim3(64 * waves), skinny_lds(nt, waves), s, g);
+    auto *fn = nt == 1 ? k_skinny<T, 1, GLU> : nt == 2 ? k_skinny<T, 2, GLU> : k_skinny<T, 4, GLU>;
+    hipLaunchKernelGGL(fn, dim3(units), dim3(64 * kSkinnyWaves), skinny_lds(nt), s, g);
     return launch_status();
 }
 
@@ -351,6 +347,8 @@ int ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_t *X, cons
 
 int64_t ln_ldx(const moe_ln_desc *n) { return n->ldx ? n->ldx : n->H; }
 int64_t ln_ldy(const moe_ln_desc *n) { return n->ldy ? n->ldy : n->H; }
+// Rows up to 512 elements are a wave's (8 columns a lane at most): us forward / backward against a workgroup for each,
+// 100,000 rows of 128 13 / 17 against 33 / 147, 60,000 of 512 22 / 27 against 27 / 91.
 constexpr int kLnWaveH = 512, kLnMaxH = 32768, kLnSumH = 8192;
 
 int ln_check(const moe_ln_desc *n) {
@@ -390,7 +388,12 @@ LnPlan ln_plan(const moe_ln_desc *n) {
 int ln_groups(const moe_ln_desc *n) {
     const LnPlan p = ln_plan(n);
     if (p.wave) return (int)std::max<int64_t>(1, std::min<int64_t>((n->rows + 4 * p.teams - 1) / (4 * p.teams), 1024));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(n->rows, p.threads <= 512 ? 512 : 256));
+    // Two on a CU, one of more than 512 threads (half as many: 16,384 rows of 7168 118 -> 218 us, twice: 124 and 2 more
+    // for the pass over the sums).  Four of up to 256 threads with 16-bit rows, 16 each, which pay for their sums (us
+    // with that pass, two / four: 16,384 rows of 2048 43 / 42, 20,000 of 1536 47 / 42, 30,000 of 1024 61 / 44, where
+    // eight take 47; 1,000 rows of 2048 14 / 19; 30,000 of 1024 in fp32 83 / 88).
+    const int64_t groups = p.threads > 512 ? 256 : p.threads <= 256 && n->x_type != MOE_TYPE_FP32 && n->rows >= 16 * 1024 ? 1024 : 512;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n->rows, groups));
 }
 // rows of sums of the long rows' second reading
 int ln_column_groups(const moe_ln_desc *n) { return (int)std::max<int64_t>(1, std::min<int64_t>((n->rows + 15) / 16, 64)); }
@@ -581,6 +584,7 @@ int moe_layer_norm_fwd(const moe_ln_desc *n, const void *x, const float *g, cons
     const LnPlan p = ln_plan(n);
     const LnArgs a{x, g, b, y, stats, n->rows, ln_ldx(n), ln_ldy(n), n->H, n->eps};
     const bool odd = !ln_even(n, x, a.ldx) || !ln_even(n, y, a.ldy) || !all_aligned({g, b});
+    // all that a CU holds: with half of them 16,384 rows of 7168 take 95 us for 79
     const int64_t per_cu = p.wave ? 8 : std::max(1, (p.chunks == 1 && n->x_type != MOE_TYPE_FP32 ? 2048 : 1024) / p.threads);
     const int grid = (int)std::min<int64_t>((n->rows + p.teams - 1) / p.teams, per_cu * device_cus());
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -10,14 +10,22 @@
 // written once.  A thread keeps the same columns for every row it takes, 8 at a time,
 // so gains and biases and the column sums of the gradient stay in its registers.
 // Rows up to 512 elements are taken by a wave or a part of one (64, 32, 16 or 8
-// lanes: no barrier), longer ones by a workgroup.  Up to 8192 elements (one chunk a
-// thread) the loads of the next row (forward: of the two next) are in flight during
-// this row's sums; longer rows are loaded as they come, and gains and biases with them.
+// lanes: no barrier), longer ones by a workgroup, with one, two (past 8192 elements) or
+// four chunks a thread (past 16384).  The loads of the next row (forward, up to two chunks: of the
+// two next) are in flight during this row's sums, and gains and biases stay in
+// registers; of four chunks the gains come with each row, and the backward loads its
+// rows as they come.  Past 8192 elements the column sums have no registers: a second
+// reading makes them.
+//
+// Measured: 57,344 rows of 7168 in bf16 forward 331 us (4.97 TB/s), 16,384 of 7168 backward
+// 140 + 5 (5.0 TB/s); 8,192 of 12,288 forward 65 (190 without the loads ahead and the gains in
+// registers), backward 86 + 45 (213 + 37); 4,096 of 32,768 forward 232 (2.3 TB/s, the gains'
+// L2 traffic twice the row's).  Rows without 16-byte alignment: 16,384 of 7,171
+// forward 106, of 7168 79.
 //
 // Any row length and stride: where H or a stride is not a multiple of 8, or a pointer
 // not of 16 bytes, the last 8 columns of a row start at H - 8 and overlap those before
-// them (ODD: they are counted once and written twice with the same value), and loads
-// are of elements' alignment.
+// them (ODD: they are counted once), and loads are of elements' alignment.
 #pragma once
 
 #include "dense.hpp"
@@ -54,10 +62,10 @@ struct Chunk {
         else
             *reinterpret_cast<u32x4 *>(p) = w;
     }
-    static __device__ __forceinline__ void store_some(char *p, const float (&o)[8], int n) {
+    static __device__ __forceinline__ void store_some(char *p, const float (&o)[8], int from, int to) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < n) reinterpret_cast<uint16_t *>(p)[e] = T::down(o[e]);
+            if (e >= from && e < to) reinterpret_cast<uint16_t *>(p)[e] = T::down(o[e]);
     }
 };
 template <>
@@ -100,10 +108,10 @@ struct Chunk<F32> {
             reinterpret_cast<f32x4 *>(p)[1] = b;
         }
     }
-    static __device__ __forceinline__ void store_some(char *p, const float (&o)[8], int n) {
+    static __device__ __forceinline__ void store_some(char *p, const float (&o)[8], int from, int to) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < n) reinterpret_cast<float *>(p)[e] = o[e];
+            if (e >= from && e < to) reinterpret_cast<float *>(p)[e] = o[e];
     }
 };
 
@@ -163,6 +171,7 @@ struct TeamSum {
 template <int CH, bool ODD, bool BUF>
 struct Columns {
     static_assert(!BUF || !ODD, "raw buffers are of whole chunks");
+    static constexpr bool SHORT = ODD && CH == 1;  // a row may be shorter than a chunk
     int at[CH], skip[CH], H;
     __device__ __forceinline__ Columns(int t, int lanes, int H_) : H(H_) {
 #pragma unroll
@@ -187,16 +196,15 @@ struct Columns {
         }
         if (!some || !p) return;
         const char *q = static_cast<const char *>(p) + elem * C::ES;
-        if (ODD && H < 8) {  // one chunk, which is the row
+        if (SHORT && H < 8) {  // one chunk, which is the row
             c[0].load_some(q, in(0) ? H : 0);
-#pragma unroll
-            for (int i = 1; i < CH; ++i) c[i] = c[0];
         } else {
 #pragma unroll
             for (int i = 0; i < CH; ++i) c[i].template load<ODD>(q + (int64_t)at[i] * C::ES);
         }
     }
-    template <class C>
+    // ONCE: what overlaps is written by the chunk before alone, otherwise twice with the same value
+    template <class C, bool ONCE = false>
     __device__ __forceinline__ void store(int i, void *p, int64_t elem, const float (&v)[8]) const {
         if constexpr (BUF) {
             C::store(raw_buffer(static_cast<char *>(p) + elem * C::ES, (uint32_t)(H * C::ES)), at[i], v);
@@ -204,8 +212,8 @@ struct Columns {
         }
         if (!in(i)) return;
         char *q = static_cast<char *>(p) + (elem + at[i]) * C::ES;
-        if (ODD && H < 8)
-            C::store_some(q, v, H);
+        if ((SHORT && H < 8) || (ODD && ONCE && skip[i]))
+            C::store_some(q, v, ONCE ? skip[i] : 0, H);
         else
             C::template store<ODD>(q, v);
     }
@@ -218,7 +226,7 @@ struct Columns {
         const char *q = reinterpret_cast<const char *>(p);
         if constexpr (BUF)
             c.load(raw_buffer(p, (uint32_t)H * 4), at[i]);
-        else if (ODD && H < 8)
+        else if (SHORT && H < 8)
             c.load_some(q, in(i) ? H : 0);
         else
             c.template load<ODD>(q + (int64_t)at[i] * 4);
@@ -236,8 +244,8 @@ __device__ __forceinline__ void ln_fwd_body(const LnArgs &a, int lanes, float *l
     int64_t row = (int64_t)blockIdx.x * team.teams + team.team;
     const int64_t step = (int64_t)gridDim.x * team.teams;
     if (row >= a.rows) return;  // the whole team, and the whole workgroup where teams meet
-    constexpr int AHEAD = CH == 1 ? 2 : 1;
-    constexpr bool BUF = !WAVE && !ODD;
+    constexpr int AHEAD = CH <= 2 ? 2 : 1;
+    constexpr bool BUF = !WAVE && !ODD, GAINS = CH <= 2;  // GAINS: they stay in registers
     Chunk<TI> c[AHEAD][CH];
     auto fetch = [&](Chunk<TI> (&to)[CH], int64_t r) { col.load(to, a.x, r * a.ldx, r < a.rows); };
     // the stores of a row: y's, and mean and 1 / std by its first thread
@@ -259,30 +267,31 @@ __device__ __forceinline__ void ln_fwd_body(const LnArgs &a, int lanes, float *l
     // later ones', so that the compiler may count on them: it waits for a row's loads and
     // not for the next row's.
 #pragma unroll
-    for (int k = 0; k < (CH == 1 ? AHEAD : 0); ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
         fetch(c[k], row + k * step);
         if constexpr (BUF) {
             const float nothing[8] = {};
             put_stats(0, false, 0.f, 0.f);
-            put(0, false, 0, nothing);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) put(0, false, i, nothing);
         }
     }
-    float g[8], b[8];
-    if (CH == 1) col.vec(0, g, a.g, 1.0f), col.vec(0, b, a.b, 0.0f);
+    float g[GAINS ? CH : 1][8], b[GAINS ? CH : 1][8];
+#pragma unroll
+    for (int i = 0; i < (GAINS ? CH : 0); ++i) col.vec(i, g[i], a.g, 1.0f), col.vec(i, b[i], a.b, 0.0f);
     if constexpr (!WAVE) {
         norm_clear(lds, 96);
         __syncthreads();
     }
     auto one = [&](Chunk<TI> (&cur)[CH]) {
         float x[CH][8], s[1] = {0.f}, s2[2] = {0.f, 0.f};
-        if (CH > 1) fetch(cur, row);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             cur[i].get(x[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[0] += col.counts(i, e) ? x[i][e] : 0.f;
         }
-        if (CH == 1) fetch(cur, row + AHEAD * step);
+        fetch(cur, row + AHEAD * step);
         sum1(s);
         const float m = s[0] * inv_h;
         // the differences' own mean is what the mean of the values lost to rounding
@@ -301,12 +310,13 @@ __device__ __forceinline__ void ln_fwd_body(const LnArgs &a, int lanes, float *l
         put_stats(row, true, m + dm, rstd);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            if (CH > 1) col.vec(i, g, a.g, 1.0f), col.vec(i, b, a.b, 0.0f);
+            const int k = GAINS ? i : 0;
+            if (!GAINS) col.vec(i, g[k], a.g, 1.0f), col.vec(i, b[k], a.b, 0.0f);
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = fmaf((x[i][e] - dm) * rstd, g[e], b[e]);
+            for (int e = 0; e < 8; ++e) o[e] = fmaf((x[i][e] - dm) * rstd, g[k][e], b[k][e]);
             put(row, true, i, o);
-            if (CH > 1) __builtin_amdgcn_sched_barrier(0);  // one chunk's gains in registers at a time
+            if (!GAINS) __builtin_amdgcn_sched_barrier(0);  // one chunk's gains in registers at a time
         }
         row += step;
     };
@@ -329,21 +339,23 @@ __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float
     const float inv_h = 1.0f / (float)a.H;
     int64_t row = (int64_t)blockIdx.x * team.teams + team.team;
     const int64_t step = (int64_t)gridDim.x * team.teams;
-    Chunk<TI> cx[CH], cr[CH];
+    // KEEP: a row's values stay unpacked through its sums, so that the next row's loads may take the chunks' registers
+    constexpr bool KEEP = CH <= 2;
+    Chunk<TI> cx[CH], cr[KEEP ? CH : 1];
     Chunk<TO> cy[CH];
     float mean = 0.f, rstd = 0.f;
     auto fetch = [&](int64_t r) {
         const bool some = r < a.rows;
         col.load(cx, a.x, r * a.ldx, some);
         col.load(cy, k.dy, r * a.ldy, some);
-        // dx may take dres' place: where columns overlap, all of dres is read before any of dx is written
-        if (CH == 1 || ODD) col.load(cr, k.dres, r * a.ldx, some);
+        if constexpr (KEEP) col.load(cr, k.dres, r * a.ldx, some);
         const float2 st = reinterpret_cast<const float2 *>(a.stats)[min(r, a.rows - 1)];
         mean = st.x, rstd = st.y;
     };
-    if (CH == 1) fetch(row);
-    float g[8], dg[8], db[8];
-    if (CH == 1) col.vec(0, g, a.g, 1.0f);
+    if (KEEP) fetch(row);
+    float g[KEEP ? CH : 1][8], dg[8], db[8];
+#pragma unroll
+    for (int i = 0; i < (KEEP ? CH : 0); ++i) col.vec(i, g[i], a.g, 1.0f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[e] = db[e] = 0.f;
     if constexpr (!WAVE) {
@@ -351,56 +363,58 @@ __device__ __forceinline__ void ln_bwd_body(const LnBwdArgs &k, int lanes, float
         __syncthreads();
     }
     for (; row < a.rows; row += step) {
-        if (CH > 1) fetch(row);
-        float xh[8], t[8], res[8], s[2] = {0.f, 0.f};
+        if (!KEEP) fetch(row);
+        float xh[KEEP ? CH : 1][8], t[KEEP ? CH : 1][8], res[KEEP ? CH : 1][8], s[2] = {0.f, 0.f};
         const float m = mean, rs = rstd;
-        // xh and dy g of a chunk; with more than one they are made again for the output
+        // xh and dy g of a chunk; not kept, they are made again for the output
         auto make = [&](int i) {
-            if (CH > 1) col.vec(i, g, a.g, 1.0f);
-            cx[i].get(xh);
-            cy[i].get(t);
+            const int k = KEEP ? i : 0;
+            if (!KEEP) col.vec(i, g[k], a.g, 1.0f);
+            cx[i].get(xh[k]);
+            cy[i].get(t[k]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                xh[e] = (xh[e] - m) * rs;
+                xh[k][e] = (xh[k][e] - m) * rs;
                 if constexpr (SUMS) {
-                    dg[e] = fmaf(t[e], xh[e], dg[e]);
-                    db[e] += t[e];
+                    dg[e] = fmaf(t[k][e], xh[k][e], dg[e]);
+                    db[e] += t[k][e];
                 }
-                t[e] *= g[e];
+                t[k][e] *= g[k][e];
             }
         };
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+            const int k = KEEP ? i : 0;
             make(i);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (col.counts(i, e)) {
-                    s[0] += t[e];
-                    s[1] = fmaf(t[e], xh[e], s[1]);
+                    s[0] += t[k][e];
+                    s[1] = fmaf(t[k][e], xh[k][e], s[1]);
                 }
-            if (CH > 1) __builtin_amdgcn_sched_barrier(0);
+            if (KEEP) cr[k].get(res[k]);
+            if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
-        if (CH == 1) {
-            cr[0].get(res);
-            fetch(row + step);
-        }
+        if (KEEP) fetch(row + step);
         sum(s);
         const float c0 = s[0] * inv_h, c1 = s[1] * inv_h;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            if (CH > 1) {
+            const int q = KEEP ? i : 0;
+            if (!KEEP) {
                 make(i);
-                if (!ODD && k.dres && col.in(i)) cr[i].template load<ODD>(static_cast<const char *>(k.dres) + (row * a.ldx + col.at[i]) * Chunk<TI>::ES);
-                cr[i].get(res);
+                if (k.dres && col.in(i)) cr[0].template load<ODD>(static_cast<const char *>(k.dres) + (row * a.ldx + col.at[i]) * Chunk<TI>::ES);
+                cr[0].get(res[q]);
             }
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                o[e] = rs * (t[e] - fmaf(xh[e], c1, c0));
-                if (k.dres) o[e] += res[e];
+                o[e] = rs * (t[q][e] - fmaf(xh[q][e], c1, c0));
+                if (k.dres) o[e] += res[q][e];
             }
-            col.template store<Chunk<TI>>(i, k.dx, row * a.ldx, o);
-            if (CH > 1) __builtin_amdgcn_sched_barrier(0);
+            // dx may take the place of dres, which the thread of the chunk before may have still to read
+            col.template store<Chunk<TI>, !KEEP>(i, k.dx, row * a.ldx, o);
+            if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
     }
     if constexpr (SUMS) {

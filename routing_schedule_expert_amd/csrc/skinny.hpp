@@ -2,12 +2,17 @@
 // the reading of the weights.
 //
 // A workgroup makes 16 weight rows' products with every row of X: 8 gate rows and the 8
-// up rows that belong to them, or 16 rows of W2.  Its waves share K between them, 64 at a
+// up rows that belong to them, or 16 rows of W2.  Its four waves share K between them, 64 at a
 // time in turn, so that together they read whole runs of a weight row.  Each wave has a
-// ring of LDS stages to itself, filled by buffer loads with the lds bit (DEPTH steps in
-// flight, 128-byte lines of 8 rows to a load) and waited for by count: no wave waits for
+// ring of LDS stages to itself, filled by buffer loads with the lds bit
+// (128-byte lines of 8 rows to a load) and waited for by count: no wave waits for
 // another until the sums of all are added, in ascending order, for the epilogue.
 // v_mfma_f32_16x16x32: the weights are the 16 rows, X's rows the columns.
+//
+// H = 7168, I = 2048, weights from memory: 8 rows 12.4 + 9.3 us (4.7 and 3.2 TB/s, of which
+// some 3.4 us of each launch pass before the first bytes are there), 64 rows 22.9 + 15.2, where each
+// workgroup's reading of X from L2 is four times that of its weights.  Eight waves a workgroup, where
+// there are no more workgroups than CUs, took 13.1 for 12.4, and H = 2048, I = 1024 5.9 for 5.2.
 #pragma once
 
 #include "dense.hpp"
@@ -15,10 +20,13 @@
 
 namespace moe {
 
-constexpr int kSkinnyDepth = 4;
+constexpr int kSkinnyWaves = 4;
+// Stages of a wave's ring: as deep as leaves room for two workgroups on a CU (four stages of 17 to 32 rows 12.2 us in the
+// down product for 10.2, of 33 to 64 rows 17.7 for 15.2).
+constexpr int skinny_depth(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
 constexpr int skinny_stage_bytes(int NT) { return 2048 * (1 + NT); }
 // dynamic LDS: the waves' rings, over which the sums go at the end
-constexpr int skinny_lds(int NT, int waves) { return waves * kSkinnyDepth * skinny_stage_bytes(NT); }
+constexpr int skinny_lds(int NT) { return kSkinnyWaves * skinny_depth(NT) * skinny_stage_bytes(NT); }
 
 struct SkinnyArgs {
     const uint16_t *X, *W;
@@ -30,10 +38,10 @@ struct SkinnyArgs {
     int act;
 };
 
-// 16 NT rows of X at most, NW waves.
-template <class T, int NT, int NW, bool GLU>
+// 16 NT rows of X at most.
+template <class T, int NT, bool GLU>
 __device__ __forceinline__ void skinny_body(const SkinnyArgs &g, uint32_t lds) {
-    constexpr int ND = 2 + 2 * NT, STAGE = skinny_stage_bytes(NT), COLS = GLU ? 8 : 16;
+    constexpr int NW = kSkinnyWaves, DEPTH = skinny_depth(NT), ND = 2 + 2 * NT, STAGE = skinny_stage_bytes(NT), COLS = GLU ? 8 : 16;
     typedef typename T::v8 v8;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * COLS;
@@ -50,7 +58,7 @@ __device__ __forceinline__ void skinny_body(const SkinnyArgs &g, uint32_t lds) {
     const uint32_t wblock = GLU ? 0 : (uint32_t)(16 * g.ldw), wbytes = (uint32_t)(2 * g.ldw) * (uint32_t)(GLU ? 8 : min(16, g.N - n0));
     const uint16_t *w0 = g.W + (int64_t)n0 * g.ldw, *w1 = GLU ? w0 + (int64_t)g.N * g.ldw : w0;
     const int steps = (g.K + kDenseK - 1) / kDenseK, left = g.K - (steps - 1) * kDenseK;
-    const uint32_t ring = lds + wave * (kSkinnyDepth * STAGE);
+    const uint32_t ring = lds + wave * (DEPTH * STAGE);
     auto fill = [&](int step, uint32_t st) {
         const bool in = step < steps;
         if (step == steps - 1 && left < kDenseK) {
@@ -68,7 +76,7 @@ __device__ __forceinline__ void skinny_body(const SkinnyArgs &g, uint32_t lds) {
         for (int i = 0; i < 2 * NT; ++i) dense_dma(rx, st + 2048 + i * 1024, xoff[i & 3] + (so + i * xblock));
     };
 #pragma unroll
-    for (int d = 0; d < kSkinnyDepth; ++d) fill(wave + d * NW, ring + d * STAGE);
+    for (int d = 0; d < DEPTH; ++d) fill(wave + d * NW, ring + d * STAGE);
     f32x4 acc[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -84,8 +92,8 @@ __device__ __forceinline__ void skinny_body(const SkinnyArgs &g, uint32_t lds) {
 #pragma unroll 1
     for (int step = wave; step < steps; step += NW) {
         const uint32_t st = ring + slot * STAGE;
-        slot = slot + 1 == kSkinnyDepth ? 0 : slot + 1;
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kSkinnyDepth - 1) * ND) : "memory");
+        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((DEPTH - 1) * ND) : "memory");
         v8 w[2], x[2][NT];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -96,7 +104,7 @@ __device__ __forceinline__ void skinny_body(const SkinnyArgs &g, uint32_t lds) {
         // the stage is in registers before it is filled again
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        fill(step + kSkinnyDepth * NW, st);
+        fill(step + DEPTH * NW, st);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
