@@ -734,8 +734,9 @@ enum {
  *   dW13 [2I][H], dW2 [H][I] out, each nullable, of dw_type: MOE_TYPE_FP32 or n->type.
  *        accumulate = 1 (fp32 only) adds to what they hold.  Zeros for rows = 0
  *   ws >= moe_gated_ffn_workspace_bytes(n, 1)
- * Outputs must not overlap inputs or each other.  Pointers 16-byte aligned; what lies
- * between rows (ldx, ldo > H) is neither read nor written.  A row's out, HU, A and dX
+ * Outputs must not overlap inputs or each other (dX in the place of X or dOut is refused), and
+ * calls that may run at once, captured graphs among them, need a workspace each.  Pointers
+ * 16-byte aligned; what lies between rows (ldx, ldo > H) is neither read nor written.  A row's out, HU, A and dX
  * depend on that row alone.  Every sum is fp32, in an order that depends on the sizes
  * only: repeated calls give bitwise the same.  fp16 values past 65504 become infinite.
  * The shared expert's gradient: HU and A are moe_layer_fwd_shared's HUs and As, whose padding rows
@@ -778,7 +779,8 @@ int moe_gated_ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_
  *   dres   [rows][H], nullable: what else arrives for x, of its type and stride
  *   dx     [rows][H] out, may be x or dres itself, or dy of the same type and stride
  *   dg, db float [H] out, both or neither NULL (g NULL or not); zeros for rows = 0
- *   ws >= moe_layer_norm_workspace_bytes(n), 16-byte aligned (unused without dg: may be NULL)
+ *   ws >= moe_layer_norm_workspace_bytes(n), 16-byte aligned (unused without dg: may be NULL);
+ *          one for each of the calls that may run at once
  * Rows may start anywhere: pointers, strides and H need only their elements' alignment
  * (g, b, dg, db, stats: 4 bytes, stats 8).  Rows whose starts and lengths are multiples of
  * 8 elements on 16-byte aligned pointers run fastest.  Other overlaps are not allowed; what
@@ -811,11 +813,14 @@ int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, cons
  *   max_norm >= 0, eps >= 0
  *   result  device: sum (of the squares of scale g, or their maximum, in 64 bits: what
  *           ranks that hold shards add up), norm and coef; 8-byte aligned
- *   ws >= moe_grad_workspace_bytes(n), 8-byte aligned
+ *   ws >= moe_grad_workspace_bytes(n), 8-byte aligned; one, and one result, for each of the calls
+ *           that may run at once
  * Squares are summed in 64 bits, in an order that depends on the sizes only.  A NaN
  * gradient makes norm and coef NaN, and all of out; an infinite one makes coef 0, and
  * out 0 but NaN where the gradient is infinite.  The caller who wants such a step
- * skipped reads result.  A norm past fp32's range is infinite there; sum, coef and out still hold.  Gradients that stay as they are (scale coef = 1, out = g) are not written.
+ * skipped reads result.  A norm past fp32's range is infinite
+ * there; sum, coef and out still hold.  Gradients that stay as they are (scale coef = 1, out = g)
+ * are not written.
  *
  * moe_grad_norm — result alone (out is not read).
  * moe_grad_scale — out = (scale *coef) g with a coef (device float) of the caller's, for

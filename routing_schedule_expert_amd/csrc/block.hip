@@ -361,6 +361,9 @@ int ln_check(const moe_ln_desc *n) {
     return MOE_OK;
 }
 
+// Whether the rows of y's side may take the place of those of x's.
+bool ln_same_rows(const moe_ln_desc *n) { return n->x_type == n->y_type && ln_ldx(n) == ln_ldy(n); }
+
 // How a row is shared out.
 struct LnPlan {
     bool wave;
@@ -567,6 +570,7 @@ int moe_gated_ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_
     }
     if (!dOut || !X || !HU || !W13 || !W2 || !ws || !all_aligned({dOut, X, HU, A, W13, W2, dX, ws})) return MOE_EINVAL;
     if (!dX && !dW13 && !dW2) return MOE_EINVAL;
+    if (dX == dOut || dX == X) return MOE_EINVAL;  // what the weights' gradients read beside it
     if ((int64_t)ws_bytes < ffn_ws_bytes(n, true)) return MOE_ENOSPC;
     const int f32 = dw_type == MOE_TYPE_FP32;
     return n->type == MOE_TYPE_BF16 ? ffn_bwd<Bf16>(n, dOut, X, HU, A, W13, W2, dX, dW13, dW2, f32, accumulate, ws, s)
@@ -579,7 +583,8 @@ int moe_layer_norm_fwd(const moe_ln_desc *n, const void *x, const float *g, cons
     const int rc = ln_check(n);
     if (rc != MOE_OK) return rc;
     if (n->rows == 0) return MOE_OK;
-    if (!x || !y || !ln_aligned(x, n->x_type) || !ln_aligned(y, n->y_type) || !aligned4(g) || !aligned4(b) || ((uintptr_t)stats & 7u))
+    if (!x || !y || !ln_aligned(x, n->x_type) || !ln_aligned(y, n->y_type) || !aligned4(g) || !aligned4(b) || ((uintptr_t)stats & 7u) ||
+        (y == x && !ln_same_rows(n)))
         return MOE_EINVAL;
     const LnPlan p = ln_plan(n);
     const LnArgs a{x, g, b, y, stats, n->rows, ln_ldx(n), ln_ldy(n), n->H, n->eps};
@@ -604,7 +609,8 @@ int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (n->rows > 0) {
         if (!x || !stats || !dy || !dx || !ln_aligned(x, n->x_type) || !ln_aligned(dy, n->y_type) || !ln_aligned(dres, n->x_type) ||
-            !ln_aligned(dx, n->x_type) || !aligned4(g) || ((uintptr_t)stats & 7u) || !aligned16(ws))
+            !ln_aligned(dx, n->x_type) || !aligned4(g) || ((uintptr_t)stats & 7u) || !aligned16(ws) ||
+            (dx == dy && !ln_same_rows(n)))
             return MOE_EINVAL;
         if (dg && !ws) return MOE_EINVAL;
         if (dg && (int64_t)ws_bytes < ln_ws_bytes(n)) return MOE_ENOSPC;

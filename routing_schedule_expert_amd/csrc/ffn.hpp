@@ -8,9 +8,15 @@
 //   dX = [dh du] W13;  dW13 = [dh du]^T X;  dW2 = dOut^T a
 //
 // a and [dh du] are operands of matrix products, so they are 16-bit; every sum is fp32.
-// A product with fewer tiles than the device has CUs is cut along K: each part leaves
+// A product with fewer tiles than the device has CUs may be cut along K: each part leaves
 // its fp32 sums in the workspace, and a second pass adds them in ascending order and
 // does the epilogue.
+//
+// Bound by the matrix cores from some hundred rows on (6 I H flop a row forward, 12 backward).
+// H = 7168, I = 2048: 16,384 rows forward 1,133 us (a library's product alone reaches 1.25
+// PFLOP/s here, this 1.27), 8,192 rows backward 1,121 (activations 207, the three gradients in
+// one launch 890).  The backward's products have their operands as they lie, which costs
+// transposing LDS reads and no copy.
 #pragma once
 
 #include "dense.hpp"

@@ -77,6 +77,7 @@ def test_ffn_refusals():
     assert bwd(ffn(), ws=None) == bwd(ffn(), ws=BAD) == EINVAL
     assert bwd(ffn(), ws_bytes=ops.gated_ffn_workspace_bytes(ffn(), True) - 1) == ENOSPC
     assert bwd(ffn(), dX=None, dW13=None, dW2=None) == EINVAL
+    assert bwd(ffn(), dX=P[0]) == bwd(ffn(), dX=P[1]) == EINVAL  # the place of dOut, of X
     assert bwd(ffn(), dw=ops.MOE_TYPE_FP16) == bwd(ffn(), dw=3) == bwd(ffn(), add=2) == EINVAL
     assert bwd(ffn(), dw=ops.MOE_TYPE_BF16, add=1) == EUNSUP
     assert lib.moe_gated_ffn_bwd(ctypes.byref(ffn(rows=0)), *([None] * 9), 2, 1, None, 0, None) == ops.MOE_OK
@@ -104,6 +105,9 @@ def test_ln_sizes_and_refusals():
     odd.x_type = 3
     assert lib.moe_layer_norm_fwd(ctypes.byref(odd), *P[:5], None) == EINVAL
     assert lib.moe_layer_norm_fwd(None, *P[:5], None) == EINVAL
+    for n in (ln(x_dtype=F32, y_dtype=B), ln(ldy=528)):  # rows that do not fit into x's place, dx's into dy's
+        assert lib.moe_layer_norm_fwd(ctypes.byref(n), P[0], P[1], P[2], P[0], P[4], None) == EINVAL
+        assert lib.moe_layer_norm_bwd(ctypes.byref(n), *P[:5], P[3], *P[6:9], 1 << 40, None) == EINVAL
     assert lib.moe_layer_norm_fwd(ctypes.byref(ln(rows=0)), *([None] * 5), None) == ops.MOE_OK
     names = ("x", "g", "b", "y", "stats")
 
