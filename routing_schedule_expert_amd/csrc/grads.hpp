@@ -6,7 +6,8 @@
 // 433 (5.7 TB/s), the scaling 930 (5.3 TB/s read and written).  Squares are summed in 64 bits (no
 // square of an fp32 number overflows or vanishes there), each workgroup's sum in a slot
 // of its own, and the second pass's workgroups each add the slots in one fixed order,
-// so no launch stands between the passes.  A maximum is that of the magnitudes' bits,
+// so no launch stands between the passes (past 2048 slots one workgroup does it: 4,096 slots, read
+// by each of 2048 workgroups, are no longer little).  A maximum is that of the magnitudes' bits,
 // where NaN is above infinity.
 //
 // The tensors of a launch come as its arguments (their addresses may be others in the
