@@ -82,17 +82,18 @@ __device__ __forceinline__ const __attribute__((address_space(4))) L &first_argu
     return *(const __attribute__((address_space(4))) L *)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-__global__ __launch_bounds__(kGradThreads) void k_grad_sums(GradLaunch<kSumTensors, false>, GradScalars k) {
+__global__ __launch_bounds__(kGradThreads) void k_grad_sums(GradLaunch<false>, GradScalars k) {
     __shared__ double lds[kGradThreads / 64];
     if (k.kind == MOE_NORM_MAX)
-        grad_sums_body<true>(first_argument<GradLaunch<kSumTensors, false>>(), k, lds);
+        grad_sums_body<true>(first_argument<GradLaunch<false>>(), k, lds);
     else
-        grad_sums_body<false>(first_argument<GradLaunch<kSumTensors, false>>(), k, lds);
+        grad_sums_body<false>(first_argument<GradLaunch<false>>(), k, lds);
 }
 
-__global__ __launch_bounds__(kGradThreads) void k_grad_scale(GradLaunch<kScaleTensors, true>, GradScalars k) {
+template <bool OUT>
+__global__ __launch_bounds__(kGradThreads) void k_grad_scale(GradLaunch<OUT>, GradScalars k) {
     __shared__ double lds[kGradThreads / 64];
-    grad_scale_body(first_argument<GradLaunch<kScaleTensors, true>>(), k, lds);
+    grad_scale_body<OUT>(first_argument<GradLaunch<OUT>>(), k, lds);
 }
 
 __global__ __launch_bounds__(kGradThreads) void k_grad_result(GradScalars k) {
@@ -123,9 +124,14 @@ int up_to(int64_t n, int d) { return (int)((n + d - 1) / d); }
 enum DenseTile { kTileL, kTileS2, kTileS, kTileX, kTiles };
 struct DenseShape {
     int mi, ni, stages, per_cu;
-    float step, ends;  // us: a step of 64 k with every CU at work, and what a tile takes besides
+    // us: a step of 64 k with every CU at work and what a tile takes besides: of one product, and among the gradients'
+    // (whose transposing reads cost small tiles more, while their ends lie beside other tiles' steps)
+    float step[2], ends[2];
 };
-constexpr DenseShape kShape[kTiles] = {{4, 4, 0, 1, 1.4f, 9.f}, {2, 2, 0, 2, 0.85f, 6.f}, {2, 2, 5, 1, 0.42f, 6.f}, {1, 2, 6, 1, 0.3f, 5.f}};
+constexpr DenseShape kShape[kTiles] = {{4, 4, 0, 1, {1.4f, 1.4f}, {9.f, 8.5f}},
+                                        {2, 2, 0, 2, {0.85f, 0.85f}, {6.f, 3.7f}},
+                                        {2, 2, 5, 1, {0.42f, 0.5f}, {6.f, 3.6f}},
+                                        {1, 2, 6, 1, {0.3f, 0.35f}, {5.f, 2.7f}}};
 
 // A product: its sizes (GLU: N of a, B has 2 N rows), its tiles and its cut along K.
 struct DensePlan {
@@ -142,11 +148,14 @@ DensePlan dense_product(int M, int N, int K, bool glu = false) { return DensePla
 // estimated from a step's and a tile's measured ones (kShape) for each choice.  One product
 // goes in rounds of the tiles that the CUs hold, where a CU with one of its two tiles
 // takes 0.6 of the time; several, by the sum of their tiles' times and part of the
-// longest's.  A cut costs the second pass (kJoin and the parts' bytes).  Measured against the
+// longest's.  A cut costs the second pass (kJoin and the parts' bytes); one product's stays within one round, of
+// several a long one (X's gradient of few rows) is cut among the others' many short tiles.  Measured against the
 // others forced, us, 256 x 256 / 128 x 128 shared / alone / 64 x 128, taken in brackets:
 // up of 333 rows (H 1032, I 520) 30 / 13 / 13 / [10], of 1,021 (2056, 1032) 55 / 27 / [25] / 36, of 600
 // (4096, 4096) 87 / [56] / 69 / 75, of 3,000 (2048, 1024) 54 / [34] / 40 / 46, of 8,192 (7168, 2048) [366] / 460; of 128
-// rows (7168, 2048) uncut 125 / 60 / 48 / 37, in four parts of K [16 + 5].  A 128 x 256 tile was
+// rows (7168, 2048) uncut 125 / 60 / 48 / 37, in four parts of K [16 + 5]; gradients of 256 rows (4096, 4096) uncut
+// 170 / 121 / 99 / 121, in four parts 70 / [66] / 85 / 124 and 6 for the join, of 1,024 (7168, 2048) [149] / 155 / 185 / 280,
+// of 8,192 (2048, 1024) 179 / [163] / 191 / 282.  A 128 x 256 tile was
 // never ahead of the better of its neighbours by more than 6%.
 DenseTile dense_plan(DensePlan *p, int n) {
     constexpr float kJoin = 5.f, kPerMiB = 0.4f;
@@ -170,13 +179,13 @@ DenseTile dense_plan(DensePlan *p, int n) {
                 q[i].splits = up_to(all, q[i].steps);
                 if (q[i].splits == 1) q[i].steps = all;
                 useful |= q[i].splits > 1;
-                const float one = q[i].steps * k.step + k.ends;
+                const float one = q[i].steps * k.step[n > 1] + k.ends[n > 1];
                 sum += one * q[i].blocks();
                 most = std::max(most, one);
                 blocks += q[i].blocks();
                 if (q[i].splits > 1) join += kJoin + kPerMiB * (float)(q[i].part_bytes() >> 20);
             }
-            if (!useful || (cut > 1 && blocks > kCus * k.per_cu)) break;
+            if (!useful || (n == 1 && cut > 1 && blocks > kCus * k.per_cu)) break;
             const int room = kCus * k.per_cu;
             const int rest = blocks % room;
             float time = join;
@@ -437,12 +446,11 @@ int ln_typed(const moe_ln_desc *n, bool odd, F &&f) {
 // Gradients.
 // ---------------------------------------------------------------------------
 
-int64_t grad_pieces_of(int64_t n, int elems) { return (n + elems - 1) / elems; }
 // few elements (up to what a launch's workgroups take in one small piece each): small pieces
-int grad_elems(const moe_grad *t, int32_t n) {
+int grad_shift(const moe_grad *t, int32_t n) {
     int64_t all = 0;
     for (int i = 0; i < n; ++i) all += t[i].numel;
-    return all <= (int64_t)kGradParts * kGradPieceFew ? kGradPieceFew : kGradPiece;
+    return all <= (int64_t)kGradParts << kGradShiftFew ? kGradShiftFew : kGradShift;
 }
 
 int grad_check(const moe_grad *t, int32_t n, bool out) {
@@ -454,6 +462,7 @@ int grad_check(const moe_grad *t, int32_t n, bool out) {
         if (k.numel >= (1ll << 44)) return MOE_EUNSUPPORTED;
         if (k.numel == 0) continue;
         if (!k.g || !ln_aligned(k.g, k.type) || (out && (!k.out || !ln_aligned(k.out, k.type)))) return MOE_EINVAL;
+        if ((uint64_t)(uintptr_t)k.g >> 48) return MOE_EUNSUPPORTED;
         all += k.numel;
         if (all >= (1ll << 44)) return MOE_EUNSUPPORTED;
     }
@@ -463,36 +472,33 @@ bool grad_scalars_ok(int32_t kind, float scale, float max_norm, float eps) {
     return (kind == MOE_NORM_L2 || kind == MOE_NORM_MAX) && scale == scale && max_norm >= 0.f && eps >= 0.f;
 }
 
-// Tensors [*at, ...) that a launch takes, as many as fit; false when none is left.
-template <int N, bool OUT>
-bool grad_fill(GradLaunch<N, OUT> &l, const moe_grad *t, int32_t n, int32_t *at, int elems) {
+// Tensors [*at, n) that a launch takes, as many as fit; false when none is left.
+template <bool OUT>
+bool grad_fill(GradLaunch<OUT> &l, const moe_grad *t, int32_t n, int32_t *at, int shift) {
     l.count = 0;
-    l.elems = elems;
+    l.shift = shift;
     int64_t pieces = 0;
-    while (*at < n && l.count < N) {
+    for (; *at < n && l.count < l.N; ++*at) {
         const moe_grad &k = t[*at];
-        if (k.numel) {
-            const int64_t p = grad_pieces_of(k.numel, elems);
-            l.t[l.count] = GradTensor{k.g, k.numel << 2 | k.type};
-            if constexpr (OUT) l.out[l.count] = k.out;
-            l.piece[l.count++] = (int32_t)pieces;
-            pieces += p;
-        }
-        ++*at;
+        if (!k.numel) continue;
+        if constexpr (OUT) l.out[l.count] = k.out;
+        l.start[l.count] = (int32_t)pieces;
+        l.t[l.count++] = grad_tensor(k.g, k.numel, k.type);
+        pieces += (k.numel + (1ll << shift) - 1) >> shift;
     }
-    l.piece[l.count] = (int32_t)pieces;
+    l.pieces = (int32_t)pieces;
     return l.count > 0;
 }
 
-int grad_launches(int32_t n) { return (n + kSumTensors - 1) / kSumTensors; }
+int grad_launches(int32_t n) { return (n + kGradTensors - 1) / kGradTensors; }
 int64_t grad_ws_bytes(int32_t n) { return 8ll * kGradParts * std::max(1, grad_launches(n)); }
 
 int launch_grad_sums(const moe_grad *t, int32_t n, GradScalars &k, hipStream_t s) {
     double *parts = k.parts;
-    GradLaunch<kSumTensors, false> l;
-    const int elems = grad_elems(t, n);
-    for (int32_t at = 0; grad_fill(l, t, n, &at, elems);) {
-        const int grid = std::min(l.piece[l.count], kGradParts);
+    GradLaunch<false> l;
+    const int shift = grad_shift(t, n);
+    for (int32_t at = 0; grad_fill(l, t, n, &at, shift);) {
+        const int grid = std::min(l.pieces, kGradParts);
         GradScalars a = k;
         a.parts = parts;
         {
@@ -512,23 +518,29 @@ int launch_grad_result(const GradScalars &k, hipStream_t s) {
     return launch_status();
 }
 
-int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s) {
-    GradLaunch<kScaleTensors, true> l;
-    const int elems = grad_elems(t, n);
+template <bool OUT>
+int launch_grad_scale_as(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s) {
+    GradLaunch<OUT> l;
+    const int shift = grad_shift(t, n);
     // from the last tensors to the first, as within a launch: the cache holds what was read last
     for (int32_t end = n; end > 0;) {
         int32_t begin = end, taken = 0;
-        while (begin > 0 && taken < kScaleTensors) taken += t[--begin].numel > 0;
+        while (begin > 0 && taken < l.N) taken += t[--begin].numel > 0;
         int32_t at = begin;
-        if (grad_fill(l, t, end, &at, elems)) {
-            const int grid = (int)std::min<int64_t>(l.piece[l.count], 8 * device_cus());
+        if (grad_fill(l, t, end, &at, shift)) {
+            const int grid = std::min(l.pieces, 8 * device_cus());
             TraceScope tr("grad_scale", s);
-            hipLaunchKernelGGL(k_grad_scale, dim3(grid), dim3(kGradThreads), 0, s, l, k);
+            hipLaunchKernelGGL(k_grad_scale<OUT>, dim3(grid), dim3(kGradThreads), 0, s, l, k);
             if (launch_status() != MOE_OK) return MOE_EHIP;
         }
         end = begin;
     }
     return MOE_OK;
+}
+int launch_grad_scale(const moe_grad *t, int32_t n, const GradScalars &k, hipStream_t s) {
+    bool own = true;
+    for (int32_t i = 0; i < n; ++i) own &= t[i].numel == 0 || t[i].out == t[i].g;
+    return own ? launch_grad_scale_as<false>(t, n, k, s) : launch_grad_scale_as<true>(t, n, k, s);
 }
 
 }  // namespace

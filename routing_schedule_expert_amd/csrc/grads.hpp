@@ -3,7 +3,7 @@
 //   norm = |s| sqrt(sum of squares)  or  |s| max,   c = min(1, max_norm / (norm + eps)),   out = (s c) g
 //
 // Two passes over the gradients, bound by memory: 480 fp32 tensors of 2.5 GB take 1,393 us, the sums
-// 433 (5.7 TB/s), the scaling 930 (5.3 TB/s read and written).  Squares are summed in 64 bits (no
+// 430 to 500 (5 to 5.8 TB/s), the scaling 900 to 940 (5.3 TB/s read and written).  Squares are summed in 64 bits (no
 // square of an fp32 number overflows or vanishes there), each workgroup's sum in a slot
 // of its own, and the second pass's workgroups each add the slots in one fixed order,
 // so no launch stands between the passes (past 2048 slots one workgroup does it: 4,096 slots, read
@@ -23,21 +23,33 @@ namespace moe {
 constexpr int kGradThreads = 512;
 // Elements of a piece: 16384 stream best (2.5 GB), but leave most CUs without one where there
 // are few (5 tensors of 100,000 elements: 9 pieces of 16384, 51 of 2048).
-constexpr int kGradPiece = 16384, kGradPieceFew = 2048;
+constexpr int kGradShift = 14, kGradShiftFew = 11;  // a piece has 2^shift elements
 constexpr int kGradParts = 2048;    // workgroups of a launch of the first pass at most
-constexpr int kSumTensors = 176, kScaleTensors = 128;  // per launch: arguments below 4 KiB
+// Tensors per launch: arguments below 4 KiB.  Where each is scaled in its own place the second pass needs no more of
+// them than the first.
+constexpr int kGradTensors = 248, kGradTensorsOut = 160;
 
+// A tensor in 12 bytes: address (48 bits), elements (44) and type (2, above).
 struct GradTensor {
-    const void *g;
-    int64_t n;  // elements << 2 | type
+    uint32_t w[3];
 };
-template <int N, bool OUT>
+inline GradTensor grad_tensor(const void *g, int64_t n, int type) {
+    const uint64_t p = (uint64_t)(uintptr_t)g;
+    return GradTensor{{(uint32_t)p, (uint32_t)(p >> 32) | (uint32_t)n << 16, (uint32_t)((uint64_t)n >> 16) | (uint32_t)type << 28}};
+}
+template <class K>  // of an argument, which lies in an address space of its own
+__device__ __forceinline__ const void *grad_address(const K &t) { return (const void *)(uintptr_t)((uint64_t)t.w[0] | (uint64_t)(t.w[1] & 0xffffu) << 32); }
+template <class K>
+__device__ __forceinline__ int64_t grad_numel(const K &t) { return (int64_t)((uint64_t)(t.w[1] >> 16) | (uint64_t)(t.w[2] & 0x0fffffffu) << 16); }
+
+template <bool OUT>
 struct GradLaunch {
+    static constexpr int N = OUT ? kGradTensorsOut : kGradTensors;
     GradTensor t[N];
-    void *out[OUT ? N : 1];
-    int32_t piece[N + 1];  // each tensor's first piece; piece[count]: all of them
-    int32_t count;
-    int32_t elems;  // of a piece
+    int32_t start[N];        // each tensor's first piece
+    void *out[OUT ? N : 1];  // without OUT: the tensors themselves
+    int32_t count, pieces;
+    int32_t shift;
 };
 struct GradScalars {
     double *parts;
@@ -132,32 +144,41 @@ __device__ __forceinline__ double grad_join(const GradSum<MAX> &acc, double *lds
     return r;
 }
 
-// f(tensor, type, from, to) of the workgroup's pieces: every gridDim.x-th.
+// f(tensor, address, type, from, to) of the workgroup's pieces: every gridDim.x-th.  Each lane holds the starts of
+// some tensors, and a piece's tensor, the last one that starts at or before it, is a count of ballots.  (A walk
+// along the starts, one load after the other, took 405 tensors of 3.7 M elements 70 us for 24.)
 template <class L, class F>
 __device__ __forceinline__ void grad_pieces(const L &l, bool backwards, F &&f) {
-    const int all = l.piece[l.count];
-    int t = backwards ? l.count - 1 : 0;
+    constexpr int N = (L::N + 63) / 64;
+    const int lane = threadIdx.x & 63, all = l.pieces;
+    int start[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) start[k] = k * 64 + lane < l.count ? l.start[k * 64 + lane] : 0x7fffffff;
     for (int i = blockIdx.x; i < all; i += gridDim.x) {
         const int c = backwards ? all - 1 - i : i;
-        if (backwards)
-            while (l.piece[t] > c) --t;
-        else
-            while (l.piece[t + 1] <= c) ++t;
-        const int64_t n = l.t[t].n >> 2, e0 = (int64_t)(c - l.piece[t]) * l.elems;
-        f(t, (int)(l.t[t].n & 3), e0, min(n, e0 + l.elems));
+        int t = -1, first = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int n = __popcll(__ballot(start[k] <= c));
+            if (n) first = __builtin_amdgcn_readlane(start[k], n - 1);
+            t += n;
+        }
+        const auto &g = l.t[t];
+        const int64_t e0 = (int64_t)(c - first) << l.shift;
+        f(t, grad_address(g), (int)(g.w[2] >> 28), e0, min(grad_numel(g), e0 + (1ll << l.shift)));
     }
 }
 
 template <bool MAX, class L>
 __device__ __forceinline__ void grad_sums_body(const L &l, const GradScalars &k, double *lds) {
     GradSum<MAX> acc;
-    grad_pieces(l, false, [&](int t, int type, int64_t e0, int64_t e1) {
+    grad_pieces(l, false, [&](int, const void *g, int type, int64_t e0, int64_t e1) {
         if (type == MOE_TYPE_FP32)
-            grad_sum_piece<F32>(l.t[t].g, e0, e1, acc);
+            grad_sum_piece<F32>(g, e0, e1, acc);
         else if (type == MOE_TYPE_BF16)
-            grad_sum_piece<Bf16>(l.t[t].g, e0, e1, acc);
+            grad_sum_piece<Bf16>(g, e0, e1, acc);
         else
-            grad_sum_piece<Fp16>(l.t[t].g, e0, e1, acc);
+            grad_sum_piece<Fp16>(g, e0, e1, acc);
     });
     const double s = grad_join(acc, lds);
     if (threadIdx.x == 0) k.parts[blockIdx.x] = s;
@@ -244,7 +265,7 @@ __device__ __forceinline__ void grad_scale_piece(const void *g, void *out, int64
 }
 
 // Backwards: what the first pass read last is what the cache still holds.
-template <class L>
+template <bool OUT, class L>
 __device__ __forceinline__ void grad_scale_body(const L &l, const GradScalars &k, double *lds) {
     float f;
     if (k.coef) {
@@ -254,15 +275,16 @@ __device__ __forceinline__ void grad_scale_body(const L &l, const GradScalars &k
         if (blockIdx.x == 0 && threadIdx.x == 0) *k.result = r;
         f = k.scale * r.coef;
     }
-    grad_pieces(l, true, [&](int t, int type, int64_t e0, int64_t e1) {
-        const void *g = l.t[t].g;
-        if (f == 1.0f && g == l.out[t]) return;
+    if (!OUT && f == 1.0f) return;
+    grad_pieces(l, true, [&](int t, const void *g, int type, int64_t e0, int64_t e1) {
+        void *out = OUT ? l.out[t] : const_cast<void *>(g);
+        if (OUT && f == 1.0f && g == out) return;
         if (type == MOE_TYPE_FP32)
-            grad_scale_piece<F32>(g, l.out[t], e0, e1, f);
+            grad_scale_piece<F32>(g, out, e0, e1, f);
         else if (type == MOE_TYPE_BF16)
-            grad_scale_piece<Bf16>(g, l.out[t], e0, e1, f);
+            grad_scale_piece<Bf16>(g, out, e0, e1, f);
         else
-            grad_scale_piece<Fp16>(g, l.out[t], e0, e1, f);
+            grad_scale_piece<Fp16>(g, out, e0, e1, f);
     });
 }
 

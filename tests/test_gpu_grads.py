@@ -89,7 +89,7 @@ def test_neighbours_in_one_word():
     assert torch.equal(flat, (keep.float() * f).bfloat16())
 
 
-@pytest.mark.parametrize("count", [0, 1, 127, 128, 129, 177, 400])
+@pytest.mark.parametrize("count", [0, 1, 127, 128, 129, 177, 192, 247, 248, 249, 400, 641])
 def test_many_tensors(count):
     grads = [rand(1 + (37 * i) % 3000, DT[i % 3], i) for i in range(count)]
     check(grads, "l2", 0.7)
@@ -203,3 +203,13 @@ def test_lists_that_do_not_fit():
     for kw in (dict(max_norm=-1.0), dict(max_norm=float("nan")), dict(max_norm=1.0, eps=-1.0), dict(max_norm=1.0, kind=2), dict(max_norm=1.0, scale=float("nan"))):
         with pytest.raises(ops.MoeError):
             ops.grad_clip(ops.make_grad_list([t]), **kw)
+
+
+@pytest.mark.parametrize("count", [160, 161, 385])
+def test_many_tensors_elsewhere(count):
+    grads = [rand(1 + (37 * i) % 3000, DT[i % 3], i) for i in range(count)]
+    keep, out = [t.clone() for t in grads], [torch.empty_like(t) for t in grads]
+    gl = ops.grad_clip(ops.make_grad_list(grads, out), 0.7)
+    f = gl.coef.clone()
+    for g, k, o in zip(grads, keep, out):
+        assert torch.equal(g, k) and torch.equal(o, (k.float() * f).to(k.dtype))
