@@ -825,7 +825,8 @@ int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, cons
  * moe_grad_norm — result alone (out is not read).
  * moe_grad_scale — out = (scale *coef) g with a coef (device float) of the caller's, for
  * instance of a sum over ranks.
- * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for 2^44 elements or more in all.
+ * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for 2^44 elements or more in all, or a gradient
+ * past address 2^48.
  */
 enum {
     MOE_NORM_L2 = 0,

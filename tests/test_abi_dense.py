@@ -154,7 +154,7 @@ def test_grad_refusals():
     assert calls(table(good), -1) == calls(None, 1) == [EINVAL] * 2
     for bad, code in (((None, 0x20000, 100, 2, 0), EINVAL), ((0x10002, 0x20000, 100, 2, 0), EINVAL), ((0x10001, 0x20000, 100, 0, 0), EINVAL),
                       ((0x10000, 0x20000, -1, 2, 0), EINVAL), ((0x10000, 0x20000, 100, 3, 0), EINVAL), ((0x10000, 0x20000, 100, 2, 1), EINVAL),
-                      ((0x10000, 0x20000, 1 << 44, 2, 0), EUNSUP)):
+                      ((0x10000, 0x20000, 1 << 44, 2, 0), EUNSUP), ((1 << 48, 0x20000, 100, 2, 0), EUNSUP)):
         assert calls(table(good, bad), 2) == [code] * 2, bad
         assert lib.moe_grad_scale(table(good, bad), 2, P[0], 1.0, None) == code
     half = (1 << 43)
