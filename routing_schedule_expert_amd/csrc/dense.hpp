@@ -37,6 +37,7 @@
 namespace moe {
 
 struct Bf16 {
+    static constexpr bool kNarrow = false;  // fp32 values may lie past its range
     typedef __bf16 v8 __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -56,6 +57,7 @@ struct Bf16 {
     static __device__ __forceinline__ float up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 };
 struct Fp16 {
+    static constexpr bool kNarrow = true;
     typedef _Float16 v8 __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -153,7 +153,12 @@ struct GluOut {
     }
 };
 
-// v = dA: [dh du] from the h and u kept; a again for dW2 where it was not kept
+// x times a kept value, where an infinite one is a number past its type's range: 0 by it is 0.
+__device__ __forceinline__ float by_kept(float x, float kept) { return x == 0.f && __builtin_isinf(kept) ? 0.f : x * kept; }
+
+// v = dA: [dh du] from the h and u kept; a again for dW2 where it was not kept.
+// In fp16, h and u past 65504 were kept as infinities.  The activation and its slope are at their limits there (0, 0 below;
+// h, 1 above), and what a 0 multiplies stays 0, as it was in the forward's fp32.
 template <class T>
 struct GluBwdOut {
     const uint16_t *HU;
@@ -172,12 +177,24 @@ struct GluBwdOut {
         float h[8], u[8], a[8], d[8];
         unpack8<T>(k.h, h);
         unpack8<T>(k.u, u);
-        activation<true>(act, h, a, d);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = T::kNarrow && __builtin_isinf(h[e]) ? copysignf(65504.f, h[e]) : h[e];
+        activation<true>(act, x, a, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            d[e] *= v[e] * u[e];
-            h[e] = v[e] * a[e];
-            a[e] *= u[e];
+            if constexpr (T::kNarrow) {
+                const bool far = __builtin_isinf(u[e]);
+                a[e] = h[e] == __builtin_inff() ? h[e] : a[e];
+                const float t = by_kept(v[e], u[e]);
+                d[e] = far && d[e] == 0.f && t == t ? 0.f : d[e] * t;
+                h[e] = by_kept(v[e], a[e]);
+                a[e] = far ? by_kept(a[e], u[e]) : by_kept(u[e], a[e]);
+            } else {
+                d[e] *= v[e] * u[e];
+                h[e] = v[e] * a[e];
+                a[e] *= u[e];
+            }
         }
         uint16_t *o = dHU + r * 2 * I + c;
         store16(o, pack8<T>(d));

@@ -363,3 +363,53 @@ def test_tensors_that_do_not_fit():
         ops.moe_gated_ffn_bwd(n, c["dOut"], c["X"], b.HU, b.A, c["W13"], c["W2"], g.dX, g.dW13.bfloat16(), g.dW2.bfloat16(), g.ws, True)
     with pytest.raises(ops.MoeError):
         ops.moe_gated_ffn_bwd(n, c["dOut"], c["X"], b.HU, b.A, c["W13"], c["W2"], g.dX, g.dW13, g.dW2, g.ws[:16])
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("kind", list(ACTS))
+def test_fp16_values_kept_as_infinities(kind, given):
+    # h and u past 65504 lie in HU as infinities, which stand for numbers: where the slope or the value is 0, or nothing
+    # arrives, their products are 0.  The reference has 200 in their place, where each activation is at its limits in 64 bits.
+    I, f16 = 40, torch.float16
+    c = make(80, 72, I, kind, f16)
+    HU, A = kept(c)
+    inf = float("inf")
+    HU[3, 5], HU[3, I + 5] = -inf, 0.01
+    HU[4, 6], HU[4, I + 6] = -inf, -inf
+    HU[5, 7], HU[5, I + 7] = -inf, inf
+    HU[6, 8], HU[6, I + 8] = inf, 0.01
+    HU[7, 9], HU[7, I + 9] = inf, inf  # a row that nothing arrives for
+    HU[7, 10], HU[7, I + 10] = 1.0, inf
+    A[torch.tensor([3, 4, 5], device=dev()), torch.tensor([5, 6, 7], device=dev())] = 0.0
+    A[6, 8], A[7, 9:11] = 700.0, 3.0
+    c["dOut"][7] = 0.0
+    b = ops.alloc_gated_ffn_bwd(c["n"], dev())
+    ops.gated_ffn_bwd(c["n"], c["dOut"], c["X"], HU, A if given else None, c["W13"], c["W2"], b)
+    ref = HU.double().nan_to_num(posinf=200.0, neginf=-200.0)
+    (dX, eX), (dW13, e13), (dW2, e2) = backward64(c, ref, A, given)
+    rows = torch.arange(80, device=dev()) != 6  # du there is infinite, as h is
+    near("dX", b.dX[rows], dX[rows], eX[rows])
+    rows = torch.arange(2 * I, device=dev()) != I + 8
+    near("dW13", b.dW13[rows], dW13[rows], e13[rows])
+    assert not bool(b.dX[6].isfinite().any()) and not bool(b.dW13[I + 8].isfinite().any())
+    cols = torch.tensor([k for k in range(I) if given or k not in (8, 9, 10)], device=dev())  # a there is infinite too
+    near("dW2", b.dW2[:, cols], dW2[:, cols], e2[:, cols])
+    # NaN is no such number
+    HU[9, 5], HU[10, I + 5], HU[10, 5] = float("nan"), float("nan"), -inf
+    ops.gated_ffn_bwd(c["n"], c["dOut"], c["X"], HU, A if given else None, c["W13"], c["W2"], b)
+    assert bool(b.dX[10].isnan().all()) and (kind == "relu" or bool(b.dX[9].isnan().all()))
+
+
+@pytest.mark.parametrize("kind", list(ACTS))
+def test_fp16_gradient_of_a_finite_forward(kind):
+    # one gate argument of -70,000: the forward's outputs are finite, and so is what its HU gives
+    c = make(70, 72, 40, kind, torch.float16)
+    c["X"][11, 3], c["W13"][17, 3] = 250.0, -280.0
+    b = fwd(c)
+    assert float(b.HU[11, 17]) == -float("inf") and float(b.A[11, 17]) == 0.0 and bool(b.out.isfinite().all())
+    c["dOut"][11] /= 64
+    for A in (b.A, None):
+        g = ops.alloc_gated_ffn_bwd(c["n"], dev())
+        ops.gated_ffn_bwd(c["n"], c["dOut"], c["X"], b.HU, A, c["W13"], c["W2"], g)
+        for name, got, (ref, err) in zip(("dX", "dW13", "dW2"), (g.dX, g.dW13, g.dW2), backward64(c, b.HU.double().nan_to_num(neginf=-200.0), b.A, A is not None)):
+            near(name, got, ref, err)
