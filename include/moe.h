@@ -808,16 +808,16 @@ int moe_layer_norm_bwd(const moe_ln_desc *n, const void *x, const float *g, cons
  *     coef = min(1, max_norm / (norm + eps)) (1 where both are 0),   out = (scale coef) g, rounded once
  *   t, n    host array of n (>= 0) tensors: g, out (g itself, or a buffer that overlaps no
  *           gradient and no other out), numel (>= 0), type (MOE_TYPE_*; of both).  No two
- *           gradients overlap.  Element alignment is enough (whole 16-byte words are read, of
- *           which a neighbour's elements are left out and never written); out of the alignment
- *           of g (modulo 16) runs fastest.  Read during the call only, and not kept
+ *           gradients overlap.  Element alignment is enough (the scaling reads whole 16-byte
+ *           words, of which a neighbour's elements are left out and never written); g on 16 bytes and
+ *           out of its alignment run fastest.  The table is read during the call only, and not kept
  *   scale   applied before the norm (1 / ranks, 1 / loss scale)
  *   max_norm >= 0, eps >= 0
  *   result  device: sum (of the squares of scale g, or their maximum, in 64 bits: what
  *           ranks that hold shards add up), norm and coef; 8-byte aligned
  *   ws >= moe_grad_workspace_bytes(n), 8-byte aligned; one, and one result, for each of the calls
  *           that may run at once
- * Squares are summed in 64 bits, in an order that depends on the sizes only.  A NaN
+ * Squares are summed in 64 bits, in an order that depends on the sizes only: not on where the gradients lie.  A NaN
  * gradient makes norm and coef NaN, and all of out; an infinite one makes coef 0, and
  * out 0 but NaN where the gradient is infinite.  The caller who wants such a step
  * skipped reads result.  A norm past fp32's range is infinite

@@ -12,8 +12,8 @@
 //
 // The tensors of a launch come as its arguments (their addresses may be others in the
 // next call).  They are cut into pieces, dealt to the workgroups in turn;
-// loads are of whole aligned 16-byte words, the neighbours' elements
-// in a tensor's first and last word left out.
+// loads are of 16 bytes: the sums' from a tensor's own start, the scaling's of whole aligned words, the
+// neighbours' elements in a tensor's first and last word left out.
 #pragma once
 
 #include "dense.hpp"
@@ -89,39 +89,41 @@ struct GradSum {
 typedef __attribute__((address_space(1))) u32x4 global_u32x4;
 __device__ __forceinline__ const global_u32x4 *grad_words(const void *g) { return (const global_u32x4 *)((uintptr_t)g & ~(uintptr_t)15); }
 
-// Elements [e0, e1) of the tensor at g.
+// 16 bytes of a tensor's elements, wherever it starts.
+struct __attribute__((packed, aligned(2))) GradLoose {
+    u32x4 v;
+};
+typedef __attribute__((address_space(1))) GradLoose global_loose;
+
+// Elements [e0, e1) of the tensor at g; e0 is a piece's first.  Words are counted from the tensor's own start, so that which
+// thread adds which elements, and with it the sum's last bits, does not hang on the address.
 template <class T, bool MAX>
 __device__ __forceinline__ void grad_sum_piece(const void *g, int64_t e0, int64_t e1, GradSum<MAX> &acc) {
     constexpr int N = GradVec<T>::N, ES = 16 / N;
-    // word w holds elements w N - lead ... of the tensor
-    const int lead = (int)(((uintptr_t)g & 15) / ES);
-    const global_u32x4 *p = grad_words(g);
-    const int64_t a = e0 + lead, b = e1 + lead;  // in the words' own count
-    const int64_t w0 = a / N, w1 = (b + N - 1) / N;
-    const int64_t in0 = (a + N - 1) / N, in1 = b / N;  // whole words
+    const global_loose *p = (const global_loose *)(uintptr_t)g;
+    const int64_t w0 = e0 / N, w1 = e1 / N;  // whole words
     auto whole = [&](u32x4 v) {
 #pragma unroll
         for (int i = 0; i < N; ++i) acc.add(GradVec<T>::get(v, i));
     };
     constexpr int U = 4;
-    int64_t w = in0 + threadIdx.x;
-    for (; w + (U - 1) * kGradThreads < in1; w += U * kGradThreads) {
+    int64_t w = w0 + threadIdx.x;
+    for (; w + (U - 1) * kGradThreads < w1; w += U * kGradThreads) {
         u32x4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = p[w + u * kGradThreads];
+        for (int u = 0; u < U; ++u) v[u] = p[w + u * kGradThreads].v;
 #pragma unroll
         for (int u = 0; u < U; ++u) whole(v[u]);
     }
-    for (; w < in1; w += kGradThreads) whole(p[w]);
-    // at most one word at each end
-    auto part = [&](int64_t k) {
-        const u32x4 v = p[k];
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (k * N + i >= a && k * N + i < b) acc.add(GradVec<T>::get(v, i));
-    };
-    if (threadIdx.x == 0 && w0 < in0) part(w0);
-    if (threadIdx.x == 64 && in1 < w1 && (in1 > w0 || w0 >= in0)) part(in1);
+    for (; w < w1; w += kGradThreads) whole(p[w].v);
+    if (threadIdx.x == 64) {  // what is left of the tensor's last word
+        for (int64_t e = w1 * N; e < e1; ++e) {
+            if constexpr (ES == 4)
+                acc.add(((const __attribute__((address_space(1))) float *)(uintptr_t)g)[e]);
+            else
+                acc.add(T::up(((const __attribute__((address_space(1))) uint16_t *)(uintptr_t)g)[e]));
+        }
+    }
 }
 
 // A workgroup's sum, on thread 0.
@@ -234,10 +236,6 @@ __device__ __forceinline__ void grad_scale_piece(const void *g, void *out, int64
         return r;
     };
     // whole words of g are words of out where both start alike, and 16 bytes of any alignment otherwise
-    struct __attribute__((packed, aligned(2))) Loose {
-        u32x4 v;
-    };
-    typedef __attribute__((address_space(1))) Loose global_loose;
     auto put = [&](int64_t w, u32x4 v) { ((global_loose *)(o + (w * N - lead) * ES))->v = v; };
     constexpr int U = 4;
     int64_t w = in0 + threadIdx.x;

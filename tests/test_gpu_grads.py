@@ -213,3 +213,17 @@ def test_many_tensors_elsewhere(count):
     f = gl.coef.clone()
     for g, k, o in zip(grads, keep, out):
         assert torch.equal(g, k) and torch.equal(o, (k.float() * f).to(k.dtype))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_the_sum_does_not_depend_on_where_gradients_lie(dtype, kind):
+    # the same values at every start of a 16-byte word: one order of additions, so the same bits
+    for n in (1, 5, 9, 2047, 2049, 16_384, 70_003, 6_000_011):
+        values, want = rand(n, dtype, n, 1.0), None
+        for start in range(8):
+            flat = torch.empty(n + 8, dtype=dtype, device=dev())
+            flat[start:start + n] = values
+            got = ops.grad_norm(ops.make_grad_list([flat[start:start + n]]), 1.0, KINDS[kind]).result.clone()
+            want = got if want is None else want
+            assert torch.equal(got, want), (n, start)
