@@ -1011,7 +1011,7 @@ def make_grad_list(grads, out=None, device=None) -> GradList:
         if b[0] < a[1]:
             raise ValueError(f"{a[2]} and {b[2]} overlap")
     device = torch.device("cuda", dev)
-    result = torch.zeros(16, dtype=torch.uint8, device=device)
+    result = torch.empty(16, dtype=torch.uint8, device=device)  # no fill: it would run on this stream, a call perhaps on another
     floats = result.view(torch.float32)
     return GradList(grads, out, table, dev, result, result.view(torch.float64)[:1], floats[2:3], floats[3:4],
                     torch.empty(load().moe_grad_workspace_bytes(len(grads)), dtype=torch.uint8, device=device))

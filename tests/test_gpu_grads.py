@@ -227,3 +227,14 @@ def test_the_sum_does_not_depend_on_where_gradients_lie(dtype, kind):
             got = ops.grad_norm(ops.make_grad_list([flat[start:start + n]]), 1.0, KINDS[kind]).result.clone()
             want = got if want is None else want
             assert torch.equal(got, want), (n, start)
+
+
+def test_a_new_list_on_another_stream():
+    # a list made while its own stream is busy, and a call at once on another
+    grads, side = [rand(100_000, torch.float32, 1), rand(333, torch.bfloat16, 2)], torch.cuda.Stream()
+    want = norm64(grads, "l2")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    gl = ops.grad_norm(ops.make_grad_list(grads), stream=side)
+    torch.cuda.synchronize()
+    assert abs(float(gl.norm) - want) <= 2 * U * want
