@@ -996,6 +996,8 @@ def make_grad_list(grads, out=None, device=None) -> GradList:
     if len(out) != len(grads):
         raise ValueError(f"{len(grads)} gradients, {len(out)} outputs")
     dev = grads[0].get_device() if grads else torch.device(device).index
+    if dev is None and torch.device(device).type == "cuda":
+        dev = torch.cuda.current_device()
     if dev is None or dev < 0:
         raise TypeError("device buffers must be CUDA (HIP) torch tensors")
     table, spans = (moe_grad * max(1, len(grads)))(), []

@@ -238,3 +238,8 @@ def test_a_new_list_on_another_stream():
     gl = ops.grad_norm(ops.make_grad_list(grads), stream=side)
     torch.cuda.synchronize()
     assert abs(float(gl.norm) - want) <= 2 * U * want
+
+
+def test_no_gradients_of_the_current_device():
+    gl = ops.grad_clip(ops.make_grad_list([], device="cuda"), 1.0)
+    assert gl.result.device == torch.device("cuda", torch.cuda.current_device()) and float(gl.norm) == 0.0 and float(gl.coef) == 1.0
