@@ -210,7 +210,7 @@ __device__ __forceinline__ moe_grad_result grad_result(const GradScalars &k, dou
     moe_grad_result r;
     r.sum = max_of ? s * scale : s * scale * scale;
     const double norm = max_of ? r.sum : sqrt(s) * scale, below = norm + (double)k.eps;
-    const double c = below == 0.0 ? 1.0 : (double)k.max_norm / below;
+    const double c = below == 0.0 ? 1.0 : __builtin_isinf(below) ? 0.0 : (double)k.max_norm / below;  // 0 for an infinite max_norm too
     r.norm = (float)norm;
     r.coef = (float)(c >= 1.0 ? 1.0 : c);  // NaN stays
     return r;

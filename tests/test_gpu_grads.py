@@ -243,3 +243,12 @@ def test_a_new_list_on_another_stream():
 def test_no_gradients_of_the_current_device():
     gl = ops.grad_clip(ops.make_grad_list([], device="cuda"), 1.0)
     assert gl.result.device == torch.device("cuda", torch.cuda.current_device()) and float(gl.norm) == 0.0 and float(gl.coef) == 1.0
+
+
+def test_an_infinite_gradient_without_a_bound():
+    for kind in KINDS:
+        t = rand(5000, torch.float32, 1)
+        t[77] = float("inf")
+        gl = ops.grad_clip(ops.make_grad_list([t]), float("inf"), KINDS[kind])
+        assert math.isinf(float(gl.norm)) and float(gl.coef) == 0.0
+        assert bool(t[77].isnan()) and not bool(t[:77].any()) and not bool(t[78:].any())
