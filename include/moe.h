@@ -734,13 +734,13 @@ enum {
  *   dW13 [2I][H], dW2 [H][I] out, each nullable, of dw_type: MOE_TYPE_FP32 or n->type.
  *        accumulate = 1 (fp32 only) adds to what they hold.  Zeros for rows = 0
  *   ws >= moe_gated_ffn_workspace_bytes(n, 1)
- * Outputs must not overlap inputs or each other (dX in the place of X or dOut is refused), and
- * calls that may run at once, captured graphs among them, need a workspace each.  Pointers
+ * Outputs must not overlap inputs or each other, but out may be X with the same stride; one that starts where such a buffer
+ * does is refused.  Calls that may run at once, captured graphs among them, need a workspace each.  Pointers
  * 16-byte aligned; what lies between rows (ldx, ldo > H) is neither read nor written.  A row's out, HU, A and dX
  * depend on that row alone.  Every sum is fp32, in an order that depends on the sizes
  * only: repeated calls give bitwise the same.  fp16 values past 65504 become infinite; the backward takes
- * an infinite h or u of fp16 for a number past 65504, so that slopes and values of 0 make 0 of it, and
- * du where h is +infinity, dh where u is infinite, are infinite otherwise.
+ * an infinite h or u of fp16 for a number past 65504: slopes and values of 0 make 0 of it, and du where h is
+ * +infinity, dh where u is infinite, are infinite otherwise.
  * The shared expert's gradient: HU and A are moe_layer_fwd_shared's HUs and As, whose padding rows
  * are not read.
  * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for H, I or a stride that is not a

@@ -294,6 +294,13 @@ int64_t ffn_ws_bytes(const moe_ffn_desc *n, bool bwd) {
     return ffn_skinny(n) ? 0 : FfnFwdPlan(n).ws_bytes();
 }
 
+// Whether no output starts where an input or another output does (NULL: not there).
+bool ffn_apart(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o)
+        if (*o && (std::find(ins.begin(), ins.end(), *o) != ins.end() || std::find(o + 1, outs.end(), *o) != outs.end())) return false;
+    return true;
+}
+
 template <class T, bool GLU>
 int launch_skinny(const SkinnyArgs &g, hipStream_t s, const char *name) {
     const int units = up_to(g.N, GLU ? 8 : 16);
@@ -559,6 +566,8 @@ int moe_gated_ffn_fwd(const moe_ffn_desc *n, const uint16_t *X, const uint16_t *
     if (!X || !W13 || !W2 || !A || !out || !all_aligned({X, W13, W2, HU, A, out, ws})) return MOE_EINVAL;
     const int64_t need = ffn_ws_bytes(n, false);
     if (need && !ws) return MOE_EINVAL;
+    // out may take the place of X, which its launch no longer reads
+    if (!ffn_apart({HU, A, out, need ? ws : nullptr}, {W13, W2}) || !ffn_apart({HU, A, need ? ws : nullptr}, {X})) return MOE_EINVAL;
     if ((int64_t)ws_bytes < need) return MOE_ENOSPC;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return n->type == MOE_TYPE_BF16 ? ffn_fwd<Bf16>(n, X, W13, W2, HU, A, out, ws, s) : ffn_fwd<Fp16>(n, X, W13, W2, HU, A, out, ws, s);
@@ -582,7 +591,7 @@ int moe_gated_ffn_bwd(const moe_ffn_desc *n, const uint16_t *dOut, const uint16_
     }
     if (!dOut || !X || !HU || !W13 || !W2 || !ws || !all_aligned({dOut, X, HU, A, W13, W2, dX, ws})) return MOE_EINVAL;
     if (!dX && !dW13 && !dW2) return MOE_EINVAL;
-    if (dX == dOut || dX == X) return MOE_EINVAL;  // what the weights' gradients read beside it
+    if (!ffn_apart({dX, dW13, dW2, ws}, {dOut, X, HU, A, W13, W2})) return MOE_EINVAL;  // one launch reads and writes them
     if ((int64_t)ws_bytes < ffn_ws_bytes(n, true)) return MOE_ENOSPC;
     const int f32 = dw_type == MOE_TYPE_FP32;
     return n->type == MOE_TYPE_BF16 ? ffn_bwd<Bf16>(n, dOut, X, HU, A, W13, W2, dX, dW13, dW2, f32, accumulate, ws, s)

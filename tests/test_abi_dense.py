@@ -177,3 +177,32 @@ def test_tensors_on_the_host():
         ops.moe_gated_ffn_fwd(n, x, w13, w2, None, x, x, None)
     with pytest.raises(TypeError):
         ops.moe_layer_norm_fwd(ops.make_layer_norm_desc(4, 64), x, None, None, x, None)
+
+
+def test_ffn_outputs_in_the_place_of_what_is_read():
+    # what a launch still reads beside the output, or writes besides: refused where both start alike
+    lib = ops.load()
+    names = ("X", "W13", "W2", "HU", "A", "out", "ws")
+
+    def fwd(n, **kw):
+        a = dict(zip(names, P)) | kw
+        return lib.moe_gated_ffn_fwd(ctypes.byref(n), *(a[k] for k in names), 1 << 40, None)
+
+    at = dict(zip(names, P))
+    for o, i in (("A", "X"), ("HU", "X"), ("A", "W13"), ("HU", "W13"), ("A", "W2"), ("HU", "W2"), ("HU", "A"), ("out", "A"), ("out", "W2"), ("out", "W13"),
+                 ("out", "HU")):
+        assert fwd(ffn(), **{o: at[i]}) == EINVAL, (o, i)
+    cut = ffn(rows=70, H=2048, I=8)  # parts in the workspace
+    for i in names[:-1]:
+        assert fwd(cut, ws=at[i]) == EINVAL, i
+    names2 = ("dOut", "X", "HU", "A", "W13", "W2", "dX", "dW13", "dW2", "ws")
+
+    def bwd(n, **kw):
+        a = dict(zip(names2, P)) | kw
+        return lib.moe_gated_ffn_bwd(ctypes.byref(n), *(a[k] for k in names2[:-1]), ops.MOE_TYPE_BF16, 0, a["ws"], 1 << 40, None)
+
+    at = dict(zip(names2, P))
+    for o in names2[6:]:
+        for i in names2:
+            if i != o:
+                assert bwd(ffn(), **{o: at[i]}) == EINVAL, (o, i)

@@ -413,3 +413,15 @@ def test_fp16_gradient_of_a_finite_forward(kind):
         ops.gated_ffn_bwd(c["n"], c["dOut"], c["X"], b.HU, A, c["W13"], c["W2"], g)
         for name, got, (ref, err) in zip(("dX", "dW13", "dW2"), (g.dX, g.dW13, g.dW2), backward64(c, b.HU.double().nan_to_num(neginf=-200.0), b.A, A is not None)):
             near(name, got, ref, err)
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_out_in_the_place_of_x(rows):
+    c = make(rows, 264, 136)
+    want, b, x = fwd(c), ops.alloc_gated_ffn(c["n"], dev()), c["X"].clone()
+    ops.moe_gated_ffn_fwd(c["n"], x, c["W13"], c["W2"], b.HU, b.A, x, b.ws)
+    assert torch.equal(x, want.out) and torch.equal(b.A, want.A)
+    g = ops.alloc_gated_ffn_bwd(c["n"], dev(), dw_dtype=torch.bfloat16)
+    for dX, dW13, dW2 in ((c["X"], None, None), (c["dOut"], None, None), (None, c["W13"], None), (None, None, c["W2"]), (None, c["X"].new_empty(0), None)):
+        with pytest.raises((ops.MoeError, ValueError)):
+            ops.moe_gated_ffn_bwd(c["n"], c["dOut"], c["X"], b.HU, b.A, c["W13"], c["W2"], dX, dW13, dW2, g.ws)
