@@ -27,17 +27,18 @@ def build(verbose: bool = False) -> str:
         objs = [os.path.join(tmpdir, os.path.basename(s) + ".o") for s in SRCS]
         procs = [subprocess.Popen([hipcc, *HIPCC_FLAGS, "-c", "-o", o, s], stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
                  for s, o in zip(SRCS, objs)]
-        for p in procs:
-            _finish(p, verbose)
+        texts = [p.communicate()[1] for p in procs]  # all of them end before the first failure is raised
+        for p, text in zip(procs, texts):
+            _check(p, text, verbose)
         tmp = OUT + ".tmp"
-        _finish(subprocess.Popen([hipcc, "--offload-arch=gfx950", "-shared", "-o", tmp, *objs], stdout=subprocess.PIPE,
-                                 stderr=subprocess.PIPE, text=True), verbose)
+        link = subprocess.Popen([hipcc, "--offload-arch=gfx950", "-shared", "-o", tmp, *objs], stdout=subprocess.PIPE,
+                                stderr=subprocess.PIPE, text=True)
+        _check(link, link.communicate()[1], verbose)
     os.replace(tmp, OUT)
     return OUT
 
 
-def _finish(p: subprocess.Popen, verbose: bool) -> None:
-    _, text = p.communicate()
+def _check(p: subprocess.Popen, text: str, verbose: bool) -> None:
     err = "\n".join(l for l in text.splitlines() if "packed-fp32-ops" not in l)
     if p.returncode != 0:
         raise RuntimeError(f"hipcc failed ({p.returncode}):\n{err}")

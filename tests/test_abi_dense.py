@@ -206,3 +206,18 @@ def test_ffn_outputs_in_the_place_of_what_is_read():
         for i in names2:
             if i != o:
                 assert bwd(ffn(), **{o: at[i]}) == EINVAL, (o, i)
+
+
+def test_a_failed_build_leaves_no_compiler_behind(tmp_path, monkeypatch):
+    from routing_schedule_expert_amd import build
+
+    # a compiler that refuses the first source at once and takes a while over the other
+    done, hipcc = tmp_path / "done", tmp_path / "hipcc"
+    hipcc.write_text(f"#!/bin/sh\ncase \"$*\" in *{build.SRCS[0]}*) echo refused >&2; exit 1;; esac\nsleep 1\necho done > {done}\n")
+    hipcc.chmod(0o755)
+    monkeypatch.setenv("HIPCC", str(hipcc))
+    monkeypatch.setattr(build, "OUT", str(tmp_path / "libmoe.so"))
+    with pytest.raises(RuntimeError, match="refused"):
+        build.build()
+    assert done.exists()
+    assert not (tmp_path / "libmoe.so").exists()
