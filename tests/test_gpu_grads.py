@@ -252,3 +252,11 @@ def test_an_infinite_gradient_without_a_bound():
         gl = ops.grad_clip(ops.make_grad_list([t]), float("inf"), KINDS[kind])
         assert math.isinf(float(gl.norm)) and float(gl.coef) == 0.0
         assert bool(t[77].isnan()) and not bool(t[:77].any()) and not bool(t[78:].any())
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("inside", [True, False])
+def test_more_slots_than_one_launch(kind, inside):
+    # 300 tensors of 16 to 20 pieces: two launches of 2048 and hundreds of slots, which a launch of its own adds
+    grads = [rand(260_001 + 211 * i, DT[i % 3], i) for i in range(300)]
+    check(grads, kind, 0.3, out=None if inside else [torch.empty_like(t) for t in grads])

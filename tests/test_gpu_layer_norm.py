@@ -281,3 +281,12 @@ def test_tensors_that_do_not_fit():
     with pytest.raises(ops.MoeError):
         k = ops.alloc_layer_norm_bwd(c["n"], dev())
         ops.moe_layer_norm_bwd(c["n"], c["x"], c["g"], b.stats, c["dy"], None, k.dx, k.both[0], None, k.ws)
+
+
+@pytest.mark.parametrize("H", [9000, 20000, 20001, 32768])
+def test_more_rows_than_workgroups(H):
+    # two and four chunks a thread, every workgroup with rows after its first
+    for tx, ty in ((B, B), (F32, F32)):
+        c = make(1200, H, tx, ty)
+        check_fwd(c, c["g"], c["b"])
+        check_bwd(c, c["g"], True)
