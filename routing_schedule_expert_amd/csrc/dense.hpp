@@ -20,7 +20,7 @@
 // before) is multiplied, across the step's one barrier too, and the loads that fill the
 // ring are spread over the MFMAs, one to four of them.
 //
-// Measured: 16,384 rows of H = 7168, I = 2048 forward 1,133 us, 1.27 PFLOP/s; the large tile's
+// Measured: 16,384 rows of H = 7168, I = 2048 forward 1,107 to 1,146 us, 1.30 to 1.26 PFLOP/s; the large tile's
 // step takes 2,470 cycles of the 2,048 of its MFMAs, and 2,320 with no memory behind its
 // loads.  The 128 x 128 tile reads its operands from LDS twice as often for its MFMAs: 900
 // cycles a step of 512, bound by LDS.

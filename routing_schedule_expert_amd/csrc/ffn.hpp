@@ -13,9 +13,9 @@
 // does the epilogue.
 //
 // Bound by the matrix cores from some hundred rows on (6 I H flop a row forward, 12 backward).
-// H = 7168, I = 2048: 16,384 rows forward 1,133 us (a library's product alone reaches 1.25
-// PFLOP/s here, this 1.27), 8,192 rows backward 1,121 (activations 207, the three gradients in
-// one launch 890).  The backward's products have their operands as they lie, which costs
+// H = 7168, I = 2048: 16,384 rows forward 722 + 385 us (1.30 PFLOP/s; a library's product of 8192^3
+// reaches 1.25 here), 8,192 rows backward 205 for the activations and 917 for the three gradients in
+// one launch, and up to 4% more where the clock is lower.  The backward's products have their operands as they lie, which costs
 // transposing LDS reads and no copy.
 #pragma once
 

@@ -2,8 +2,8 @@
 //
 //   norm = |s| sqrt(sum of squares)  or  |s| max,   c = min(1, max_norm / (norm + eps)),   out = (s c) g
 //
-// Two passes over the gradients, bound by memory: 480 fp32 tensors of 2.5 GB take 1,374 us, the sums
-// 433 (5.7 TB/s), the scaling 920 (5.4 TB/s read and written).  Squares are summed in 64 bits (no
+// Two passes over the gradients, bound by memory: 480 fp32 tensors of 2.5 GB take 1,360 us, the sums
+// 432 (5.7 TB/s), the scaling 922 (5.4 TB/s read and written).  Squares are summed in 64 bits (no
 // square of an fp32 number overflows or vanishes there), each workgroup's sum in a slot
 // of its own, and the second pass's workgroups each add the slots in one fixed order,
 // so no launch stands between the passes (past 2048 slots one workgroup does it: 4,096 slots, read

@@ -17,11 +17,11 @@
 // rows as they come.  Past 8192 elements the column sums have no registers: a second
 // reading makes them.
 //
-// Measured: 57,344 rows of 7168 in bf16 forward 331 us (4.97 TB/s), 16,384 of 7168 backward
-// 140 + 5 (5.0 TB/s); 8,192 of 12,288 forward 65 (190 without the loads ahead and the gains in
-// registers), backward 86 + 45 (213 + 37); 4,096 of 32,768 forward 232 (2.3 TB/s, the gains'
-// L2 traffic twice the row's).  Rows without 16-byte alignment: 16,384 of 7,171
-// forward 106, of 7168 79.
+// Measured: 57,344 rows of 7168 in bf16 forward 329 us (5.0 TB/s), 16,384 of 7168 backward
+// 132 and 5 for the sums of the column sums (5.2 TB/s); 8,192 of 12,288 forward 67 (190 without the loads ahead and
+// the gains in registers), backward 95, 93 for its column sums and 5; 4,096 of 32,768 forward 237 (2.3 TB/s, the gains'
+// L2 traffic twice the row's), backward 265, 116 and 7.  Rows without 16-byte alignment: 16,384 of 7,171
+// forward 108, of 7168 83.
 //
 // Any row length and stride: where H or a stride is not a multiple of 8, or a pointer
 // not of 16 bytes, the last 8 columns of a row start at H - 8 and overlap those before
