@@ -740,7 +740,7 @@ enum {
  * depend on that row alone.  Every sum is fp32, in an order that depends on the sizes
  * only: repeated calls give bitwise the same.  fp16 values past 65504 become infinite; the backward takes
  * an infinite h or u of fp16 for a number past 65504: slopes and values of 0 make 0 of it, and du where h is
- * +infinity, dh where u is infinite, are infinite otherwise.
+ * +infinity, dh where u is infinite and an a computed again where either is are infinite otherwise.
  * The shared expert's gradient: HU and A are moe_layer_fwd_shared's HUs and As, whose padding rows
  * are not read.
  * Errors: MOE_EINVAL, MOE_ENOSPC, MOE_EUNSUPPORTED for H, I or a stride that is not a

@@ -425,3 +425,22 @@ def test_out_in_the_place_of_x(rows):
     for dX, dW13, dW2 in ((c["X"], None, None), (c["dOut"], None, None), (None, c["W13"], None), (None, None, c["W2"]), (None, c["X"].new_empty(0), None)):
         with pytest.raises((ops.MoeError, ValueError)):
             ops.moe_gated_ffn_bwd(c["n"], c["dOut"], c["X"], b.HU, b.A, c["W13"], c["W2"], dX, dW13, dW2, g.ws)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_fp16_infinite_u_where_nothing_arrives(sign):
+    # a column of W2 without weights: nothing arrives at dA, but a, made again from an infinite u, is infinite
+    I = 40
+    c = make(80, 72, I, "silu", torch.float16)
+    c["W2"][:, 10] = 0.0
+    HU, A = kept(c)
+    HU[7, 10], HU[7, I + 10] = 1.0, sign * float("inf")
+    b = ops.alloc_gated_ffn_bwd(c["n"], dev())
+    ops.gated_ffn_bwd(c["n"], c["dOut"], c["X"], HU, None, c["W13"], c["W2"], b)
+    assert torch.equal(b.dW2[:, 10], torch.where(c["dOut"][7] > 0, sign, -sign) * float("inf"))
+    ref = HU.double().nan_to_num(posinf=200.0, neginf=-200.0)
+    (dX, eX), (dW13, e13), (dW2, e2) = backward64(c, ref, A, False)
+    rest = torch.arange(I, device=dev()) != 10
+    near("dX", b.dX, dX, eX)
+    near("dW13", b.dW13, dW13, e13)
+    near("dW2", b.dW2[:, rest], dW2[:, rest], e2[:, rest])
